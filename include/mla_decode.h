@@ -83,7 +83,9 @@ typedef enum mla_kv_dtype {
 #define MLA_DEVFLAG_CTX_RANGE 0x2  /* seq_lens[b] < 0 or beyond the plan's max_ctx
                                       (clamped to [0, max_ctx] on the device) */
 #define MLA_DEVFLAG_TIMEOUT 0x4    /* a bounded barrier wait gave up         */
-#define MLA_DEVFLAG_Q_RANGE 0x8    /* fp8 path: |q| beyond the fp16 range    */
+#define MLA_DEVFLAG_Q_RANGE 0x8    /* fp8 or shared-prefix path: |q| beyond the fp16 range */
+#define MLA_DEVFLAG_KV_RANGE 0x10  /* shared prefix: a cache value beyond the fp16
+                                      range, infinite or NaN */
 
 #define MLA_DECODE_PLAN_VERSION 1
 #define MLA_D_QK 576 /* query/key row width: 512 latent + 64 rope */
@@ -428,6 +430,95 @@ int mla_decode_fwd_noalloc(const mla_decode_plan_t* plan, const void* q, const v
                            int64_t num_pages, const float* kv_scale, const int32_t* block_table,
                            int64_t bt_stride, const int32_t* seq_lens, float softmax_scale,
                            void* out, float* lse, void* stream);
+
+/*
+ * Decode for a batch that shares a prefix.  The first prefix_len tokens of
+ * every sequence are the same cached rows (a system prompt, a document that
+ * many requests ask about).  Their scores against the query rows of the whole
+ * batch are one product, so each shared row is read once for 128 query rows
+ * instead of once per sequence; every sequence's own keys follow, and the two
+ * parts are merged into one softmax.  The result is that of mla_decode_fwd +
+ * mla_decode_combine on the same arguments: for sequence b, token i, head h
+ *
+ *   n   = causal ? ctx_b - Sq + i + 1 : ctx_b        (clamped to [0, ctx_b])
+ *   key j < prefix_len is row prefix_table[j / page_size][j % page_size],
+ *   key j >= prefix_len is row block_table[b][j / page_size][j % page_size],
+ *   out, lse over the keys j < n as above.
+ *
+ * A sequence may be shorter than the prefix (it sees its first ctx_b keys) or
+ * empty (out = 0, lse = -inf).  prefix_len need not be a multiple of
+ * page_size: block_table[b]'s page at prefix_len / page_size is then the
+ * sequence's own copy of the page, of which only the slots from prefix_len %
+ * page_size on are read.
+ *
+ * The shared rows and the query rows are staged in f16 (exact for bf16 and
+ * e4m3 values of magnitude 2^-14 to 65504, to 2^-25 below that); larger or
+ * non-finite values set MLA_DEVFLAG_KV_RANGE / MLA_DEVFLAG_Q_RANGE, and the
+ * rows that use them are undefined.  A non-finite shared key also spoils the
+ * rows of sequences too short to see it.
+ */
+typedef struct mla_decode_prefix_plan_t {
+  int32_t version;       /* MLA_DECODE_PREFIX_PLAN_VERSION */
+  int32_t batch, num_heads, sq, page_size, kv_dtype, causal; /* as mla_decode_plan_t */
+  int32_t rows;          /* H * Sq: query rows per sequence */
+  int32_t total_rows;    /* B * H * Sq */
+  int32_t prefix_len;    /* shared keys */
+  int32_t max_ctx;       /* longest context the plan covers, the prefix included */
+  int32_t num_sms;       /* SM count the partition was balanced for */
+  int32_t row_blocks;    /* ceil(total_rows / 128) */
+  int32_t prefix_tiles;  /* ceil(prefix_len / 256) */
+  int32_t pairs;         /* CTA pairs that share row_blocks * prefix_tiles tiles */
+  int32_t prefix_slots;  /* most partials a row gets from the shared keys */
+  int32_t key_tile;      /* of the own keys' decode, as mla_decode_plan_t */
+  int32_t own_chunk;     /* keys per split of a sequence's own keys */
+  int32_t own_splits;    /* splits of the longest sequence's own keys (0: none has any) */
+  int32_t wait_limit_us; /* as mla_decode_plan_t: 0 = 2 s; the one field a caller may set */
+  int64_t ws_status_offset;     /* int32 status word */
+  int64_t ws_keys_offset;       /* f16 [prefix_len, 576] */
+  int64_t ws_q_offset;          /* f16 [total_rows, 576] */
+  int64_t ws_prefix_o_offset;   /* fp32 [prefix_slots, total_rows, 512] */
+  int64_t ws_prefix_lse_offset; /* fp32 [prefix_slots, total_rows] */
+  int64_t ws_own_o_offset;      /* fp32 [B, own_splits, rows, 512] */
+  int64_t ws_own_lse_offset;    /* fp32 [B, own_splits, rows] */
+  int64_t workspace_bytes;
+} mla_decode_prefix_plan_t;
+
+#define MLA_DECODE_PREFIX_PLAN_VERSION 1
+#define MLA_PREFIX_MAX_ROWS (1 << 24) /* B * H * Sq */
+#define MLA_PREFIX_MAX_LEN (1 << 22)  /* shared keys */
+
+/* The partition of both parts.  Arguments as mla_decode_plan, with the length
+ * of the shared prefix (0 .. MLA_PREFIX_MAX_LEN; 0: a plain decode); seq_lens
+ * count the prefix.  The plan stays valid for later calls whose contexts are
+ * all <= plan->max_ctx, with the same prefix length.  Pure host code.
+ * Returns MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (more than
+ * MLA_PREFIX_MAX_ROWS rows) or MLA_ERR_CUDA. */
+int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batch, int32_t prefix_len,
+                           int32_t num_heads, int32_t sq, int32_t page_size, int32_t kv_dtype,
+                           int32_t causal, int32_t num_sms, mla_decode_prefix_plan_t* plan);
+
+/* The decode, both parts and the merge: out and lse are final when the queued
+ * work is done.  Arguments as mla_decode_fwd, and
+ *   prefix_table  device int32 [ceil(prefix_len / page_size)]: the shared
+ *                 keys' pages (a row of block_table serves, if that sequence
+ *                 holds the whole prefix).  NULL allowed when prefix_len is 0.
+ *   block_table   entries before prefix_len / page_size are never read.  NULL
+ *                 allowed when plan->own_splits is 0.
+ *   softmax_scale >= 0
+ * Page ids and contexts out of range are clamped and flagged as in
+ * mla_decode_fwd.  Resets the status word first.  The workspace (256-byte
+ * aligned, >= plan->workspace_bytes) holds nothing between calls; calls that
+ * may overlap need one each. */
+int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const void* q,
+                          const void* kv_cache, int64_t num_pages, const float* kv_scale,
+                          const int32_t* prefix_table, const int32_t* block_table,
+                          int64_t bt_stride, const int32_t* seq_lens, float softmax_scale,
+                          void* out, float* lse, void* workspace, size_t workspace_bytes,
+                          void* stream);
+
+/* mla_decode_check for the last prefix call that used `workspace`. */
+int mla_decode_prefix_check(const mla_decode_prefix_plan_t* plan, const void* workspace,
+                            void* stream, int32_t* host_status);
 
 /* Static text for a status code. */
 const char* mla_status_string(int status);

@@ -11,7 +11,9 @@ Names follow the C ABI: ``plan`` -> ``mla_decode_plan``, ``fwd`` ->
 ``mla_decode_check``, ``epilogue`` -> ``mla_decode_epilogue``, ``step`` ->
 ``mla_decode_step``; the device-planned path: ``dplan_info``, ``plan_device``,
 ``fwd_dplan`` and ``combine_dplan``; ``gather_kv_b_proj`` ->
-``mla_gather_kv_b_proj``.  ``decode`` is plan + fwd + combine with freshly
+``mla_gather_kv_b_proj``; for a batch that shares a prefix: ``prefix_plan``,
+``prefix_fwd`` and ``prefix_check`` -> ``mla_decode_prefix_*``, and
+``decode_prefix``.  ``decode`` is plan + fwd + combine with freshly
 allocated outputs and workspace, for convenience.
 """
 from __future__ import annotations
@@ -40,12 +42,14 @@ DEVFLAG_BAD_PAGE = 0x1
 DEVFLAG_CTX_RANGE = 0x2
 DEVFLAG_TIMEOUT = 0x4
 DEVFLAG_Q_RANGE = 0x8
+DEVFLAG_KV_RANGE = 0x10
 
 # Every symbol include/mla_decode.h declares.
 EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_fwd", "mla_decode_combine",
                     "mla_decode_check", "mla_decode_dplan_info", "mla_decode_plan_device",
                     "mla_decode_fwd_dplan", "mla_decode_combine_dplan", "mla_decode_epilogue",
                     "mla_decode_step", "mla_gather_kv_b_proj", "mla_decode_fwd_noalloc",
+                    "mla_decode_prefix_plan", "mla_decode_prefix_fwd", "mla_decode_prefix_check",
                     "mla_status_string", "mla_decode_version")
 
 
@@ -71,6 +75,20 @@ class DPlan(ctypes.Structure):
         (n, ctypes.c_int64) for n in (
             "ws_units_offset", "ws_seq_offset", "ws_count_offset", "ws_partial_o_offset",
             "ws_partial_lse_offset", "ws_status_offset", "workspace_bytes")]
+
+    def as_dict(self):
+        return {n: getattr(self, n) for n, _ in self._fields_}
+
+
+class PrefixPlan(ctypes.Structure):
+    """Mirror of ``mla_decode_prefix_plan_t`` (plain old data)."""
+    _fields_ = [(n, ctypes.c_int32) for n in (
+        "version", "batch", "num_heads", "sq", "page_size", "kv_dtype", "causal", "rows",
+        "total_rows", "prefix_len", "max_ctx", "num_sms", "row_blocks", "prefix_tiles", "pairs",
+        "prefix_slots", "key_tile", "own_chunk", "own_splits", "wait_limit_us")] + [
+        (n, ctypes.c_int64) for n in (
+            "ws_status_offset", "ws_keys_offset", "ws_q_offset", "ws_prefix_o_offset",
+            "ws_prefix_lse_offset", "ws_own_o_offset", "ws_own_lse_offset", "workspace_bytes")]
 
     def as_dict(self):
         return {n: getattr(self, n) for n, _ in self._fields_}
@@ -129,6 +147,14 @@ def lib():
     L.mla_decode_step.argtypes = [P, vp, vp, vp, vp, vp, i32, vp, vp, i64, vp, vp, i64, vp, f32,
                                   vp, vp, vp, ctypes.c_size_t, vp]
     L.mla_decode_step.restype = ctypes.c_int
+    X = ctypes.POINTER(PrefixPlan)
+    L.mla_decode_prefix_plan.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, i32, X]
+    L.mla_decode_prefix_plan.restype = ctypes.c_int
+    L.mla_decode_prefix_fwd.argtypes = [X, vp, vp, i64, vp, vp, vp, i64, vp, f32, vp, vp, vp,
+                                        ctypes.c_size_t, vp]
+    L.mla_decode_prefix_fwd.restype = ctypes.c_int
+    L.mla_decode_prefix_check.argtypes = [X, vp, vp, ctypes.POINTER(i32)]
+    L.mla_decode_prefix_check.restype = ctypes.c_int
     L.mla_decode_check.argtypes = [P, vp, vp, ctypes.POINTER(i32)]
     L.mla_decode_check.restype = ctypes.c_int
     L.mla_status_string.argtypes = [ctypes.c_int]
@@ -295,7 +321,65 @@ def check(p: Plan, workspace, stream=None) -> int:
     return int(v.value)
 
 
-def workspace_for(p: Plan, device="cuda"):
+def prefix_plan(seq_lens_host, prefix_len: int, num_heads: int, sq: int, page_size: int,
+                kv_dtype: int = KV_BF16, causal: bool = False, num_sms: int = 0) -> PrefixPlan:
+    """``mla_decode_prefix_plan``: lengths as ``plan``, the shared prefix counted in them."""
+    import numpy as np
+    lens = np.ascontiguousarray(np.asarray(seq_lens_host, dtype=np.int32).reshape(-1))
+    p = PrefixPlan()
+    st = lib().mla_decode_prefix_plan(lens.ctypes.data, int(lens.size), int(prefix_len),
+                                      int(num_heads), int(sq), int(page_size), int(kv_dtype),
+                                      int(bool(causal)), int(num_sms), ctypes.byref(p))
+    _raise(st, "mla_decode_prefix_plan")
+    return p
+
+
+def prefix_fwd(p: PrefixPlan, q, kv_cache, kv_scale, prefix_table, block_table, seq_lens,
+               softmax_scale: float, out, lse, workspace, stream=None) -> None:
+    """``mla_decode_prefix_fwd``: the shared keys for all rows, each sequence's own keys, merged."""
+    st = lib().mla_decode_prefix_fwd(
+        ctypes.byref(p), _ptr(q), _ptr(kv_cache), int(kv_cache.shape[0]), _ptr(kv_scale),
+        _ptr(prefix_table), _ptr(block_table),
+        0 if block_table is None else int(block_table.stride(0)), _ptr(seq_lens),
+        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), _ws_bytes(workspace),
+        _stream(stream))
+    _raise(st, "mla_decode_prefix_fwd")
+
+
+def prefix_check(p: PrefixPlan, workspace, stream=None) -> int:
+    """``mla_decode_prefix_check``: device status bits (blocks until the stream drains)."""
+    v = ctypes.c_int32(0)
+    st = lib().mla_decode_prefix_check(ctypes.byref(p), _ptr(workspace), _stream(stream),
+                                       ctypes.byref(v))
+    if st not in (OK, ERR_DEVICE_CHECK, ERR_TIMEOUT):
+        _raise(st, "mla_decode_prefix_check")
+    return int(v.value)
+
+
+def decode_prefix(q, kv_cache, prefix_table, block_table, seq_lens, prefix_len: int,
+                  seq_lens_host=None, kv_scale=None, softmax_scale: float | None = None,
+                  causal: bool = False, p: PrefixPlan | None = None, workspace=None, stream=None):
+    """prefix_plan + prefix_fwd; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H])."""
+    import torch
+    B, Sq, H, D = q.shape
+    assert D == D_QK
+    kv_dtype = KV_FP8_E4M3 if kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn) else KV_BF16
+    if softmax_scale is None:
+        softmax_scale = 1.0 / math.sqrt(192.0)
+    if p is None:
+        host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
+        p = prefix_plan(host, prefix_len, H, Sq, int(kv_cache.shape[1]), kv_dtype, causal)
+    if workspace is None:
+        workspace = workspace_for(p, q.device)
+    out = torch.empty((B, Sq, H, D_V), dtype=torch.bfloat16, device=q.device)
+    lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
+    prefix_fwd(p, q, kv_cache, kv_scale, prefix_table, block_table, seq_lens, softmax_scale, out,
+               lse, workspace, stream)
+    return out, lse
+
+
+def workspace_for(p, device="cuda"):
+    """A workspace of the size that a plan (``Plan``, ``DPlan`` or ``PrefixPlan``) names."""
     import torch
     return torch.empty(max(int(p.workspace_bytes), 256), dtype=torch.uint8, device=device)
 

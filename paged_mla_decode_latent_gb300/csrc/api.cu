@@ -99,6 +99,8 @@ int fwd_impl(const mla_decode_plan_t* plan, const void* q, const void* kv_cache,
   p.num_splits = plan->num_splits;
   p.max_ctx = plan->max_ctx;
   p.row_blocks = plan->row_blocks;
+  p.key_begin = 0;
+  p.partials = 0;
 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (reset_status && cudaMemsetAsync(p.status, 0, sizeof(int32_t), s) != cudaSuccess)

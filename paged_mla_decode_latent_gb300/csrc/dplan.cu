@@ -337,6 +337,8 @@ extern "C" int mla_decode_fwd_dplan(const mla_decode_dplan_t* dplan, const void*
   p.chunk_len = 0;
   p.num_splits = 1;
   p.max_ctx = dplan->ctx_capacity;
+  p.key_begin = 0;
+  p.partials = 0;
   p.row_blocks = dplan->row_blocks;
   p.key_tile = dplan->key_tile;
   if (mla_launch_fwd(p, stream) != 0) return MLA_ERR_CUDA;

@@ -319,9 +319,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
       if (threadIdx.x == 0 && rank == 0 && split == 0) atomicOr(p.status, MLA_DEVFLAG_CTX_RANGE);
       ctx = ctx < 0 ? 0 : p.max_ctx;
     }
-    k0 = split * p.chunk_len;
+    k0 = p.key_begin + split * p.chunk_len;
     k1 = min(k0 + p.chunk_len, ctx);
-    single = p.num_splits == 1;
+    single = p.num_splits == 1 && !p.partials;
     part = (size_t)b * p.num_splits + split;
   }
   const int n_tiles = k1 > k0 ? (k1 - k0 + T - 1) / T : 0;

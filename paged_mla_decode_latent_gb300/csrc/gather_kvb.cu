@@ -402,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-namespace {
+namespace mla {
 
-// The driver's tensor-map encoder, looked up once through the runtime (no
-// link-time dependency on the driver library).
+// No link-time dependency on the driver library: the entry point is looked up
+// through the runtime.
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::once_flag once;
   static void* fn = nullptr;
@@ -419,7 +419,21 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
 }
 
-}  // namespace
+bool tensor_map_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows,
+                     int cols, int box_rows) {
+  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
+  if (encode == nullptr) return false;
+  const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t gstride[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  const cuuint32_t estride[2] = {1, 1};
+  return encode(map, type, 2, const_cast<void*>(base), gdim, gstride, box, estride,
+                CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace mla
 
 extern "C" int mla_gather_kv_b_proj(const void* kv_cache, int64_t num_pages, int32_t page_size,
                                     int32_t kv_dtype, const float* kv_scale,
@@ -487,16 +501,9 @@ extern "C" int mla_gather_kv_b_proj(const void* kv_cache, int64_t num_pages, int
   // The weights [H, 256, 512] as a 2-D tensor of H * 256 rows of 512 bf16,
   // read in boxes of 128 rows x 64 dims with the 128-byte swizzle of the
   // K-major operand.
-  const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (encode == nullptr) return MLA_ERR_CUDA;
   CUtensorMap wmap;
-  const cuuint64_t gdim[2] = {(cuuint64_t)kLatent, (cuuint64_t)num_heads * 256};
-  const cuuint64_t gstride[1] = {(cuuint64_t)kLatent * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)kUnitN};
-  const cuuint32_t estride[2] = {1, 1};
-  if (encode(&wmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(w_kv_b), gdim, gstride,
-             box, estride, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+  if (!mla::tensor_map_rows(&wmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, w_kv_b,
+                            (int64_t)num_heads * 256, kLatent, kUnitN))
     return MLA_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((max_ctx + kTok - 1) / kTok, (num_heads + group - 1) / group, batch);

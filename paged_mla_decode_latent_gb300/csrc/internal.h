@@ -2,6 +2,8 @@
 // translation units (not part of the public ABI).
 #pragma once
 
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -45,6 +47,10 @@ struct FwdParams {
   int key_tile;              // 64: the 128-row kernel; 128: the few-row kernel
   int batch, heads, sq, rows, page_size, kv_dtype, causal;
   int chunk_len, num_splits, max_ctx, row_blocks;
+  // Host-planned launches: the keys start at key_begin of every sequence (the
+  // shared prefix before it is another launch's), and partials != 0 writes
+  // partials even where there is one split (something else is merged in).
+  int key_begin, partials;
 };
 
 // Raises a kernel's dynamic shared-memory limit to `bytes` on device `dev`,
@@ -61,7 +67,45 @@ struct CombineParams {
   int batch, rows, num_splits;
 };
 
+// ---------------------------------------------------------- shared prefix ---
+
+constexpr int kPrefixTile = 256;  // shared keys per tile
+
+// The tiles of all row blocks, row block by row block, dealt to the CTA pairs
+// in equal contiguous shares: pair i takes [share(i), share(i + 1)).
+__host__ __device__ inline int64_t prefix_share(int64_t total, int pairs, int i) {
+  return total * i / pairs;
+}
+// The pair whose share holds tile x.
+__host__ __device__ inline int prefix_pair_of(int64_t total, int pairs, int64_t x) {
+  return (int)(((x + 1) * pairs - 1) / total);
+}
+
+// The shared-prefix pass: all rows of the batch against the shared keys.
+struct PrefixParams {
+  const float* kv_scale;    // device fp32[1], or nullptr (bf16 cache)
+  const int32_t* seq_lens;  // [B]
+  float* part_o;            // fp32 [slots, rows, 512]
+  float* part_lse;          // fp32 [slots, rows]
+  int32_t* status;
+  uint64_t wait_ns;
+  int64_t total_tiles;      // row blocks * tiles
+  float softmax_scale;
+  int rows, rows_per_seq, heads, sq, causal;
+  int prefix_len, max_ctx, tiles, pairs;
+};
+
+// The driver's tensor-map encoder, looked up once (nullptr if the driver has
+// none), and a 2-D 16-bit map of `rows` rows of `cols` elements read in boxes
+// of box_rows x 64 with the 128-byte swizzle.  False on failure.
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+bool tensor_map_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows,
+                     int cols, int box_rows);
+
 }  // namespace mla
+
+int mla_launch_prefix_sm103(const mla::PrefixParams& p, const CUtensorMap& kmap,
+                            const CUtensorMap& qmap, void* stream);
 
 // The few-row kernel (128-key tiles) takes problems of at most this many
 // score rows per sequence: 64 with a bf16 cache, 16 with fp8.

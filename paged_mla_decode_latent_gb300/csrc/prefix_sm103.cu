@@ -1,0 +1,506 @@
+// prefix_sm103.cu -- decode attention over the keys that every sequence of a
+// batch shares, for the query rows of the whole batch at once.
+//
+// The batch's B * Sq * H query rows are one [rows, 576] matrix and the shared
+// keys one [P, 576] matrix, so the scores are a plain product: a key is loaded
+// once per 128 rows instead of once per sequence.  Row r sees the first
+// min(P, n_r) keys, n_r its own causal or ragged limit:
+//
+//   z_j = c <q_r, k_j>,  j < min(P, n_r);   lse = ln sum_j e^z_j
+//   o   = sum_j e^(z_j - lse) k_j[0:512]
+//
+// and (o, lse) go to the workspace as one partial of the row, merged with the
+// partials of the sequence's own keys by the combine.
+//
+// Both matrices come staged: contiguous f16 rows of 576 (the staging kernel
+// walks the block table and converts the cache once, instead of once per row
+// block).  f16 keeps every bf16 and e4m3 value of ordinary size exactly, and
+// gives the weights 11 significant bits, so no second pass for heavy keys is
+// needed; values beyond 65504 are flagged by the staging kernel.
+//
+// Split over a CTA pair.  An fp32 accumulator of 128 rows x 512 value dims
+// fills the TMEM of one SM, so a pair shares the 128 rows: `cta_group::2` MMAs
+// with M = 128 give each CTA 64 rows and put the two halves of N on the two
+// halves of its TMEM lanes.  64 rows x 512 dims are then 256 columns, a
+// 256-key score tile 128 columns, and two score buffers fit beside O.  Nothing
+// is exchanged between the CTAs except operands the MMA itself reads.  At N =
+// 256 such an MMA runs at the full rate (64 cycles measured; N = 128: 50).
+//
+// Every operand streams through one ring of 16 KB slabs, each worth four MMAs
+// (256 cycles): per 256-key tile and CTA 9 score slabs [128 keys x 64 dims]
+// and 8 value slabs [64 keys x 128 dims].  The values are loaded again instead
+// of kept from the score slabs: a slab's offset must mean the same operand in
+// both CTAs, and for scores the pair splits the keys, for values the dims.
+//
+// Warps: 0-7 softmax (warp w: TMEM lane quarter w % 4, score columns 64 (w /
+// 4) .. + 63), 8 loads, 9 (even CTA) issues the MMAs: scores of tile t + 1,
+// then values of tile t, so the softmax of a tile has the length of both in
+// which to finish.
+//
+// Work: tiles of all row blocks laid end to end are dealt to the pairs in
+// equal contiguous shares; a pair walks its one to three segments (row block,
+// tile range) in one launch.
+//
+// Every wait is bounded; one that runs out sets MLA_DEVFLAG_TIMEOUT, after
+// which the CTA's loops run to their end without waiting or issuing.
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/mla_decode.h"
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace {
+
+constexpr int T = mla::kPrefixTile;  // 256 keys per tile
+constexpr int kSlots = 7;            // ring slabs
+constexpr int SLAB = 16384;
+constexpr int QSLAB = 64 * 128;      // 64 rows x 64 dims
+constexpr int PSLAB = 64 * 128;      // 64 rows x 64 keys
+constexpr int OFF_Q = 0;                          // 9 slabs, 72 KB
+constexpr int OFF_P = OFF_Q + 9 * QSLAB;          // 4 slabs, 32 KB
+constexpr int OFF_RING = OFF_P + 4 * PSLAB;       // 7 slabs, 112 KB
+constexpr int OFF_X = OFF_RING + kSlots * SLAB;   // row maxima / sums: [2][4][64] floats
+constexpr int OFF_BAR = OFF_X + 2 * 4 * 64 * 4;
+constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
+static_assert(SMEM_BYTES <= 232448, "smem");
+
+constexpr int kSoftmaxWarps = 8;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kThreads = 32 * 10;
+
+constexpr uint32_t TM_O = 0;    // 2 x 128 columns: dims 128 j .. of each value half
+constexpr uint32_t TM_S = 256;  // two 128-column score buffers
+constexpr uint32_t TM_COLS = 512;
+
+// Weights are 2^(z - m + kHead) in f16: kHead leaves the weights of rows whose
+// maximum is current at 2^kHead, so 21 binary orders below it keep all 11
+// bits; the running maximum may lag by kLag before O is rescaled, and 2^(kHead
+// + kLag) = 32768 stays below the largest f16.
+constexpr float kHead = 7.f, kLag = 8.f;
+constexpr float kMaxSentinel = -1.0e30f;
+constexpr uint64_t kDrainNs = 500000000ull;
+constexpr uint32_t kSleepNs = 20000;
+
+struct Bars {
+  uint64_t full[kSlots];   // slab landed in both CTAs (even CTA)
+  uint64_t empty[kSlots];  // slab read by the MMAs (both)
+  uint64_t q_full;         // a segment's query rows landed in both CTAs (even CTA)
+  uint64_t q_empty;        // the segment's last score MMA is done (both)
+  uint64_t s_full[2];      // scores written (both)
+  uint64_t p_full;         // weights written by the 16 softmax warps of the pair (even CTA)
+  uint64_t o_done;         // values of the tile accumulated (both)
+  uint64_t o_free;         // the segment's O read by the 16 softmax warps (even CTA)
+  uint64_t drain;
+  uint32_t tmem_base;
+  int32_t abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+struct Ctx {
+  int32_t* status;
+  volatile int32_t* abort;
+  uint64_t limit_ns;
+  uint32_t sleep_ns;
+};
+
+// True when the phase completed; false once any wait of this CTA has run out.
+__device__ __forceinline__ bool wait(const Ctx& c, uint32_t bar, uint32_t parity) {
+  if (ptx::mbar_try_wait_cluster(bar, parity, c.sleep_ns)) return true;
+  const uint64_t t0 = ptx::globaltimer_ns();
+  while (true) {
+    if (*c.abort) return false;
+    if (ptx::mbar_try_wait_cluster(bar, parity, c.sleep_ns)) return true;
+    if (ptx::globaltimer_ns() - t0 > c.limit_ns) {
+      atomicOr(c.status, MLA_DEVFLAG_TIMEOUT);
+      *c.abort = 1;
+      return false;
+    }
+  }
+}
+
+__device__ __forceinline__ float fast_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  __half2 v = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+// K-major, 128B-swizzled operand (8-row groups 1 KB apart).
+__device__ __forceinline__ uint64_t kdesc(uint32_t addr) { return ptx::smem_desc(addr, 16, 1024, 2); }
+// MN-major values: 64-dim halves of a slab 8 KB apart, 8-key groups 1 KB apart.
+__device__ __forceinline__ uint64_t vdesc(uint32_t addr) { return ptx::smem_desc(addr, 8192, 1024, 2); }
+
+// The four warps that hold one set of 32 rows.
+__device__ __forceinline__ void group_sync(int g) {
+  asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
+}
+
+// A pair's walk over its segments: row block rb, tiles [t0, t1).
+struct Walk {
+  int64_t at, end;
+  int tiles;
+  int rb, t0, t1;
+  __device__ __forceinline__ Walk(const mla::PrefixParams& p, int pair)
+      : at(mla::prefix_share(p.total_tiles, p.pairs, pair)),
+        end(mla::prefix_share(p.total_tiles, p.pairs, pair + 1)),
+        tiles(p.tiles) {}
+  __device__ __forceinline__ bool next() {
+    if (at >= end) return false;
+    rb = (int)(at / tiles);
+    t0 = (int)(at - (int64_t)rb * tiles);
+    t1 = (int)min((int64_t)tiles, t0 + (end - at));
+    at += t1 - t0;
+    return true;
+  }
+};
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    prefix_kernel(mla::PrefixParams p, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap qmap) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
+  Bars& bars = *reinterpret_cast<Bars*>(smem + OFF_BAR);
+  const uint32_t sbase = ptx::smem_u32(smem);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = ptx::cluster_ctarank();
+  const int pair = blockIdx.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kSlots; ++i) {
+      ptx::mbar_init(ptx::smem_u32(&bars.full[i]), 1);
+      ptx::mbar_init(ptx::smem_u32(&bars.empty[i]), 1);
+    }
+    ptx::mbar_init(ptx::smem_u32(&bars.q_full), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars.q_empty), 1);
+    for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&bars.s_full[i]), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars.p_full), 2 * kSoftmaxWarps);
+    ptx::mbar_init(ptx::smem_u32(&bars.o_done), 1);
+    ptx::mbar_init(ptx::smem_u32(&bars.o_free), 2 * kSoftmaxWarps);
+    ptx::mbar_init(ptx::smem_u32(&bars.drain), 1);
+    bars.abort = 0;
+    ptx::fence_mbar_init_cluster();
+  }
+  if (warp == kMmaWarp) {
+    ptx::tmem_alloc_pair(ptx::smem_u32(&bars.tmem_base), TM_COLS);
+    ptx::tmem_relinquish_pair();
+  }
+  ptx::tc_fence_before();
+  ptx::cluster_sync_all();  // both CTAs' barriers are initialised before any remote arrive
+  ptx::tc_fence_after();
+  ptx::grid_dependency_wait();
+  const uint32_t tmem = bars.tmem_base;
+  Ctx c{p.status, &bars.abort, p.wait_ns,
+        (uint32_t)(p.wait_ns < (uint64_t)kSleepNs ? p.wait_ns : (uint64_t)kSleepNs)};
+  Walk w(p, pair);
+
+  if (warp == kLoadWarp) {
+    // -------------------------------------------------------------- loads ---
+    if (lane == 0) {
+      int slot = 0, issued = 0;
+      uint32_t ph = 1;  // a fresh barrier passes the wait for the phase before its first
+      bool ok = true;
+      auto slab = [&](int x0, int y0, int x1, int y1) {
+        ok = ok && wait(c, ptx::smem_u32(&bars.empty[slot]), ph);
+        if (!ok) return;
+        const uint32_t bar = ptx::mapa(ptx::smem_u32(&bars.full[slot]), 0);
+        if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars.full[slot]), 2 * SLAB);
+        const uint32_t dst = sbase + OFF_RING + slot * SLAB;
+        ptx::tma_load_2d_pair(dst, &kmap, x0, y0, bar);
+        ptx::tma_load_2d_pair(dst + SLAB / 2, &kmap, x1, y1, bar);
+        ++issued;
+        if (++slot == kSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      };
+      auto scores = [&](int t) {
+        const int y = t * T + 128 * (int)rank;
+        for (int d = 0; d < 9; ++d) slab(64 * d, y, 64 * d, y + 64);
+      };
+      for (int seg = 0; w.next(); ++seg) {
+        if (seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.q_empty), (seg - 1) & 1);
+        if (ok) {
+          if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars.q_full), 2 * 9 * QSLAB);
+          const uint32_t bar = ptx::mapa(ptx::smem_u32(&bars.q_full), 0);
+          for (int d = 0; d < 9; ++d)
+            ptx::tma_load_2d_pair(sbase + OFF_Q + d * QSLAB, &qmap, 64 * d,
+                                  w.rb * mla::kRowTile + 64 * (int)rank, bar);
+        }
+        scores(w.t0);
+        for (int t = w.t0; t < w.t1; ++t) {
+          if (t + 1 < w.t1) scores(t + 1);
+          for (int kg = 0; kg < 4; ++kg)
+            for (int j = 0; j < 2; ++j) {
+              const int x = 256 * (int)rank + 128 * j;
+              slab(x, t * T + 64 * kg, x + 64, t * T + 64 * kg);
+            }
+        }
+      }
+      // After a wait ran out, copies may still be landing: the even CTA, whose
+      // barriers count both CTAs' bytes, waits for the last ones.
+      if (!ok && rank == 0) {
+        const uint64_t start = ptx::globaltimer_ns();
+        for (int i = max(0, issued - kSlots); i < issued; ++i)
+          while (!ptx::mbar_try_wait(ptx::smem_u32(&bars.full[i % kSlots]), (i / kSlots) & 1))
+            if (ptx::globaltimer_ns() - start > kDrainNs) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp == kMmaWarp) {
+    // ---------------------------------------------------------------- MMA ---
+    if (lane == 0 && rank == 0) {
+      const uint32_t id_qk = ptx::idesc_f16(128, T, 0u, false, false);
+      const uint32_t id_pv = ptx::idesc_f16(128, 256, 0u, false, true);
+      // A slab, a 32-byte step of 16 dims or a 2 KB step of 16 keys is an add
+      // to the descriptor's start address (16-byte units, no carry).
+      const uint64_t dq = kdesc(sbase + OFF_Q), dp = kdesc(sbase + OFF_P);
+      const uint64_t dk = kdesc(sbase + OFF_RING), dv = vdesc(sbase + OFF_RING);
+      bool ok = true;
+      int slot = 0;
+      uint32_t ph = 0;
+      uint32_t it = 0;  // tiles whose scores this pair has issued, over all segments
+      auto advance = [&] {
+        ptx::mma_commit_pair(ptx::smem_u32(&bars.empty[slot]));
+        if (++slot == kSlots) {
+          slot = 0;
+          ph ^= 1u;
+        }
+      };
+      auto values = [&](uint32_t i, bool first) {
+        ok = ok && wait(c, ptx::smem_u32(&bars.p_full), i & 1);
+        for (int kg = 0; kg < 4 && ok; ++kg)
+          for (int j = 0; j < 2 && ok; ++j) {
+            ok = wait(c, ptx::smem_u32(&bars.full[slot]), ph);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              ptx::mma_ss_pair(tmem + TM_O + 128 * j, dp + kg * (PSLAB >> 4) + 2 * k,
+                               dv + slot * (SLAB >> 4) + k * (2048 >> 4), id_pv,
+                               !(first && kg == 0 && k == 0));
+            advance();
+          }
+        if (ok) ptx::mma_commit_pair(ptx::smem_u32(&bars.o_done));
+      };
+      for (int seg = 0; ok && w.next(); ++seg) {
+        ok = wait(c, ptx::smem_u32(&bars.q_full), seg & 1);
+        const int n = w.t1 - w.t0;
+        for (int t = 0; t < n && ok; ++t) {
+          for (int d = 0; d < 9 && ok; ++d) {
+            ok = wait(c, ptx::smem_u32(&bars.full[slot]), ph);
+            if (!ok) break;
+            ptx::tc_fence_after();
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              ptx::mma_ss_pair(tmem + TM_S + 128 * (it & 1), dq + d * (QSLAB >> 4) + 2 * k,
+                               dk + slot * (SLAB >> 4) + 2 * k, id_qk, (d | k) != 0);
+            advance();
+          }
+          if (!ok) break;
+          ptx::mma_commit_pair(ptx::smem_u32(&bars.s_full[it & 1]));
+          if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
+          ++it;
+          if (t == 1 && seg > 0) ok = wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
+          if (t > 0) values(it - 2, t == 1);
+        }
+        if (n == 1 && seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
+        if (ok) values(it - 1, n == 1);
+      }
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------ softmax ---
+    // This thread: TMEM lane l = 32 q4 + lane, i.e. row l % 64 of the CTA's 64
+    // and half l / 64 of N; score columns 64 ch .. 64 ch + 63, so the 64-key
+    // group kg of its row, and O columns 128 ch .. + 127, so 128 value dims.
+    const int q4 = warp & 3, ch = warp >> 2;
+    const int r = 32 * (q4 & 1) + lane;
+    const int kg = 2 * (q4 >> 1) + ch;
+    const int dim0 = 256 * (q4 >> 1) + 128 * ch;
+    const uint32_t lanes = (uint32_t)(32 * q4) << 16;
+    const float s_kv = p.kv_scale != nullptr ? *p.kv_scale : 1.f;
+    // A scale of zero is taken as the smallest that keeps -inf * c2 = -inf.
+    const float c2 = fmaxf(p.softmax_scale * s_kv * 1.4426950408889634f, 1.0e-37f);
+    const uint32_t p_full = ptx::mapa(ptx::smem_u32(&bars.p_full), 0);
+    const uint32_t o_free = ptx::mapa(ptx::smem_u32(&bars.o_free), 0);
+    volatile float* xch = reinterpret_cast<volatile float*>(smem + OFF_X);
+    const uint32_t p_row = sbase + OFF_P + kg * PSLAB + r * 128;
+    uint32_t it = 0;
+    while (w.next()) {
+      const int row = w.rb * mla::kRowTile + 64 * (int)rank + r;
+      int limit = 0;  // shared keys this row sees
+      if (row < p.rows) {
+        const int b = row / p.rows_per_seq;
+        int ctx = p.seq_lens[b];
+        if (ctx < 0 || ctx > p.max_ctx) {
+          atomicOr(p.status, MLA_DEVFLAG_CTX_RANGE);
+          ctx = ctx < 0 ? 0 : p.max_ctx;
+        }
+        const int tok = (row - b * p.rows_per_seq) / p.heads;
+        const int n = p.causal ? ctx - p.sq + tok + 1 : ctx;
+        limit = max(0, min(n, p.prefix_len));
+      }
+      float m = kMaxSentinel, l = 0.f;
+      for (int t = w.t0; t < w.t1; ++t, ++it) {
+        wait(c, ptx::smem_u32(&bars.s_full[it & 1]), (it >> 1) & 1);
+        __syncwarp();
+        ptx::tc_fence_after();
+        uint32_t s[2][32];
+        ptx::tmem_ld32(tmem + lanes + TM_S + 128 * (it & 1) + 64 * ch, s[0]);
+        ptx::tmem_ld32(tmem + lanes + TM_S + 128 * (it & 1) + 64 * ch + 32, s[1]);
+        ptx::tmem_ld_wait();
+        const int lim = limit - t * T - 64 * kg;  // keys of this thread's 64 that the row sees
+        const bool all = __all_sync(0xffffffffu, lim >= 64);
+        if (!all) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (32 * h + i >= lim) s[h][i] = 0xFF800000u;  // -inf: weight 0
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[h][i]));
+        const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+        volatile float* x = xch + (it & 1) * 256;
+        x[kg * 64 + r] = mine;
+        group_sync(q4 & 1);
+        const float mt = fmaxf(fmaxf(x[r], x[64 + r]), fmaxf(x[128 + r], x[192 + r])) * c2;
+        // The row's maximum moves only when it lags by more than kLag; a row
+        // that has seen no key yet keeps the sentinel.
+        const bool need = mt > m + kLag;
+        const float mn = need ? mt : m;
+        const float alpha = need ? exp2f(m - mn) : 1.f;
+        m = mn;
+        l *= alpha;
+        const float base = kHead - m;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pk[32];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const float a = fast_exp2(fmaf(__uint_as_float(s[h][i]), c2, base));
+            const float b2 = fast_exp2(fmaf(__uint_as_float(s[h][i + 1]), c2, base));
+            sum[i & 3] += a;
+            sum[(i & 3) + 1] += b2;
+            pk[16 * h + i / 2] = pack_f16(a, b2);
+          }
+        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        // The weights' buffer and O are free once the values of the tile
+        // before are accumulated (a segment's first tile waited for that at
+        // the end of the segment before).
+        if (t > w.t0) {
+          wait(c, ptx::smem_u32(&bars.o_done), (it - 1) & 1);
+          __syncwarp();
+          if (__any_sync(0xffffffffu, need)) {
+            ptx::tc_fence_after();
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t o[32];
+              const uint32_t col = tmem + lanes + TM_O + 128 * ch + 32 * cc;
+              ptx::tmem_ld32(col, o);
+              ptx::tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              ptx::tmem_st32(col, o);
+            }
+            ptx::tmem_st_wait();
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v)
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + ((v ^ (r & 7)) * 16)),
+                       "r"(pk[4 * v]), "r"(pk[4 * v + 1]), "r"(pk[4 * v + 2]), "r"(pk[4 * v + 3])
+                       : "memory");
+        ptx::fence_proxy_async_smem();
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive_cluster(p_full);
+      }
+      // The segment's partial: O / l and the log-sum-exp.
+      group_sync(q4 & 1);  // the exchange buffer's last maxima are read
+      xch[kg * 64 + r] = l;
+      group_sync(q4 & 1);
+      l = (xch[r] + xch[64 + r]) + (xch[128 + r] + xch[192 + r]);
+      const bool good = wait(c, ptx::smem_u32(&bars.o_done), (it - 1) & 1);
+      __syncwarp();
+      ptx::tc_fence_after();
+      const int first = mla::prefix_pair_of(p.total_tiles, p.pairs, (int64_t)w.rb * p.tiles);
+      const size_t slot = (size_t)(pair - first) * p.rows + row;
+      const float inv = l > 0.f ? s_kv / l : 0.f;
+      const bool write = good && row < p.rows;
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t o[32];
+        ptx::tmem_ld32(tmem + lanes + TM_O + 128 * ch + 32 * cc, o);
+        ptx::tmem_ld_wait();
+        if (write) {
+          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * mla::kDV + dim0 + 32 * cc);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
+                                 __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+        }
+      }
+      if (write && kg == 0)
+        p.part_lse[slot] = l > 0.f ? (m - kHead + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      ptx::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive_cluster(o_free);
+      group_sync(q4 & 1);  // the sums are read before the next segment's maxima
+    }
+  }
+
+  // ------------------------------------------------------------ teardown ---
+  ptx::tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp && bars.abort && rank == 0) {
+    if (lane == 0) {
+      ptx::mma_commit_pair(ptx::smem_u32(&bars.drain));
+      const uint64_t start = ptx::globaltimer_ns();
+      while (!ptx::mbar_try_wait(ptx::smem_u32(&bars.drain), 0))
+        if (ptx::globaltimer_ns() - start > kDrainNs) break;
+    }
+    __syncwarp();
+  }
+  ptx::cluster_sync_all();  // no CTA leaves, or frees TMEM, while the pair still works
+  if (warp == kMmaWarp) {
+    ptx::tc_fence_after();
+    ptx::tmem_dealloc_pair(tmem, TM_COLS);
+  }
+}
+
+}  // namespace
+
+int mla_launch_prefix_sm103(const mla::PrefixParams& p, const CUtensorMap& kmap,
+                            const CUtensorMap& qmap, void* stream) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return (int)e;
+  e = mla::opt_in_smem(reinterpret_cast<const void*>(prefix_kernel), SMEM_BYTES, dev, 8);
+  if (e != cudaSuccess) return (int)e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * p.pairs, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.dynamicSmemBytes = SMEM_BYTES;
+  cfg.stream = static_cast<cudaStream_t>(stream);
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return (int)cudaLaunchKernelEx(&cfg, prefix_kernel, p, kmap, qmap);
+}

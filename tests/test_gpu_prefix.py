@@ -1,0 +1,233 @@
+"""The shared-prefix decode against the fp64 oracle on the same bits, at the
+bar of parity.py: the pass over the shared keys, the merge with each sequence's
+own keys, the masks and the walk of the CTA pairs over row blocks."""
+import numpy as np
+import pytest
+
+import mla_synth as syn
+from parity import assert_close
+from prefix_problems import PrefixProblem
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP8 = syn.KV_BF16, syn.KV_FP8_E4M3
+
+CASES = {
+    # name: (batch, sq, heads, lens, prefix, page_size, kv_dtype, causal)
+    "one_key": (1, 1, 1, [1], 1, 1, BF16, False),
+    "one_row_one_own_key": (1, 1, 1, [2], 1, 1, BF16, False),
+    "tile_minus_one": (2, 1, 16, [255, 300], 255, 16, BF16, False),
+    "tile": (2, 1, 16, [256, 257], 256, 16, BF16, False),
+    "tile_plus_one": (2, 1, 16, [257, 258], 257, 16, BF16, False),
+    "h128": (3, 1, 128, [700, 701, 900], 700, 1, BF16, False),
+    "h128_one_block_short": (1, 1, 100, [1300], 1200, 16, BF16, False),
+    "h16_b20_fp8": (20, 1, 16, [1000 + 7 * i for i in range(20)], 1000, 64, FP8, False),
+    "h128_fp8": (2, 1, 128, [640, 530], 512, 64, FP8, False),
+    "odd_pages": (13, 3, 12, [4999 + 1 + 25 * i for i in range(13)], 4999, 7, FP8, True),
+    "causal_mtp": (5, 4, 16, [520, 604, 513, 530, 777], 512, 16, BF16, True),
+    # Sequences shorter than the prefix, shorter than the tokens, empty, just at it.
+    "short_sequences": (8, 4, 16, [0, 2, 5, 255, 300, 511, 512, 516], 512, 16, BF16, True),
+    "short_sequences_unmasked": (4, 1, 40, [0, 1, 300, 700], 640, 16, BF16, False),
+    "all_empty": (3, 1, 16, [0, 0, 0], 64, 16, BF16, False),
+    "no_prefix": (3, 1, 16, [40, 0, 129], 0, 16, BF16, False),
+    "no_own_keys": (4, 1, 64, [600] * 4, 600, 1, BF16, False),
+    "long_own": (2, 1, 128, [3300, 400], 300, 16, BF16, False),
+    "rows_two_blocks_a_sequence": (2, 2, 128, [900, 850], 800, 16, BF16, True),
+}
+
+
+@pytest.mark.parametrize("name", list(CASES))
+def test_against_oracle(name):
+    p = PrefixProblem(*CASES[name], seed=len(name))
+    out, lse, plan, status = p.run()
+    assert status == 0
+    assert_close(out, lse, *p.reference(), name)
+
+
+@pytest.mark.parametrize("num_sms", [2, 4, 6, 10, 38, 152])
+def test_pairs_and_segments(num_sms):
+    """One pair walks every row block; more cut row blocks at odd tiles."""
+    p = PrefixProblem(5, 1, 128, [1500 + i for i in range(5)], 1450, 1, seed=3)
+    ref = p.reference()
+    out, lse, plan, status = p.run(num_sms=num_sms)
+    assert status == 0 and plan.pairs <= num_sms // 2
+    assert_close(out, lse, *ref, f"{plan.pairs} pairs")
+
+
+def test_plan_of_every_pair_count():
+    """Any pair count gives the same rows, within the bar: the merge of cut row blocks."""
+    p = PrefixProblem(3, 1, 100, [2100, 2090, 2400], 2080, 16, seed=5)
+    ref, t = p.reference(), p.to_device()
+    for sms in range(2, 56, 6):
+        out, lse, plan, status = p.run(t=t, num_sms=sms)
+        assert status == 0
+        assert_close(out, lse, *ref, f"sms {sms}, {plan.pairs} pairs, {plan.prefix_slots} slots")
+
+
+@pytest.mark.parametrize("heads,sq,dtype", [(16, 4, BF16), (128, 1, BF16), (16, 1, FP8)])
+def test_outlier_keys(heads, sq, dtype):
+    p = PrefixProblem(6, sq, heads, [2300 + 30 * i for i in range(6)], 2222, 16, dtype, sq > 1,
+                      seed=11, outlier_frac=0.01)
+    out, lse, plan, status = p.run()
+    assert status == 0
+    assert_close(out, lse, *p.reference(), "outliers")
+
+
+def test_running_maximum_is_rescaled():
+    """Scores that climb by far more than the lag from tile to tile."""
+    p = PrefixProblem(2, 1, 128, [1300, 1290], 1280, 1, seed=2)
+    ramp = np.linspace(0.02, 3.0, 1280, dtype=np.float32)
+    f = syn.bf16_bits_to_f32(p.cache)
+    q0 = syn.bf16_bits_to_f32(p.q_bits)[0, 0, 0]
+    for j in range(1280):  # key j leans on the first row's query more and more
+        f[p.prefix_table[j], 0] += ramp[j] * q0
+    p.cache = syn.f32_to_bf16_bits(f)
+    out, lse, plan, status = p.run()
+    assert status == 0
+    ref = p.reference()
+    assert ref[1].max() > 100  # the climb is there
+    assert_close(out, lse, *ref, "ramp")
+
+
+@pytest.mark.parametrize("scale", [0.0, 2.0 ** -10, 0.5])
+def test_scales(scale):
+    p = PrefixProblem(3, 1, 32, [300, 100, 270], 260, 16, seed=4, scale=scale, q_mult=0.25)
+    out, lse, _, status = p.run()
+    assert status == 0
+    assert_close(out, lse, *p.reference(), f"scale {scale}")
+
+
+def test_same_as_the_decode_without_sharing():
+    """The documented equality: the plain decode on tables that hold the prefix."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(4, 2, 16, [700, 650, 649, 800], 640, 16, causal=True, seed=8)
+    t = p.to_device()
+    out, lse, _, _ = p.run(t=t)
+    full = t["bt"].clone()
+    full[:, :40] = t["pt"]
+    o2, l2 = mla.decode(t["q"], t["cache"], full, t["lens"], softmax_scale=p.scale, causal=True)
+    assert_close(out, lse, o2.double().cpu().numpy(), l2.double().cpu().numpy(), "decode")
+    o3, l3 = mla.decode_prefix(t["q"], t["cache"], full[0], full, t["lens"], 640,
+                               softmax_scale=p.scale, causal=True)
+    torch.cuda.synchronize()
+    assert np.array_equal(o3.double().cpu().numpy(), out) and np.array_equal(l3.double().cpu().numpy(), lse)
+
+
+def test_deterministic_and_workspace_reuse():
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(9, 1, 64, [3000 + i for i in range(9)], 2950, 16, seed=6)
+    t, plan = p.to_device(), p.plan()
+    ws = torch.full((int(plan.workspace_bytes),), 255, dtype=torch.uint8, device="cuda")
+    a = p.run(t=t, plan=plan, workspace=ws)
+    b = p.run(t=t, plan=plan, workspace=ws)
+    assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+    assert_close(a[0], a[1], *p.reference(), "reuse")
+    assert mla.prefix_check(plan, ws) == 0
+
+
+def test_graph_replay_with_new_lengths():
+    """Captured once; the lengths, the queries and the cache change under it."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    big = PrefixProblem(6, 1, 128, [1400, 1280, 1100, 1350, 1281, 1290], 1280, 16, seed=9)
+    t, plan = big.to_device(), big.plan()
+    ws = mla.workspace_for(plan)
+    out = torch.empty(6, 1, 128, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(6, 1, 128, device="cuda")
+    call = lambda: mla.prefix_fwd(plan, t["q"], t["cache"], None, t["pt"], t["bt"], t["lens"],  # noqa: E731
+                                  big.scale, out, lse, ws)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        call()
+    for lens in ([1400, 1280, 1100, 1350, 1281, 1290], [1290, 0, 1100, 1281, 1281, 700],
+                 [1, 1280, 1000, 1300, 1281, 1285]):
+        big.lens = np.asarray(lens, np.int32)
+        t["lens"].copy_(torch.from_numpy(big.lens))
+        t["q"].mul_(-1.0)
+        big.q_bits = big.q_bits ^ np.uint16(0x8000)
+        out.fill_(float("nan"))
+        g.replay()
+        torch.cuda.synchronize()
+        assert mla.prefix_check(plan, ws) == 0
+        assert_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), *big.reference(), f"{lens}")
+
+
+def test_side_stream():
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(3, 1, 64, [600, 610, 590], 580, 16, seed=10)
+    t, plan = p.to_device(), p.plan()
+    ws = mla.workspace_for(plan)
+    out = torch.empty(3, 1, 64, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(3, 1, 64, device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    mla.prefix_fwd(plan, t["q"], t["cache"], None, t["pt"], t["bt"], t["lens"], p.scale, out, lse,
+                   ws, stream=s)
+    assert mla.prefix_check(plan, ws, stream=s) == 0
+    assert_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), *p.reference(), "stream")
+
+
+def test_bad_pages_and_contexts_are_flagged():
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(4, 1, 16, [600, 610, 590, 640], 580, 16, seed=12)
+    t, plan = p.to_device(), p.plan()
+    t["pt"][3] = 1 << 28
+    assert p.run(t=t, plan=plan)[3] & mla.DEVFLAG_BAD_PAGE
+    t = p.to_device()
+    t["bt"][2, 36] = -5
+    out, lse, _, status = p.run(t=t, plan=plan)
+    assert status & mla.DEVFLAG_BAD_PAGE
+    ref = p.reference()
+    keep = [0, 1, 3]
+    assert_close(out[keep], lse[keep], ref[0][keep], ref[1][keep], "the other sequences")
+    t = p.to_device()
+    t["lens"][1] = 100000  # clamped to the plan's 640: the table has no page there for it
+    t["bt"][1, 38:] = t["bt"][1, 37]
+    t["lens"][0] = -3
+    out, lse, _, status = p.run(t=t, plan=plan)
+    assert status & mla.DEVFLAG_CTX_RANGE
+    assert np.all(out[0] == 0) and np.all(np.isneginf(lse[0]))
+    assert_close(out[2:], lse[2:], ref[0][2:], ref[1][2:], "the other sequences")
+
+
+@pytest.mark.parametrize("what", ["cache", "cache_nan", "q"])
+def test_values_beyond_f16_are_flagged(what):
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(2, 1, 16, [300, 290], 256, 16, seed=13)
+    t = p.to_device()
+    if what == "q":
+        t["q"][1, 0, 3, 5] = 70000.0
+    else:
+        t["cache"][int(p.prefix_table[2]), 4, 9] = 70000.0 if what == "cache" else float("nan")
+    out, lse, _, status = p.run(t=t)
+    assert status == (mla.DEVFLAG_Q_RANGE if what == "q" else mla.DEVFLAG_KV_RANGE)
+    if what == "q":  # only the row that holds it
+        ref = p.reference()
+        assert_close(out[0], lse[0], ref[0][0], ref[1][0], "the other sequence")
+
+
+def test_small_values():
+    """Below 2^-14 the staged values keep an absolute 2^-25: q and cache scaled down."""
+    p = PrefixProblem(2, 1, 64, [400, 380], 300, 1, seed=14, q_mult=2.0 ** -9)
+    out, lse, _, status = p.run()
+    assert status == 0
+    assert_close(out, lse, *p.reference(), "small q")
+
+
+def test_a_wait_that_runs_out():
+    """A 1 us limit ends every long wait; the call reports it and the next one is whole."""
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(16, 1, 128, [4096 + 64] * 16, 4096, 16, seed=15)
+    t, plan = p.to_device(), p.plan()
+    ws = mla.workspace_for(plan)
+    plan.wait_limit_us = 1
+    assert p.run(t=t, plan=plan, workspace=ws)[3] & mla.DEVFLAG_TIMEOUT
+    plan.wait_limit_us = 0
+    out, lse, _, status = p.run(t=t, plan=plan, workspace=ws)
+    assert status == 0
+    assert_close(out, lse, *p.reference(), "after the timeout")

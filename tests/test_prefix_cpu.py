@@ -1,0 +1,113 @@
+"""Host side of the shared-prefix decode: the plan and the refusals."""
+import ctypes
+
+import numpy as np
+import pytest
+
+import paged_mla_decode_latent_gb300 as mla
+
+
+@pytest.fixture(scope="module", autouse=True)
+def built():
+    mla.build()
+
+
+def share(total, pairs, i):
+    return total * i // pairs
+
+
+@pytest.mark.parametrize("batch,heads,sq,prefix,own,sms", [
+    (1, 1, 1, 1, 0, 152), (4, 16, 1, 512, 64, 152), (64, 128, 1, 8192, 512, 152),
+    (13, 12, 3, 4999, 333, 152), (128, 128, 1, 23333, 512, 152), (3, 100, 1, 255, 1, 2),
+    (7, 128, 8, 100000, 10, 148), (2, 16, 1, 0, 90, 152), (5, 64, 1, 257, 0, 37)])
+def test_plan(batch, heads, sq, prefix, own, sms):
+    lens = [prefix + (own * (b + 1)) // batch for b in range(batch)]
+    p = mla.prefix_plan(lens, prefix, heads, sq, 16, mla.KV_BF16, sq > 1, sms)
+    assert p.total_rows == batch * heads * sq and p.row_blocks == -(-p.total_rows // 128)
+    assert p.prefix_tiles == -(-prefix // 256) and p.max_ctx == max(lens)
+    assert p.own_splits * p.own_chunk >= own and p.own_chunk % p.key_tile == 0
+    assert (p.own_splits == 0) == (own == 0)
+    total = p.row_blocks * p.prefix_tiles
+    if prefix:
+        assert 1 <= p.pairs <= min(max(1, sms // 2), total)
+        # Every pair has a tile, every tile one pair, and the slots cover a row block's pairs.
+        edges = [share(total, p.pairs, i) for i in range(p.pairs + 1)]
+        assert edges[0] == 0 and edges[-1] == total and all(a < b for a, b in zip(edges, edges[1:]))
+        slots = 0
+        for j in range(p.row_blocks):
+            t0, t1 = j * p.prefix_tiles, (j + 1) * p.prefix_tiles
+            holders = [i for i in range(p.pairs) if edges[i] < t1 and edges[i + 1] > t0]
+            first = ((t0 + 1) * p.pairs - 1) // total
+            assert holders[0] == first and holders == list(range(holders[0], holders[-1] + 1))
+            slots = max(slots, len(holders))
+        assert p.prefix_slots == slots
+    offs = [p.ws_status_offset, p.ws_keys_offset, p.ws_q_offset, p.ws_prefix_o_offset,
+            p.ws_prefix_lse_offset, p.ws_own_o_offset, p.ws_own_lse_offset, p.workspace_bytes]
+    sizes = [16, prefix * 1152, p.total_rows * 1152 if prefix else 0,
+             p.prefix_slots * p.total_rows * 2048, p.prefix_slots * p.total_rows * 4,
+             p.own_splits * p.total_rows * 2048, p.own_splits * p.total_rows * 4]
+    for a, b, n in zip(offs, offs[1:], sizes):
+        assert a % 256 == 0 and b - a >= n
+
+
+def test_struct_layout():
+    assert ctypes.sizeof(mla.PrefixPlan) == 20 * 4 + 8 * 8
+
+
+@pytest.mark.parametrize("kw", [
+    dict(lens=[-1]), dict(lens=[]), dict(prefix=-1), dict(prefix=(1 << 22) + 1), dict(heads=0),
+    dict(heads=129), dict(sq=0), dict(sq=17), dict(heads=128, sq=9), dict(page=0), dict(page=4097),
+    dict(dtype=2)])
+def test_plan_refuses(kw):
+    a = dict(lens=[100], prefix=64, heads=16, sq=1, page=16, dtype=0)
+    a.update(kw)
+    with pytest.raises(mla.MLADecodeError) as e:
+        mla.prefix_plan(a["lens"], a["prefix"], a["heads"], a["sq"], a["page"], a["dtype"], False, 152)
+    assert e.value.status == mla.ERR_INVALID_ARG
+
+
+def test_plan_refuses_too_many_rows():
+    with pytest.raises(mla.MLADecodeError) as e:
+        mla.prefix_plan([1] * 65535, 1, 128, 8, 1, 0, True, 152)
+    assert e.value.status == mla.ERR_UNSUPPORTED
+
+
+def fwd(plan, **kw):
+    """mla_decode_prefix_fwd on made-up aligned addresses: every refusal comes before any use."""
+    a = dict(q=1 << 20, cache=2 << 20, pages=64, scale=None, pt=3 << 20, bt=4 << 20, stride=16,
+             lens=5 << 20, softmax=0.07, out=6 << 20, lse=7 << 20, ws=8 << 20,
+             bytes=plan.workspace_bytes)
+    a.update(kw)
+    return mla.lib().mla_decode_prefix_fwd(
+        ctypes.byref(plan), a["q"], a["cache"], a["pages"], a["scale"], a["pt"], a["bt"],
+        a["stride"], a["lens"], a["softmax"], a["out"], a["lse"], a["ws"], a["bytes"], None)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(q=None), -1), (dict(cache=None), -1), (dict(pt=None), -1), (dict(bt=None), -1),
+    (dict(lens=None), -1), (dict(out=None), -1), (dict(lse=None), -1), (dict(q=(1 << 20) + 2), -1),
+    (dict(cache=(1 << 20) + 8), -1), (dict(out=(1 << 20) + 8), -1), (dict(pt=(1 << 20) + 2), -1),
+    (dict(scale=(1 << 20) + 1), -1), (dict(pages=0), -1), (dict(pages=1 << 30), -2),
+    (dict(stride=6), -1), (dict(softmax=float("nan")), -1), (dict(softmax=float("inf")), -1),
+    (dict(softmax=-1.0), -1), (dict(ws=None), -3), (dict(ws=(8 << 20) + 16), -3), (dict(bytes=100), -3)])
+def test_fwd_refuses(kw, status):
+    plan = mla.prefix_plan([100, 120], 64, 16, 1, 16, 0, False, 152)
+    assert fwd(plan, **kw) == status
+
+
+@pytest.mark.parametrize("field,value", [
+    ("version", 0), ("batch", 0), ("rows", 17), ("total_rows", 33), ("prefix_len", 600),
+    ("prefix_tiles", 2), ("pairs", 0), ("pairs", 100), ("prefix_slots", 5), ("own_splits", 400),
+    ("own_chunk", 100), ("key_tile", 64), ("wait_limit_us", -1), ("kv_dtype", 7), ("page_size", 0)])
+def test_fwd_refuses_an_edited_plan(field, value):
+    plan = mla.prefix_plan([100, 120], 64, 16, 1, 16, 0, False, 152)
+    setattr(plan, field, value)
+    assert fwd(plan) == mla.ERR_INVALID_ARG
+
+
+def test_plan_is_quick():
+    import time
+    t0 = time.perf_counter()
+    for _ in range(3):
+        mla.prefix_plan(np.full(128, 23500), 23333, 128, 1, 16, 0, False, 152)
+    assert (time.perf_counter() - t0) / 3 < 0.25
