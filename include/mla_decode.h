@@ -86,6 +86,7 @@ typedef enum mla_kv_dtype {
 #define MLA_DEVFLAG_Q_RANGE 0x8    /* fp8 or shared-prefix path: |q| beyond the fp16 range */
 #define MLA_DEVFLAG_KV_RANGE 0x10  /* shared prefix: a cache value beyond the fp16
                                       range, infinite or NaN */
+#define MLA_DEVFLAG_POSITION 0x20  /* rotation: a position outside the table */
 
 #define MLA_DECODE_PLAN_VERSION 1
 #define MLA_D_QK 576 /* query/key row width: 512 latent + 64 rope */
@@ -370,6 +371,51 @@ int mla_decode_epilogue(const void* ql_nope, const void* q_pe, const void* kv_c,
                         int32_t num_heads, void* q_out, void* kv_cache, int64_t num_pages,
                         int32_t page_size, int32_t kv_dtype, const float* kv_scale,
                         int32_t cache_inputs_early, int32_t* status, void* stream);
+
+/*
+ * mla_decode_rope_epilogue -- mla_decode_epilogue for inputs that are not yet
+ * rotated: the position rotation is applied to the rope dims on the way.
+ *
+ *   (c_i, s_i)           = cos_sin[positions[t]][i], [32 + i]          i < 32
+ *   rot(x)               = the pairs (x_a, x_b) of x as
+ *                          (x_a c_i - x_b s_i, x_b c_i + x_a s_i), with (a, b)
+ *                          = (2i, 2i + 1) if interleaved, else (i, i + 32)
+ *   q_out[t, h, 0:512]   = ql_nope[t, h, :]     q_out[t, h, 512:576] = rot(q_pe[t, h, :])
+ *   row                  = kv_c[t, :] || rot(k_pe[t, :])
+ *   cache[slot / page_size][slot % page_size][:] = row                bf16 cache
+ *                                              = e4m3(row / kv_scale) fp8 cache
+ * The rotation is fp32, rounded once to the type it is stored in.  slot < 0 (a
+ * padding token) inserts nothing; its query rows are still written.  The slots
+ * of one call are distinct (of two tokens with one slot, each 16-byte piece
+ * keeps either).
+ *
+ * The inputs may be views of the projections they come from: strides are in
+ * elements, >= 0 and multiples of 8, the last dimension contiguous, every base
+ * 16-byte aligned; the stride of a dimension of one is ignored.
+ *
+ * ql_nope      device bf16 [T, H, 512], strides (ql_stride_t, ql_stride_h)
+ * q_pe         device bf16 [T, H, 64], strides (q_pe_stride_t, q_pe_stride_h)
+ * kv_c, k_pe   device bf16 [T, 512], [T, 64], token strides
+ * positions    device int64 [T]; one outside [0, max_positions) is clamped, and
+ *              sets MLA_DEVFLAG_POSITION unless the token is padding
+ * cos_sin      device fp32 [max_positions, 64], 16-byte aligned
+ * slot_mapping, num_tokens, num_heads, q_out, kv_cache, num_pages, page_size,
+ * kv_dtype, kv_scale, status   as mla_decode_epilogue; q_out is contiguous
+ * inputs_early 1: positions and slot_mapping are older than the kernel this
+ *              call is queued behind and are read before the dependency wait;
+ *              0: nothing is
+ * Returns MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (T * (H + 1) past
+ * 2^31 - 1) or MLA_ERR_CUDA.
+ */
+int mla_decode_rope_epilogue(const void* ql_nope, int64_t ql_stride_t, int64_t ql_stride_h,
+                             const void* q_pe, int64_t q_pe_stride_t, int64_t q_pe_stride_h,
+                             const void* kv_c, int64_t kv_c_stride, const void* k_pe,
+                             int64_t k_pe_stride, const int64_t* positions, const float* cos_sin,
+                             int64_t max_positions, int32_t interleaved,
+                             const int64_t* slot_mapping, int32_t num_tokens, int32_t num_heads,
+                             void* q_out, void* kv_cache, int64_t num_pages, int32_t page_size,
+                             int32_t kv_dtype, const float* kv_scale, int32_t inputs_early,
+                             int32_t* status, void* stream);
 
 /*
  * mla_decode_step -- one decode of the layer: mla_decode_epilogue for the

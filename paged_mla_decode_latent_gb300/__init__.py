@@ -8,13 +8,14 @@ the library is missing, every call raises.
 
 Names follow the C ABI: ``plan`` -> ``mla_decode_plan``, ``fwd`` ->
 ``mla_decode_fwd``, ``combine`` -> ``mla_decode_combine``, ``check`` ->
-``mla_decode_check``, ``epilogue`` -> ``mla_decode_epilogue``, ``step`` ->
+``mla_decode_check``, ``epilogue`` -> ``mla_decode_epilogue``,
+``rope_epilogue`` -> ``mla_decode_rope_epilogue``, ``step`` ->
 ``mla_decode_step``; the device-planned path: ``dplan_info``, ``plan_device``,
 ``fwd_dplan`` and ``combine_dplan``; ``gather_kv_b_proj`` ->
 ``mla_gather_kv_b_proj``; for a batch that shares a prefix: ``prefix_plan``,
-``prefix_fwd`` and ``prefix_check`` -> ``mla_decode_prefix_*``, and
-``decode_prefix``.  ``decode`` is plan + fwd + combine with freshly
-allocated outputs and workspace, for convenience.
+``prefix_fwd`` and ``prefix_check`` -> ``mla_decode_prefix_*``.  ``decode`` is
+plan + fwd + combine, and ``decode_prefix`` prefix_plan + prefix_fwd, with
+freshly allocated outputs and workspace, for convenience.
 """
 from __future__ import annotations
 
@@ -43,12 +44,13 @@ DEVFLAG_CTX_RANGE = 0x2
 DEVFLAG_TIMEOUT = 0x4
 DEVFLAG_Q_RANGE = 0x8
 DEVFLAG_KV_RANGE = 0x10
+DEVFLAG_POSITION = 0x20
 
 # Every symbol include/mla_decode.h declares.
 EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_fwd", "mla_decode_combine",
                     "mla_decode_check", "mla_decode_dplan_info", "mla_decode_plan_device",
                     "mla_decode_fwd_dplan", "mla_decode_combine_dplan", "mla_decode_epilogue",
-                    "mla_decode_step", "mla_gather_kv_b_proj", "mla_decode_fwd_noalloc",
+                    "mla_decode_rope_epilogue", "mla_decode_step", "mla_gather_kv_b_proj", "mla_decode_fwd_noalloc",
                     "mla_decode_prefix_plan", "mla_decode_prefix_fwd", "mla_decode_prefix_check",
                     "mla_status_string", "mla_decode_version")
 
@@ -147,6 +149,10 @@ def lib():
     L.mla_decode_step.argtypes = [P, vp, vp, vp, vp, vp, i32, vp, vp, i64, vp, vp, i64, vp, f32,
                                   vp, vp, vp, ctypes.c_size_t, vp]
     L.mla_decode_step.restype = ctypes.c_int
+    L.mla_decode_rope_epilogue.argtypes = [vp, i64, i64, vp, i64, i64, vp, i64, vp, i64, vp, vp,
+                                           i64, i32, vp, i32, i32, vp, vp, i64, i32, i32, vp, i32,
+                                           vp, vp]
+    L.mla_decode_rope_epilogue.restype = ctypes.c_int
     X = ctypes.POINTER(PrefixPlan)
     L.mla_decode_prefix_plan.argtypes = [vp, i32, i32, i32, i32, i32, i32, i32, i32, X]
     L.mla_decode_prefix_plan.restype = ctypes.c_int
@@ -176,6 +182,30 @@ def version() -> str:
 def _raise(st, where):
     if st != OK:
         raise MLADecodeError(st, where)
+
+
+def _is_fp8(cache):
+    import torch
+    return cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+
+
+def _expect(where, t, dtype, shape, strided=False):
+    """Refuses (ERR_INVALID_ARG) a tensor that is not what the C ABI reads: its dtype (a name, or
+    None), its shape (None: any extent), rows or all of it contiguous, the current CUDA device."""
+    import torch
+    if (t is not None and t.is_cuda and t.device.index == torch.cuda.current_device()
+            and (dtype is None or t.dtype == getattr(torch, dtype)) and t.dim() == len(shape)
+            and all(n is None or n == m for n, m in zip(shape, t.shape))
+            and (t.stride(-1) == 1 or t.shape[-1] == 1 if strided else t.is_contiguous())):
+        return
+    raise MLADecodeError(ERR_INVALID_ARG, where)
+
+
+def _row_stride(table):
+    """Elements between the rows of a block table (one row: its length)."""
+    if table is None:
+        return 0
+    return int(table.stride(0)) if table.shape[0] > 1 else int(table.shape[1])
 
 
 def _ptr(t):
@@ -299,6 +329,37 @@ def epilogue(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_cache, kv_scale=
     _raise(st, "mla_decode_epilogue")
 
 
+def rope_epilogue(ql_nope, q_pe, kv_c, k_pe, positions, cos_sin, slot_mapping, q_out, kv_cache,
+                  kv_scale=None, interleaved: bool = True, inputs_early: bool = False, status=None,
+                  stream=None) -> None:
+    """``mla_decode_rope_epilogue``: ``epilogue`` with the rope dims of q_pe and k_pe rotated by
+    their positions.  The four inputs may be strided views (last dimension contiguous)."""
+    where = "mla_decode_rope_epilogue"
+    T, H, _ = ql_nope.shape
+    fp8 = _is_fp8(kv_cache)
+    _expect(where, ql_nope, "bfloat16", (T, H, D_V), strided=True)
+    _expect(where, q_pe, "bfloat16", (T, H, 64), strided=True)
+    _expect(where, kv_c, "bfloat16", (T, D_V), strided=True)
+    _expect(where, k_pe, "bfloat16", (T, 64), strided=True)
+    _expect(where, positions, "int64", (T,))
+    _expect(where, cos_sin, "float32", (None, 64))
+    _expect(where, slot_mapping, "int64", (T,))
+    _expect(where, q_out, "bfloat16", (T, H, D_QK))
+    _expect(where, kv_cache, None if fp8 else "bfloat16", (None, None, D_QK))
+    if fp8:
+        _expect(where, kv_scale, "float32", (1,))
+    if status is not None:
+        _expect(where, status, "int32", (1,))
+    st = lib().mla_decode_rope_epilogue(
+        ql_nope.data_ptr(), ql_nope.stride(0), ql_nope.stride(1), q_pe.data_ptr(), q_pe.stride(0),
+        q_pe.stride(1), kv_c.data_ptr(), kv_c.stride(0), k_pe.data_ptr(), k_pe.stride(0),
+        positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], int(bool(interleaved)),
+        slot_mapping.data_ptr(), T, H, q_out.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
+        kv_cache.shape[1], KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale if fp8 else None),
+        int(bool(inputs_early)), _ptr(status), _stream(stream))
+    _raise(st, where)
+
+
 def step(p: Plan, ql_nope, q_pe, kv_c, k_pe, slot_mapping, q, kv_cache, kv_scale, block_table,
          seq_lens, softmax_scale: float, out, lse, workspace, cache_inputs_early: bool = False,
          stream=None) -> None:
@@ -337,13 +398,33 @@ def prefix_plan(seq_lens_host, prefix_len: int, num_heads: int, sq: int, page_si
 def prefix_fwd(p: PrefixPlan, q, kv_cache, kv_scale, prefix_table, block_table, seq_lens,
                softmax_scale: float, out, lse, workspace, stream=None) -> None:
     """``mla_decode_prefix_fwd``: the shared keys for all rows, each sequence's own keys, merged."""
+    where = "mla_decode_prefix_fwd"
+    B, Sq, H = p.batch, p.sq, p.num_heads
+    _expect(where, q, "bfloat16", (B, Sq, H, D_QK))
+    fp8 = p.kv_dtype == KV_FP8_E4M3
+    _expect(where, kv_cache, None if fp8 else "bfloat16", (None, p.page_size, D_QK))
+    if _is_fp8(kv_cache) != fp8:
+        raise MLADecodeError(ERR_INVALID_ARG, where)
+    if kv_scale is not None:
+        _expect(where, kv_scale, "float32", (1,))
+    if p.prefix_tiles:
+        _expect(where, prefix_table, "int32", (None,))
+        if prefix_table.shape[0] * p.page_size < p.prefix_len:
+            raise MLADecodeError(ERR_INVALID_ARG, where)
+    if p.own_splits:
+        _expect(where, block_table, "int32", (B, None), strided=True)
+        if block_table.shape[1] * p.page_size < p.max_ctx:
+            raise MLADecodeError(ERR_INVALID_ARG, where)
+    _expect(where, seq_lens, "int32", (B,))
+    _expect(where, out, "bfloat16", (B, Sq, H, D_V))
+    _expect(where, lse, "float32", (B, Sq, H))
+    _expect(where, workspace, None, (None,))
     st = lib().mla_decode_prefix_fwd(
         ctypes.byref(p), _ptr(q), _ptr(kv_cache), int(kv_cache.shape[0]), _ptr(kv_scale),
         _ptr(prefix_table), _ptr(block_table),
-        0 if block_table is None else int(block_table.stride(0)), _ptr(seq_lens),
-        float(softmax_scale), _ptr(out), _ptr(lse), _ptr(workspace), _ws_bytes(workspace),
-        _stream(stream))
-    _raise(st, "mla_decode_prefix_fwd")
+        _row_stride(block_table), _ptr(seq_lens), float(softmax_scale), _ptr(out), _ptr(lse),
+        _ptr(workspace), _ws_bytes(workspace), _stream(stream))
+    _raise(st, where)
 
 
 def prefix_check(p: PrefixPlan, workspace, stream=None) -> int:
