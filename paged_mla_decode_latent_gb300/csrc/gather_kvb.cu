@@ -402,10 +402,10 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-namespace mla {
+namespace {
 
-// No link-time dependency on the driver library: the entry point is looked up
-// through the runtime.
+// The driver's tensor-map encoder, looked up once through the runtime (no
+// link-time dependency on the driver library).
 PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   static std::once_flag once;
   static void* fn = nullptr;
@@ -419,18 +419,34 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder() {
   return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
 }
 
-bool tensor_map_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows,
-                     int cols, int box_rows) {
+bool encode_map(CUtensorMap* map, CUtensorMapDataType type, int rank, const void* base,
+                const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
   const PFN_cuTensorMapEncodeTiled_v12000 encode = tensor_map_encoder();
-  if (encode == nullptr) return false;
-  const cuuint64_t gdim[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
-  const cuuint64_t gstride[1] = {(cuuint64_t)cols * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
-  const cuuint32_t estride[2] = {1, 1};
-  return encode(map, type, 2, const_cast<void*>(base), gdim, gstride, box, estride,
+  const cuuint32_t step[3] = {1, 1, 1};
+  return encode != nullptr &&
+         encode(map, type, rank, const_cast<void*>(base), dims, strides, box, step,
                 CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace
+
+namespace mla {
+
+bool tensor_map_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows,
+                     int cols, int box_rows) {
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+  const cuuint64_t strides[1] = {(cuuint64_t)cols * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+  return encode_map(map, type, 2, base, dims, strides, box);
+}
+
+bool tensor_map_groups(CUtensorMap* map, const void* base, int64_t rows, int box_groups) {
+  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, kDQK / 64};
+  const cuuint64_t strides[2] = {kDQK * 2, 128};
+  const cuuint32_t box[3] = {64, 64, (cuuint32_t)box_groups};
+  return encode_map(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, base, dims, strides, box);
 }
 
 }  // namespace mla

@@ -3,7 +3,6 @@
 #pragma once
 
 #include <cuda.h>
-#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -95,17 +94,19 @@ struct PrefixParams {
   int prefix_len, max_ctx, tiles, pairs;
 };
 
-// The driver's tensor-map encoder, looked up once (nullptr if the driver has
-// none), and a 2-D 16-bit map of `rows` rows of `cols` elements read in boxes
-// of box_rows x 64 with the 128-byte swizzle.  False on failure.
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+// Tensor maps with the 128-byte swizzle; false on failure.  _rows: a 2-D
+// 16-bit map of `rows` rows of `cols` elements, in boxes of box_rows x 64.
+// _groups: f16 rows of 576 as [9 groups][rows][64], in boxes of box_groups x
+// 64 rows x 64.
 bool tensor_map_rows(CUtensorMap* map, CUtensorMapDataType type, const void* base, int64_t rows,
                      int cols, int box_rows);
+bool tensor_map_groups(CUtensorMap* map, const void* base, int64_t rows, int box_groups);
 
 }  // namespace mla
 
-int mla_launch_prefix_sm103(const mla::PrefixParams& p, const CUtensorMap& kmap,
-                            const CUtensorMap& qmap, void* stream);
+// keys: f16 [prefix_len, 576]; rows: f16 [p.rows, 576].
+int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, const void* rows,
+                            void* stream);
 
 // The few-row kernel (128-key tiles) takes problems of at most this many
 // score rows per sequence: 64 with a bf16 cache, 16 with fp8.

@@ -13,7 +13,6 @@
 //   own      the decode kernels over keys [P, ctx_b) of each sequence
 //   merge    the partials of a row -> out, lse
 
-#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -343,13 +342,6 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   float* pre_lse = reinterpret_cast<float*>(ws + plan->ws_prefix_lse_offset);
   float* own_o = reinterpret_cast<float*>(ws + plan->ws_own_o_offset);
   float* own_lse = reinterpret_cast<float*>(ws + plan->ws_own_lse_offset);
-  CUtensorMap kmap, qmap;
-  if (plan->prefix_tiles > 0 &&
-      (!mla::tensor_map_rows(&kmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + plan->ws_keys_offset,
-                             plan->prefix_len, MLA_D_QK, 64) ||
-       !mla::tensor_map_rows(&qmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, ws + plan->ws_q_offset,
-                             plan->total_rows, MLA_D_QK, 64)))
-    return MLA_ERR_CUDA;
   if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;
 
   if (plan->prefix_tiles > 0) {
@@ -387,7 +379,7 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
     p.max_ctx = plan->max_ctx;
     p.tiles = plan->prefix_tiles;
     p.pairs = plan->pairs;
-    if (mla_launch_prefix_sm103(p, kmap, qmap, stream) != 0) return MLA_ERR_CUDA;
+    if (mla_launch_prefix_sm103(p, g.k_out, g.q_out, stream) != 0) return MLA_ERR_CUDA;
   }
 
   if (plan->own_splits > 0) {

@@ -109,12 +109,18 @@ struct Ctx {
 };
 
 // True when the phase completed; false once any wait of this CTA has run out.
+// kCluster: the phase's arrivals come from threads of both CTAs.
+template <bool kCluster = false>
 __device__ __forceinline__ bool wait(const Ctx& c, uint32_t bar, uint32_t parity) {
-  if (ptx::mbar_try_wait_cluster(bar, parity, c.sleep_ns)) return true;
+  auto done = [&] {
+    return kCluster ? ptx::mbar_try_wait_cluster(bar, parity, c.sleep_ns)
+                    : ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns);
+  };
+  if (kCluster ? done() : ptx::mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
     if (*c.abort) return false;
-    if (ptx::mbar_try_wait_cluster(bar, parity, c.sleep_ns)) return true;
+    if (done()) return true;
     if (ptx::globaltimer_ns() - t0 > c.limit_ns) {
       atomicOr(c.status, MLA_DEVFLAG_TIMEOUT);
       *c.abort = 1;
@@ -165,13 +171,16 @@ struct Walk {
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_kernel(mla::PrefixParams p, const __grid_constant__ CUtensorMap kmap,
+                  const __grid_constant__ CUtensorMap vmap,
                   const __grid_constant__ CUtensorMap qmap) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem + OFF_BAR);
   const uint32_t sbase = ptx::smem_u32(smem);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // Through a shuffle, so that the compiler knows the warp index is uniform:
+  // the MMA and load loops then keep their addresses in uniform registers.
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = ptx::cluster_ctarank();
   const int pair = blockIdx.x >> 1;
 
@@ -198,123 +207,140 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::cluster_sync_all();  // both CTAs' barriers are initialised before any remote arrive
   ptx::tc_fence_after();
   ptx::grid_dependency_wait();
-  const uint32_t tmem = bars.tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
   Ctx c{p.status, &bars.abort, p.wait_ns,
         (uint32_t)(p.wait_ns < (uint64_t)kSleepNs ? p.wait_ns : (uint64_t)kSleepNs)};
   Walk w(p, pair);
 
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------- loads ---
-    if (lane == 0) {
-      int slot = 0, issued = 0;
-      uint32_t ph = 1;  // a fresh barrier passes the wait for the phase before its first
-      bool ok = true;
-      auto slab = [&](int x0, int y0, int x1, int y1) {
-        ok = ok && wait(c, ptx::smem_u32(&bars.empty[slot]), ph);
-        if (!ok) return;
-        const uint32_t bar = ptx::mapa(ptx::smem_u32(&bars.full[slot]), 0);
-        if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars.full[slot]), 2 * SLAB);
-        const uint32_t dst = sbase + OFF_RING + slot * SLAB;
-        ptx::tma_load_2d_pair(dst, &kmap, x0, y0, bar);
-        ptx::tma_load_2d_pair(dst + SLAB / 2, &kmap, x1, y1, bar);
-        ++issued;
-        if (++slot == kSlots) {
-          slot = 0;
-          ph ^= 1u;
-        }
-      };
-      auto scores = [&](int t) {
-        const int y = t * T + 128 * (int)rank;
-        for (int d = 0; d < 9; ++d) slab(64 * d, y, 64 * d, y + 64);
-      };
-      for (int seg = 0; w.next(); ++seg) {
-        if (seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.q_empty), (seg - 1) & 1);
-        if (ok) {
-          if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars.q_full), 2 * 9 * QSLAB);
-          const uint32_t bar = ptx::mapa(ptx::smem_u32(&bars.q_full), 0);
-          for (int d = 0; d < 9; ++d)
-            ptx::tma_load_2d_pair(sbase + OFF_Q + d * QSLAB, &qmap, 64 * d,
-                                  w.rb * mla::kRowTile + 64 * (int)rank, bar);
-        }
-        scores(w.t0);
-        for (int t = w.t0; t < w.t1; ++t) {
-          if (t + 1 < w.t1) scores(t + 1);
-          for (int kg = 0; kg < 4; ++kg)
-            for (int j = 0; j < 2; ++j) {
-              const int x = 256 * (int)rank + 128 * j;
-              slab(x, t * T + 64 * kg, x + 64, t * T + 64 * kg);
-            }
+    // The whole warp walks the slabs (uniform control flow), one lane issues.
+    const bool leader = ptx::elect_one();
+    const uint32_t full0 = ptx::mapa(ptx::smem_u32(&bars.full[0]), 0);
+    const uint32_t full_own = ptx::smem_u32(&bars.full[0]), empty_own = ptx::smem_u32(&bars.empty[0]);
+    int slot = 0, issued = 0;
+    uint32_t ph = 1;  // a fresh barrier passes the wait for the phase before its first
+    bool ok = true;
+    auto reserve = [&] {
+      ok = ok && wait(c, empty_own + 8 * slot, ph);
+      if (ok && leader && rank == 0) ptx::mbar_arrive_expect_tx(full_own + 8 * slot, 2 * SLAB);
+    };
+    auto advance = [&] {
+      issued += ok;
+      if (++slot == kSlots) {
+        slot = 0;
+        ph ^= 1u;
+      }
+    };
+    auto scores = [&](int t) {
+      const int y = t * T + 128 * (int)rank;
+      for (int d = 0; d < 9; ++d) {
+        reserve();
+        if (ok && leader)
+          ptx::tma_load_2d_pair(sbase + OFF_RING + slot * SLAB, &kmap, 64 * d, y, full0 + 8 * slot);
+        advance();
+      }
+    };
+    for (int seg = 0; w.next(); ++seg) {
+      if (seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.q_empty), (seg - 1) & 1);
+      if (ok && leader) {
+        if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars.q_full), 2 * 9 * QSLAB);
+        const uint32_t bar = ptx::mapa(ptx::smem_u32(&bars.q_full), 0);
+        for (int d = 0; d < 9; d += 3)
+          ptx::tma_load_3d_pair(sbase + OFF_Q + d * QSLAB, &qmap, 0,
+                                w.rb * mla::kRowTile + 64 * (int)rank, d, bar);
+      }
+      scores(w.t0);
+      for (int t = w.t0; t < w.t1; ++t) {
+        if (t + 1 < w.t1) scores(t + 1);
+        for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, dims 128 (v % 2) of the CTA's half
+          reserve();
+          if (ok && leader)
+            ptx::tma_load_3d_pair(sbase + OFF_RING + slot * SLAB, &vmap, 0, t * T + 64 * (v >> 1),
+                                  4 * (int)rank + 2 * (v & 1), full0 + 8 * slot);
+          advance();
         }
       }
-      // After a wait ran out, copies may still be landing: the even CTA, whose
-      // barriers count both CTAs' bytes, waits for the last ones.
-      if (!ok && rank == 0) {
-        const uint64_t start = ptx::globaltimer_ns();
-        for (int i = max(0, issued - kSlots); i < issued; ++i)
-          while (!ptx::mbar_try_wait(ptx::smem_u32(&bars.full[i % kSlots]), (i / kSlots) & 1))
-            if (ptx::globaltimer_ns() - start > kDrainNs) break;
-      }
+    }
+    // After a wait ran out, copies may still be landing: the even CTA, whose
+    // barriers count both CTAs' bytes, waits for the last ones.
+    if (!ok && rank == 0 && leader) {
+      const uint64_t start = ptx::globaltimer_ns();
+      for (int i = max(0, issued - kSlots); i < issued; ++i)
+        while (!ptx::mbar_try_wait(full_own + 8 * (i % kSlots), (i / kSlots) & 1))
+          if (ptx::globaltimer_ns() - start > kDrainNs) break;
     }
     __syncwarp();
   } else if (warp == kMmaWarp) {
     // ---------------------------------------------------------------- MMA ---
-    if (lane == 0 && rank == 0) {
-      const uint32_t id_qk = ptx::idesc_f16(128, T, 0u, false, false);
-      const uint32_t id_pv = ptx::idesc_f16(128, 256, 0u, false, true);
+    // The whole warp walks the slabs of the even CTA, one lane issues.  A slab
+    // is 256 cycles of MMAs, so what the loop does between two slabs' MMAs is
+    // kept short: the next slab's barrier is tried while they run.
+    if (rank == 0) {
+      const bool leader = ptx::elect_one();
+      constexpr uint32_t id_qk = ptx::idesc_f16(128, T, 0u, false, false);
+      constexpr uint32_t id_pv = ptx::idesc_f16(128, 256, 0u, false, true);
       // A slab, a 32-byte step of 16 dims or a 2 KB step of 16 keys is an add
       // to the descriptor's start address (16-byte units, no carry).
       const uint64_t dq = kdesc(sbase + OFF_Q), dp = kdesc(sbase + OFF_P);
       const uint64_t dk = kdesc(sbase + OFF_RING), dv = vdesc(sbase + OFF_RING);
+      const uint32_t full0 = ptx::smem_u32(&bars.full[0]), empty0 = ptx::smem_u32(&bars.empty[0]);
       bool ok = true;
+      bool ready = false;  // the current slab has landed
       int slot = 0;
       uint32_t ph = 0;
       uint32_t it = 0;  // tiles whose scores this pair has issued, over all segments
+      auto take = [&] {  // the current slab
+        if (!ready) ok = ok && wait(c, full0 + 8 * slot, ph);
+        ptx::tc_fence_after();
+      };
       auto advance = [&] {
-        ptx::mma_commit_pair(ptx::smem_u32(&bars.empty[slot]));
+        if (leader) ptx::mma_commit_pair(empty0 + 8 * slot);
         if (++slot == kSlots) {
           slot = 0;
           ph ^= 1u;
         }
+        ready = ptx::mbar_test_wait(full0 + 8 * slot, ph);
       };
       auto values = [&](uint32_t i, bool first) {
-        ok = ok && wait(c, ptx::smem_u32(&bars.p_full), i & 1);
-        for (int kg = 0; kg < 4 && ok; ++kg)
-          for (int j = 0; j < 2 && ok; ++j) {
-            ok = wait(c, ptx::smem_u32(&bars.full[slot]), ph);
-            if (!ok) break;
-            ptx::tc_fence_after();
+        ok = ok && wait<true>(c, ptx::smem_u32(&bars.p_full), i & 1);
+        for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, O columns 128 (v % 2)
+          take();
+          if (leader && ok) {
 #pragma unroll
             for (int k = 0; k < 4; ++k)
-              ptx::mma_ss_pair(tmem + TM_O + 128 * j, dp + kg * (PSLAB >> 4) + 2 * k,
+              ptx::mma_ss_pair(tmem + TM_O + 128 * (v & 1), dp + (v >> 1) * (PSLAB >> 4) + 2 * k,
                                dv + slot * (SLAB >> 4) + k * (2048 >> 4), id_pv,
-                               !(first && kg == 0 && k == 0));
-            advance();
+                               !(first && v < 2 && k == 0));
           }
-        if (ok) ptx::mma_commit_pair(ptx::smem_u32(&bars.o_done));
+          advance();
+        }
+        if (leader) ptx::mma_commit_pair(ptx::smem_u32(&bars.o_done));
       };
-      for (int seg = 0; ok && w.next(); ++seg) {
-        ok = wait(c, ptx::smem_u32(&bars.q_full), seg & 1);
+      for (int seg = 0; w.next(); ++seg) {
+        ok = ok && wait(c, ptx::smem_u32(&bars.q_full), seg & 1);
         const int n = w.t1 - w.t0;
-        for (int t = 0; t < n && ok; ++t) {
-          for (int d = 0; d < 9 && ok; ++d) {
-            ok = wait(c, ptx::smem_u32(&bars.full[slot]), ph);
-            if (!ok) break;
-            ptx::tc_fence_after();
+        for (int t = 0; t < n; ++t) {
+          for (int d = 0; d < 9; ++d) {
+            take();
+            if (leader && ok) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-              ptx::mma_ss_pair(tmem + TM_S + 128 * (it & 1), dq + d * (QSLAB >> 4) + 2 * k,
-                               dk + slot * (SLAB >> 4) + 2 * k, id_qk, (d | k) != 0);
+              for (int k = 0; k < 4; ++k)
+                ptx::mma_ss_pair(tmem + TM_S + 128 * (it & 1), dq + d * (QSLAB >> 4) + 2 * k,
+                                 dk + slot * (SLAB >> 4) + 2 * k, id_qk, (d | k) != 0);
+            }
             advance();
           }
-          if (!ok) break;
-          ptx::mma_commit_pair(ptx::smem_u32(&bars.s_full[it & 1]));
-          if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
+          if (leader) {
+            ptx::mma_commit_pair(ptx::smem_u32(&bars.s_full[it & 1]));
+            if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
+          }
           ++it;
-          if (t == 1 && seg > 0) ok = wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
+          if (t == 1 && seg > 0) ok = ok && wait<true>(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
           if (t > 0) values(it - 2, t == 1);
         }
-        if (n == 1 && seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
-        if (ok) values(it - 1, n == 1);
+        if (n == 1 && seg > 0) ok = ok && wait<true>(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
+        values(it - 1, n == 1);
       }
     }
     __syncwarp();
@@ -485,8 +511,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-int mla_launch_prefix_sm103(const mla::PrefixParams& p, const CUtensorMap& kmap,
-                            const CUtensorMap& qmap, void* stream) {
+int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, const void* rows,
+                            void* stream) {
+  // Score slabs: 128 keys x 64 dims.  Value slabs: 64 keys x 2 x 64 dims and
+  // query slabs: 64 rows x 3 x 64 dims, the 64-dim groups of a row as a third
+  // dimension, so that one copy fills a slab group by group.
+  CUtensorMap kmap, vmap, qmap;
+  if (!mla::tensor_map_rows(&kmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, keys, p.prefix_len, mla::kDQK, 128) ||
+      !mla::tensor_map_groups(&vmap, keys, p.prefix_len, 2) ||
+      !mla::tensor_map_groups(&qmap, rows, p.rows, 3))
+    return (int)cudaErrorUnknown;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
@@ -502,5 +536,5 @@ int mla_launch_prefix_sm103(const mla::PrefixParams& p, const CUtensorMap& kmap,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, prefix_kernel, p, kmap, qmap);
+  return (int)cudaLaunchKernelEx(&cfg, prefix_kernel, p, kmap, vmap, qmap);
 }
