@@ -108,25 +108,26 @@ struct Ctx {
   uint32_t sleep_ns;
 };
 
-// True when the phase completed; false once any wait of this CTA has run out.
-// kCluster: the phase's arrivals come from threads of both CTAs.
-template <bool kCluster = false>
-__device__ __forceinline__ bool wait(const Ctx& c, uint32_t bar, uint32_t parity) {
-  auto done = [&] {
-    return kCluster ? ptx::mbar_try_wait_cluster(bar, parity, c.sleep_ns)
-                    : ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns);
-  };
-  if (kCluster ? done() : ptx::mbar_try_wait(bar, parity)) return true;
+// The rest of a wait whose first sleep passed in vain: the timer and the abort
+// word.  Out of line, so that the loops around the waits stay short (with this
+// inlined and the slab loops unrolled they ran from the instruction cache's
+// misses: 136 against 107 us at batch 64 x 8192).
+__device__ __noinline__ bool wait_slow(const Ctx& c, uint32_t bar, uint32_t parity) {
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
     if (*c.abort) return false;
-    if (done()) return true;
+    if (ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns)) return true;
     if (ptx::globaltimer_ns() - t0 > c.limit_ns) {
       atomicOr(c.status, MLA_DEVFLAG_TIMEOUT);
       *c.abort = 1;
       return false;
     }
   }
+}
+
+// True when the phase completed; false once any wait of this CTA has run out.
+__device__ __forceinline__ bool wait(const Ctx& c, uint32_t bar, uint32_t parity) {
+  return ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns) || wait_slow(c, bar, parity);
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -234,6 +235,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     auto scores = [&](int t) {
       const int y = t * T + 128 * (int)rank;
+#pragma unroll 1
       for (int d = 0; d < 9; ++d) {
         reserve();
         if (ok && leader)
@@ -253,6 +255,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       scores(w.t0);
       for (int t = w.t0; t < w.t1; ++t) {
         if (t + 1 < w.t1) scores(t + 1);
+#pragma unroll 1
         for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, dims 128 (v % 2) of the CTA's half
           reserve();
           if (ok && leader)
@@ -286,13 +289,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t dk = kdesc(sbase + OFF_RING), dv = vdesc(sbase + OFF_RING);
       const uint32_t full0 = ptx::smem_u32(&bars.full[0]), empty0 = ptx::smem_u32(&bars.empty[0]);
       bool ok = true;
-      bool ready = false;  // the current slab has landed
+      bool ready = false, next = false;  // the current slab, the one after it has landed
       int slot = 0;
       uint32_t ph = 0;
       uint32_t it = 0;  // tiles whose scores this pair has issued, over all segments
       auto take = [&] {  // the current slab
         if (!ready) ok = ok && wait(c, full0 + 8 * slot, ph);
         ptx::tc_fence_after();
+        const bool wrap = slot == kSlots - 1;
+        next = ptx::mbar_test_wait(wrap ? full0 : full0 + 8 * (slot + 1), wrap ? ph ^ 1u : ph);
       };
       auto advance = [&] {
         if (leader) ptx::mma_commit_pair(empty0 + 8 * slot);
@@ -300,10 +305,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           slot = 0;
           ph ^= 1u;
         }
-        ready = ptx::mbar_test_wait(full0 + 8 * slot, ph);
+        ready = next;
       };
       auto values = [&](uint32_t i, bool first) {
-        ok = ok && wait<true>(c, ptx::smem_u32(&bars.p_full), i & 1);
+        ok = ok && wait(c, ptx::smem_u32(&bars.p_full), i & 1);
+#pragma unroll 1
         for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, O columns 128 (v % 2)
           take();
           if (leader && ok) {
@@ -321,6 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ok = ok && wait(c, ptx::smem_u32(&bars.q_full), seg & 1);
         const int n = w.t1 - w.t0;
         for (int t = 0; t < n; ++t) {
+#pragma unroll 1
           for (int d = 0; d < 9; ++d) {
             take();
             if (leader && ok) {
@@ -336,10 +343,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
           }
           ++it;
-          if (t == 1 && seg > 0) ok = ok && wait<true>(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
+          if (t == 1 && seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
           if (t > 0) values(it - 2, t == 1);
         }
-        if (n == 1 && seg > 0) ok = ok && wait<true>(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
+        if (n == 1 && seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
         values(it - 1, n == 1);
       }
     }
@@ -467,21 +474,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int first = mla::prefix_pair_of(p.total_tiles, p.pairs, (int64_t)w.rb * p.tiles);
       const size_t slot = (size_t)(pair - first) * p.rows + row;
       const float inv = l > 0.f ? s_kv / l : 0.f;
-      const bool write = good && row < p.rows;
+      // A thread holds one row, so 32 columns at a time go through the warp's
+      // 4 KB of the weights' buffer (read by now), 16-byte chunks swizzled by the
+      // row, and leave as 128-byte pieces of rows: written straight from the
+      // registers, every store touched 32 lines (11 us a segment instead of 3).
+      const uint32_t stage = p_row - lane * 128;  // where this warp writes its weights
+      const int row0 = w.rb * mla::kRowTile + 64 * (int)rank + 32 * (q4 & 1);  // the warp's first
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t o[32];
         ptx::tmem_ld32(tmem + lanes + TM_O + 128 * ch + 32 * cc, o);
         ptx::tmem_ld_wait();
-        if (write) {
-          float4* dst = reinterpret_cast<float4*>(p.part_o + slot * mla::kDV + dim0 + 32 * cc);
 #pragma unroll
-          for (int v = 0; v < 8; ++v)
-            dst[v] = make_float4(__uint_as_float(o[4 * v]) * inv, __uint_as_float(o[4 * v + 1]) * inv,
-                                 __uint_as_float(o[4 * v + 2]) * inv, __uint_as_float(o[4 * v + 3]) * inv);
+        for (int v = 0; v < 8; ++v)
+          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
+                           stage + lane * 128 + ((v ^ (lane & 7)) * 16)),
+                       "f"(__uint_as_float(o[4 * v]) * inv), "f"(__uint_as_float(o[4 * v + 1]) * inv),
+                       "f"(__uint_as_float(o[4 * v + 2]) * inv), "f"(__uint_as_float(o[4 * v + 3]) * inv)
+                       : "memory");
+        __syncwarp();
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const int rr = 4 * v + (lane >> 3), c8 = lane & 7;
+          float4 x;
+          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
+                       : "r"(stage + rr * 128 + ((c8 ^ (rr & 7)) * 16))
+                       : "memory");
+          if (good && row0 + rr < p.rows)
+            *reinterpret_cast<float4*>(p.part_o + ((size_t)(pair - first) * p.rows + row0 + rr) * mla::kDV +
+                                       dim0 + 32 * cc + 4 * c8) = x;
         }
+        __syncwarp();
       }
-      if (write && kg == 0)
+      if (good && row < p.rows && kg == 0)
         p.part_lse[slot] = l > 0.f ? (m - kHead + log2f(l)) * 0.6931471805599453f : -INFINITY;
       ptx::tc_fence_before();
       __syncwarp();
