@@ -182,7 +182,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // Through a shuffle, so that the compiler knows the warp index is uniform:
   // the MMA and load loops then keep their addresses in uniform registers.
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-  const uint32_t rank = ptx::cluster_ctarank();
+  const uint32_t rank = blockIdx.x & 1;  // the CTA's rank in its cluster, as a uniform value
   const int pair = blockIdx.x >> 1;
 
   if (threadIdx.x == 0) {
@@ -217,7 +217,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // -------------------------------------------------------------- loads ---
     // The whole warp walks the slabs (uniform control flow), one lane issues.
     const bool leader = ptx::elect_one();
-    const uint32_t full0 = ptx::mapa(ptx::smem_u32(&bars.full[0]), 0);
+    const uint32_t full0 = __shfl_sync(0xffffffffu, ptx::mapa(ptx::smem_u32(&bars.full[0]), 0), 0);
     const uint32_t full_own = ptx::smem_u32(&bars.full[0]), empty_own = ptx::smem_u32(&bars.empty[0]);
     int slot = 0, issued = 0;
     uint32_t ph = 1;  // a fresh barrier passes the wait for the phase before its first
@@ -326,28 +326,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int seg = 0; w.next(); ++seg) {
         ok = ok && wait(c, ptx::smem_u32(&bars.q_full), seg & 1);
         const int n = w.t1 - w.t0;
-        for (int t = 0; t < n; ++t) {
+        for (int t = 0; t <= n; ++t) {
+          if (t < n) {
 #pragma unroll 1
-          for (int d = 0; d < 9; ++d) {
-            take();
-            if (leader && ok) {
+            for (int d = 0; d < 9; ++d) {
+              take();
+              if (leader && ok) {
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                ptx::mma_ss_pair(tmem + TM_S + 128 * (it & 1), dq + d * (QSLAB >> 4) + 2 * k,
-                                 dk + slot * (SLAB >> 4) + 2 * k, id_qk, (d | k) != 0);
+                for (int k = 0; k < 4; ++k)
+                  ptx::mma_ss_pair(tmem + TM_S + 128 * (it & 1), dq + d * (QSLAB >> 4) + 2 * k,
+                                   dk + slot * (SLAB >> 4) + 2 * k, id_qk, (d | k) != 0);
+              }
+              advance();
             }
-            advance();
+            if (leader) {
+              ptx::mma_commit_pair(ptx::smem_u32(&bars.s_full[it & 1]));
+              if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
+            }
+            ++it;
           }
-          if (leader) {
-            ptx::mma_commit_pair(ptx::smem_u32(&bars.s_full[it & 1]));
-            if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
-          }
-          ++it;
+          if (t == 0) continue;
+          // O is free once the segment before is read.
           if (t == 1 && seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
-          if (t > 0) values(it - 2, t == 1);
+          values(it - 1 - (t < n), t == 1);
         }
-        if (n == 1 && seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
-        values(it - 1, n == 1);
       }
     }
     __syncwarp();
