@@ -497,11 +497,11 @@ int mla_decode_fwd_noalloc(const mla_decode_plan_t* plan, const void* q, const v
  * sequence's own copy of the page, of which only the slots from prefix_len %
  * page_size on are read.
  *
- * The shared rows and the query rows are staged in f16 (exact for bf16 and
- * e4m3 values of magnitude 2^-14 to 65504, to 2^-25 below that); larger or
- * non-finite values set MLA_DEVFLAG_KV_RANGE / MLA_DEVFLAG_Q_RANGE, and the
- * rows that use them are undefined.  A non-finite shared key also spoils the
- * rows of sequences too short to see it.
+ * Keys and query rows are staged in f16 (exact for bf16 and e4m3 values of
+ * magnitude 2^-14 to 65504, to 2^-25 below that).  A larger or non-finite key
+ * sets MLA_DEVFLAG_KV_RANGE, and the rows that see it come out NaN; such a
+ * query value sets MLA_DEVFLAG_Q_RANGE and spoils its row.  (Long own keys are
+ * read as they are, by the kernels of mla_decode_fwd, and follow its rules.)
  */
 typedef struct mla_decode_prefix_plan_t {
   int32_t version;       /* MLA_DECODE_PREFIX_PLAN_VERSION */
@@ -513,18 +513,21 @@ typedef struct mla_decode_prefix_plan_t {
   int32_t num_sms;       /* SM count the partition was balanced for */
   int32_t row_blocks;    /* ceil(total_rows / 128) */
   int32_t prefix_tiles;  /* ceil(prefix_len / 256) */
-  int32_t pairs;         /* CTA pairs that share row_blocks * prefix_tiles tiles */
-  int32_t prefix_slots;  /* most partials a row gets from the shared keys */
+  int32_t pairs;         /* CTA pairs that share the tiles of all row blocks */
+  int32_t own_folded;    /* 1: a sequence's own keys are further tiles of its row blocks */
+  int32_t block_keys;    /* own keys that a row block has room for, when folded */
   int32_t key_tile;      /* of the own keys' decode, as mla_decode_plan_t */
-  int32_t own_chunk;     /* keys per split of a sequence's own keys */
-  int32_t own_splits;    /* splits of the longest sequence's own keys (0: none has any) */
+  int32_t own_chunk;     /* keys per split of a sequence's own keys, when not folded */
+  int32_t own_splits;    /* splits of the longest sequence's own keys (0: folded, or none) */
   int32_t wait_limit_us; /* as mla_decode_plan_t: 0 = 2 s; the one field a caller may set */
-  int64_t ws_status_offset;     /* int32 status word */
-  int64_t ws_keys_offset;       /* f16 [prefix_len, 576] */
+  int32_t reserved0;
+  int64_t ws_status_offset;     /* int32 status word [4], int32 [B + 1] */
+  int64_t ws_partition_offset;  /* the device's partition of the tiles */
+  int64_t ws_keys_offset;       /* f16 [256 prefix_tiles + row_blocks * block_keys, 576] */
   int64_t ws_q_offset;          /* f16 [total_rows, 576] */
-  int64_t ws_prefix_o_offset;   /* fp32 [prefix_slots, total_rows, 512] */
-  int64_t ws_prefix_lse_offset; /* fp32 [prefix_slots, total_rows] */
-  int64_t ws_own_o_offset;      /* fp32 [B, own_splits, rows, 512] */
+  int64_t ws_prefix_o_offset;   /* fp32 [row_blocks + pairs, 128, 512] partials */
+  int64_t ws_prefix_lse_offset; /* fp32 [row_blocks + pairs, 128] */
+  int64_t ws_own_o_offset;      /* fp32 [B, own_splits, rows, 512] partials */
   int64_t ws_own_lse_offset;    /* fp32 [B, own_splits, rows] */
   int64_t workspace_bytes;
 } mla_decode_prefix_plan_t;
@@ -549,7 +552,7 @@ int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batch, int32_t 
  *                 keys' pages (a row of block_table serves, if that sequence
  *                 holds the whole prefix).  NULL allowed when prefix_len is 0.
  *   block_table   entries before prefix_len / page_size are never read.  NULL
- *                 allowed when plan->own_splits is 0.
+ *                 allowed when plan->max_ctx <= prefix_len.
  *   softmax_scale >= 0
  * Page ids and contexts out of range are clamped and flagged as in
  * mla_decode_fwd.  Resets the status word first.  The workspace (256-byte

@@ -87,9 +87,10 @@ class PrefixPlan(ctypes.Structure):
     _fields_ = [(n, ctypes.c_int32) for n in (
         "version", "batch", "num_heads", "sq", "page_size", "kv_dtype", "causal", "rows",
         "total_rows", "prefix_len", "max_ctx", "num_sms", "row_blocks", "prefix_tiles", "pairs",
-        "prefix_slots", "key_tile", "own_chunk", "own_splits", "wait_limit_us")] + [
+        "own_folded", "block_keys", "key_tile", "own_chunk", "own_splits", "wait_limit_us",
+        "reserved0")] + [
         (n, ctypes.c_int64) for n in (
-            "ws_status_offset", "ws_keys_offset", "ws_q_offset", "ws_prefix_o_offset",
+            "ws_status_offset", "ws_partition_offset", "ws_keys_offset", "ws_q_offset", "ws_prefix_o_offset",
             "ws_prefix_lse_offset", "ws_own_o_offset", "ws_own_lse_offset", "workspace_bytes")]
 
     def as_dict(self):
@@ -411,7 +412,7 @@ def prefix_fwd(p: PrefixPlan, q, kv_cache, kv_scale, prefix_table, block_table, 
         _expect(where, prefix_table, "int32", (None,))
         if prefix_table.shape[0] * p.page_size < p.prefix_len:
             raise MLADecodeError(ERR_INVALID_ARG, where)
-    if p.own_splits:
+    if p.max_ctx > p.prefix_len:
         _expect(where, block_table, "int32", (B, None), strided=True)
         if block_table.shape[1] * p.page_size < p.max_ctx:
             raise MLADecodeError(ERR_INVALID_ARG, where)

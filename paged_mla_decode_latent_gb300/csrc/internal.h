@@ -68,10 +68,9 @@ struct CombineParams {
 
 // ---------------------------------------------------------- shared prefix ---
 
-constexpr int kPrefixTile = 256;  // shared keys per tile
+constexpr int kPrefixTile = 256;  // keys per tile
 
-// The tiles of all row blocks, row block by row block, dealt to the CTA pairs
-// in equal contiguous shares: pair i takes [share(i), share(i + 1)).
+// A pair's share of `total` tiles: [share(i), share(i + 1)).
 __host__ __device__ inline int64_t prefix_share(int64_t total, int pairs, int i) {
   return total * i / pairs;
 }
@@ -80,18 +79,61 @@ __host__ __device__ inline int prefix_pair_of(int64_t total, int pairs, int64_t 
   return (int)(((x + 1) * pairs - 1) / total);
 }
 
-// The shared-prefix pass: all rows of the batch against the shared keys.
-struct PrefixParams {
-  const float* kv_scale;    // device fp32[1], or nullptr (bf16 cache)
+// What the staging, the attention and the merge of a shared-prefix call know
+// of its rows, keys and partition.
+struct PrefixShape {
   const int32_t* seq_lens;  // [B]
-  float* part_o;            // fp32 [slots, rows, 512]
-  float* part_lse;          // fp32 [slots, rows]
+  int64_t* first_tile;      // [row blocks + 1]: the tiles before each row block
+  int2* pair_start;         // [pairs]: row block and tile at which a pair starts
+  int32_t* own_off;         // [row blocks, block_seqs]: a sequence's first own key in its block's
+  // [B + 1]: 2^31 - 1 - (first key of the sequence's own, and of the shared
+  // ones, that f16 cannot hold); 0: none
+  int32_t* bad;
   int32_t* status;
+  int rows, rows_per_seq, heads, sq, causal, batch;
+  int prefix_len, max_ctx;
+  int tiles;       // of the shared keys
+  int pairs, row_blocks;
+  int fold;        // own keys are further tiles of each row block
+  int block_seqs;  // most sequences with rows in one row block
+  int block_keys;  // own keys that a row block's region holds (a multiple of the tile)
+
+#ifdef __CUDACC__
+  __device__ __forceinline__ int context(int b) const {
+    const int ctx = seq_lens[b];
+    return ctx < 0 ? 0 : min(ctx, max_ctx);
+  }
+  __device__ __forceinline__ int own(int b) const { return max(0, context(b) - prefix_len); }
+  // Keys that row r (of sequence b) sees.
+  __device__ __forceinline__ int visible(int r, int b) const {
+    const int ctx = context(b);
+    const int tok = (r - b * rows_per_seq) / heads;
+    return causal ? max(0, min(ctx, ctx - sq + tok + 1)) : ctx;
+  }
+  // Whether one of them is a key that f16 cannot hold.
+  __device__ __forceinline__ bool sees_bad(int b, int n) const {
+    return n > 0x7FFFFFFF - max(bad[b], bad[batch]);
+  }
+  __device__ __forceinline__ int first_seq(int block) const {
+    return (int)((int64_t)block * kRowTile / rows_per_seq);
+  }
+  __device__ __forceinline__ int last_seq(int block) const {
+    const int64_t r = (int64_t)(block + 1) * kRowTile - 1;
+    return (int)((r < rows ? r : rows - 1) / rows_per_seq);
+  }
+#endif
+};
+
+struct PrefixParams {
+  PrefixShape g;
+  const float* kv_scale;  // device fp32[1], or nullptr (bf16 cache)
+  uint16_t* out;          // bf16 [rows, 512] and [rows]: row blocks that one pair holds
+  float* lse;
+  float* part_o;          // fp32 [row blocks + pairs, 128, 512]: segment pair + row block
+  float* part_lse;        // fp32 [row blocks + pairs, 128]
   uint64_t wait_ns;
-  int64_t total_tiles;      // row blocks * tiles
   float softmax_scale;
-  int rows, rows_per_seq, heads, sq, causal;
-  int prefix_len, max_ctx, tiles, pairs;
+  int partials;           // every row block writes partials (something else is merged in)
 };
 
 // Tensor maps with the 128-byte swizzle; false on failure.  _rows: a 2-D
@@ -104,9 +146,10 @@ bool tensor_map_groups(CUtensorMap* map, const void* base, int64_t rows, int box
 
 }  // namespace mla
 
-// keys: f16 [prefix_len, 576]; rows: f16 [p.rows, 576].
-int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, const void* rows,
-                            void* stream);
+// keys: f16 [key_rows, 576], the shared keys' tiles, then each row block's own;
+// rows: f16 [p.g.rows, 576].
+int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, int64_t key_rows,
+                            const void* rows, void* stream);
 
 // The few-row kernel (128-key tiles) takes problems of at most this many
 // score rows per sequence: 64 with a bf16 cache, 16 with fp8.

@@ -1,17 +1,16 @@
 // prefix.cu -- decode attention for a batch that shares a prefix: the plan,
-// the staging of the shared keys, the merge and the entry points.
+// the staging of keys and queries, the merge and the entry points.
 //
 // With P shared keys, sequence b's query rows attend to the shared keys and to
-// its own keys [P, ctx_b); one softmax over both is the log-sum-exp merge of
-// the two parts' partials:
-//   L = ln sum_s e^lse_s,   out = sum_s e^(lse_s - L) o_s.
-//
-// One call queues:
-//   stage    shared keys (through prefix_table) and the query rows -> f16 rows
-//            in the workspace
-//   prefix   prefix_sm103.cu: all rows of the batch against the shared keys
-//   own      the decode kernels over keys [P, ctx_b) of each sequence
-//   merge    the partials of a row -> out, lse
+// its own keys [P, ctx_b) under one softmax.  One call queues:
+//   stage   shared keys (through prefix_table), query rows and, where they are
+//           folded in, the own keys -> f16 rows in the workspace; the
+//           partition of the tiles over the CTA pairs
+//   prefix  prefix_sm103.cu
+//   own     where they are not folded in: the decode kernels over keys [P,
+//           ctx_b) of each sequence
+//   merge   the partials of a row:
+//             L = ln sum_s e^lse_s,   out = sum_s e^(lse_s - L) o_s
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -31,183 +30,416 @@ namespace {
 
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 constexpr int kPieces = 72;  // 8-element pieces of a 576-wide row
-constexpr int kStageThreads = 256;
 constexpr int kMaxPairs = 256;
-constexpr int kMaxParts = kMaxPairs + mla::kMaxSplits;  // partials of a row
+constexpr int kChunk = 32;  // rows a staging CTA copies
+constexpr int kStageThreads = 256;
+constexpr int kStageIters = kChunk * kPieces / kStageThreads;  // 9 pieces a thread
+constexpr int kPadChunks = mla::kPrefixTile / kChunk;
+constexpr int64_t kMaxOwnRows = 1 << 18;  // own keys that are folded in at most (302 MB staged)
 
 struct StageParams {
+  mla::PrefixShape g;
   const void* cache;
   int64_t num_pages;
-  const int32_t* table;
+  const int32_t* prefix_table;
+  const int32_t* block_table;
+  int64_t bt_stride;
   const uint16_t* q;
-  uint16_t* k_out;  // f16 [prefix_len, 576]
+  uint16_t* k_out;  // f16 [tiles * 256 + row blocks * block_keys, 576]
   uint16_t* q_out;  // f16 [rows, 576]
-  int32_t* status;
-  int prefix_len, rows, page_size, fp8;
+  int page_size, fp8;
+  int prefix_chunks, q_chunks, own_chunks;  // own_chunks: per (row block, sequence)
 };
 
-__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w, bool& bad) {
-  const float lo = __uint_as_float(w << 16), hi = __uint_as_float(w & 0xFFFF0000u);
-  bad |= !(fabsf(lo) <= 65504.f) || !(fabsf(hi) <= 65504.f);
-  const __half2 v = __floats2half2_rn(lo, hi);
+__device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t w) {
+  const __half2 v = __floats2half2_rn(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-// One thread per 8-element piece: rows [0, prefix_len) are the shared keys,
-// the rest the query rows.  Memory-bound (1152 or 576 B in, 1152 B out a row).
+// True if one of two f16 values is infinite or NaN: what a bf16 value beyond
+// 65504 (or itself not finite) becomes.
+__device__ __forceinline__ bool not_finite(uint32_t w) {
+  return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
+}
+
+__device__ __forceinline__ uint4 load_piece(const StageParams& p, int64_t row, int piece) {
+  if (!p.fp8)
+    return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + row * MLA_D_QK)[piece];
+  const uint2 c = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + row * MLA_D_QK)[piece];
+  return make_uint4(c.x, c.y, 0, 0);
+}
+
+__device__ __forceinline__ uint4 to_f16(const StageParams& p, uint4 v, bool fp8) {
+  if (!fp8)
+    return make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
+  const uint32_t c[2] = {v.x, v.y};
+  uint32_t w[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e)  // exact for every code; NaN codes become NaN
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w[e]) : "h"((uint16_t)(c[e >> 1] >> (16 * (e & 1)))));
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// A value that f16 cannot hold is staged as zero, and its key remembered.
+__device__ __noinline__ uint4 drop_bad(const StageParams& p, uint4 v, int key, int who) {
+  uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  for (int i = 0; i < 4; ++i) {
+    if ((w[i] & 0x7C00u) == 0x7C00u) w[i] &= 0xFFFF0000u;
+    if ((w[i] & 0x7C000000u) == 0x7C000000u) w[i] &= 0xFFFFu;
+  }
+  atomicOr(p.g.status, MLA_DEVFLAG_KV_RANGE);
+  atomicMax(p.g.bad + who, 0x7FFFFFFF - key);
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ bool any_bad(uint4 v) {
+  return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
+}
+
+// The tiles before each row block, where each pair starts and where each
+// sequence's own keys lie in its row blocks' regions.
+__device__ void partition(const StageParams& p) {
+  __shared__ int64_t warp_sum[kStageThreads / 32];
+  __shared__ int64_t carry_s;
+  const mla::PrefixShape& g = p.g;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) carry_s = 0;
+  __syncthreads();
+  for (int j0 = 0; j0 < g.row_blocks; j0 += kStageThreads) {
+    const int j = j0 + threadIdx.x;
+    int64_t n = 0;
+    if (j < g.row_blocks) {
+      int own = 0;
+      if (g.fold) {
+        const int b0 = g.first_seq(j), b1 = g.last_seq(j);
+        for (int b = b0; b <= b1; ++b) {
+          g.own_off[j * g.block_seqs + b - b0] = own;
+          own += g.own(b);
+        }
+      }
+      n = g.tiles + (own + mla::kPrefixTile - 1) / mla::kPrefixTile;
+    }
+    int64_t x = n;  // inclusive scan over the threads
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    if (lane == 31) warp_sum[warp] = x;
+    __syncthreads();
+    int64_t before = carry_s;
+    for (int k = 0; k < warp; ++k) before += warp_sum[k];
+    if (j < g.row_blocks) {
+      g.first_tile[j] = before + x - n;
+      if (j == g.row_blocks - 1) g.first_tile[j + 1] = before + x;
+    }
+    __syncthreads();
+    if (threadIdx.x == kStageThreads - 1) carry_s = before + x;
+    __syncthreads();
+  }
+  const int64_t total = carry_s;
+  for (int j = threadIdx.x; j < g.row_blocks; j += kStageThreads) {
+    const int64_t a = g.first_tile[j], z = g.first_tile[j + 1];
+    for (int64_t i = (a * g.pairs + total - 1) / total; i < g.pairs; ++i) {
+      const int64_t s = mla::prefix_share(total, g.pairs, (int)i);
+      if (s >= z) break;
+      if (s >= a) g.pair_start[i] = make_int2(j, (int)(s - a));
+    }
+  }
+  // Contexts out of range, once per sequence.
+  for (int b = threadIdx.x; b < g.batch; b += kStageThreads)
+    if (g.seq_lens[b] < 0 || g.seq_lens[b] > g.max_ctx) atomicOr(g.status, MLA_DEVFLAG_CTX_RANGE);
+}
+
+// CTA 0: the partition.  Then one CTA per 32 rows: shared keys (with zeros up
+// to the tile's end), query rows, own keys (row block by row block, sequence
+// by sequence, then the zeros up to the last tile's end).  Bound by memory:
+// 1152 or 576 B in and 1152 B out a row, 9 loads in flight a thread.
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
-  const uint32_t i = blockIdx.x * kStageThreads + threadIdx.x;
-  const uint32_t row = i / kPieces, piece = i % kPieces;
-  if (row >= (uint32_t)p.prefix_len + (uint32_t)p.rows) return;
-  bool bad = false;
-  uint4 v;
-  if (row < (uint32_t)p.prefix_len) {
-    const uint32_t page_i = row / (uint32_t)p.page_size;
-    int64_t page = p.table[page_i];
+  ptx::launch_dependents();
+  const mla::PrefixShape& g = p.g;
+  if (blockIdx.x == 0) {
+    partition(p);
+    return;
+  }
+  int u = blockIdx.x - 1;
+  // Rows [0, n) of this CTA go to `dst`; the first n_src of them come from
+  // `src` or through a page table (from key `key0` of it), the rest are zero.
+  int n = kChunk, n_src = 0, key0 = 0, who = -1;
+  const uint16_t* src = nullptr;
+  const int32_t* table = nullptr;
+  int64_t dst_row = 0;
+  uint16_t* dst = p.k_out;
+  if (u < p.prefix_chunks) {
+    key0 = u * kChunk;
+    dst_row = key0;
+    n_src = min(kChunk, max(0, g.prefix_len - key0));
+    table = p.prefix_table;
+    who = g.batch;
+  } else if ((u -= p.prefix_chunks) < p.q_chunks) {
+    const int r0 = u * kChunk;
+    n = n_src = min(kChunk, g.rows - r0);
+    src = p.q + (int64_t)r0 * MLA_D_QK;
+    dst = p.q_out;
+    dst_row = r0;
+  } else {
+    u -= p.q_chunks;
+    const int per_block = g.block_seqs * p.own_chunks + kPadChunks;
+    const int j = u / per_block, k = (u - j * per_block) / p.own_chunks;
+    const int c = u - j * per_block - k * p.own_chunks;
+    const int b0 = g.first_seq(j), b1 = g.last_seq(j);
+    const bool pad = k >= g.block_seqs;
+    const int b = b0 + k;
+    const int first_key = c * kChunk;  // of the sequence's own
+    int own = 0;
+    if (!pad) {
+      if (b > b1) return;
+      own = g.own(b);
+      if (first_key >= own) return;
+    }
+    // Own keys of the block's sequences before this one (pad: of all).
+    __shared__ int sum_s;
+    if (threadIdx.x == 0) sum_s = 0;
+    __syncthreads();
+    int part = 0;
+    for (int i = b0 + threadIdx.x; i <= (pad ? b1 : b - 1); i += kStageThreads) part += g.own(i);
+    if (part > 0) atomicAdd(&sum_s, part);
+    __syncthreads();
+    const int64_t region = (int64_t)g.tiles * mla::kPrefixTile + (int64_t)j * g.block_keys;
+    if (pad) {
+      const int end = (sum_s + mla::kPrefixTile - 1) / mla::kPrefixTile * mla::kPrefixTile;
+      const int at = sum_s + (u - j * per_block - g.block_seqs * p.own_chunks) * kChunk;
+      n = min(kChunk, end - at);
+      if (n <= 0) return;
+      dst_row = region + at;
+    } else {
+      n = n_src = min(kChunk, own - first_key);
+      table = p.block_table + (int64_t)b * p.bt_stride;
+      key0 = g.prefix_len + first_key;
+      dst_row = region + sum_s + first_key;
+      who = b;
+    }
+  }
+  uint4 v[kStageIters];
+#pragma unroll
+  for (int i = 0; i < kStageIters; ++i) {
+    const int at = threadIdx.x + i * kStageThreads;
+    const int row = at / kPieces, piece = at % kPieces;
+    v[i] = make_uint4(0, 0, 0, 0);
+    if (row >= n_src) continue;
+    if (src != nullptr) {
+      v[i] = reinterpret_cast<const uint4*>(src)[at];
+      continue;
+    }
+    const uint32_t key = (uint32_t)(key0 + row), page_i = key / (uint32_t)p.page_size;
+    int64_t page = table[page_i];
     if (page < 0 || page >= p.num_pages) {
-      if (piece == 0) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
+      if (piece == 0) atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
       page = 0;
     }
-    const int64_t at = (page * p.page_size + (row - page_i * (uint32_t)p.page_size)) * MLA_D_QK + piece * 8;
-    if (p.fp8) {
-      const uint2 codes = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + at);
-      const uint32_t cw[2] = {codes.x, codes.y};
-      uint32_t w[4];
+    v[i] = load_piece(p, page * p.page_size + (key - page_i * (uint32_t)p.page_size), piece);
+  }
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint16_t two = (uint16_t)(cw[e >> 1] >> (16 * (e & 1)));
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(w[e]) : "h"(two));
-        bad |= (two & 0x7Fu) == 0x7Fu || (two & 0x7F00u) == 0x7F00u;  // NaN codes
-      }
-      v = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + at);
-      v = make_uint4(bf16x2_to_f16x2(v.x, bad), bf16x2_to_f16x2(v.y, bad),
-                     bf16x2_to_f16x2(v.z, bad), bf16x2_to_f16x2(v.w, bad));
+  for (int i = 0; i < kStageIters; ++i) {
+    const int at = threadIdx.x + i * kStageThreads;
+    const int row = at / kPieces;
+    if (row >= n) continue;
+    v[i] = to_f16(p, v[i], src == nullptr && p.fp8);
+    if (any_bad(v[i])) {
+      if (src == nullptr) v[i] = drop_bad(p, v[i], key0 + row, who);
+      else atomicOr(g.status, MLA_DEVFLAG_Q_RANGE);  // spoils its own row only
     }
-    if (bad) atomicOr(p.status, MLA_DEVFLAG_KV_RANGE);
-    reinterpret_cast<uint4*>(p.k_out)[(size_t)row * kPieces + piece] = v;
-  } else {
-    const size_t at = (size_t)(row - (uint32_t)p.prefix_len) * kPieces + piece;
-    v = reinterpret_cast<const uint4*>(p.q)[at];
-    v = make_uint4(bf16x2_to_f16x2(v.x, bad), bf16x2_to_f16x2(v.y, bad), bf16x2_to_f16x2(v.z, bad),
-                   bf16x2_to_f16x2(v.w, bad));
-    if (bad) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
-    reinterpret_cast<uint4*>(p.q_out)[at] = v;
+    reinterpret_cast<uint4*>(dst + dst_row * MLA_D_QK)[at] = v[i];
   }
 }
 
 struct MergeParams {
-  const float* pre_o;    // [slots, total rows, 512]
-  const float* pre_lse;  // [slots, total rows]
+  mla::PrefixShape g;
+  const float* pre_o;    // [row blocks + pairs, 128, 512]
+  const float* pre_lse;  // [row blocks + pairs, 128]
   const float* own_o;    // [B, splits, rows, 512]
   const float* own_lse;  // [B, splits, rows]
   uint16_t* out;
   float* lse;
-  int64_t total_tiles;
-  int total_rows, rows, splits, tiles, pairs;
+  int splits;            // of the own keys, where they are not folded in
 };
 
-// One 128-thread CTA per row, 4 value dims a thread (as combine.cu, whose
-// partials have one layout; here a row's come from two).
-__global__ void __launch_bounds__(128) merge_kernel(MergeParams p) {
-  const int r = blockIdx.x;
-  const int b = r / p.rows, local = r - b * p.rows;
-  __shared__ float w_s[kMaxParts];
-  __shared__ float red[4];
-  __shared__ float L_s;
+// kWarps warps a CTA, one CTA per row: warp w takes partials w, w + kWarps,
+// ... under the row's maximum, 16 value dims a lane, and the warps' sums are
+// added at the end.  Rows of blocks that one pair finished return at once.
+template <int kWarps>
+__global__ void __launch_bounds__(32 * kWarps) merge_kernel(MergeParams p) {
+  const mla::PrefixShape& g = p.g;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int r = blockIdx.x, b = r / g.rows_per_seq, local = r - b * g.rows_per_seq;
+  __shared__ float4 acc_s[kWarps > 1 ? kWarps : 1][128];
+  __shared__ float sum_s[kWarps];
   ptx::grid_dependency_wait();
-  int np = 0;  // partials over the shared keys
-  if (p.tiles > 0) {
-    const int64_t t0 = (int64_t)(r / mla::kRowTile) * p.tiles;
-    np = mla::prefix_pair_of(p.total_tiles, p.pairs, t0 + p.tiles - 1) -
-         mla::prefix_pair_of(p.total_tiles, p.pairs, t0) + 1;
+  int first = 0, np = 0;  // pairs that hold a part of the row's block
+  const int j = r / mla::kRowTile;
+  if (g.tiles > 0) {
+    const int64_t total = g.first_tile[g.row_blocks];
+    first = mla::prefix_pair_of(total, g.pairs, g.first_tile[j]);
+    np = mla::prefix_pair_of(total, g.pairs, g.first_tile[j + 1] - 1) - first + 1;
+    if (np == 1 && p.splits == 0) return;
   }
   const int n = np + p.splits;
-  auto row_of = [&](int s) -> size_t {  // partial s of this row, in its own array
-    return s < np ? (size_t)s * p.total_rows + r : ((size_t)b * p.splits + (s - np)) * p.rows + local;
+  auto lse_of = [&](int s) -> float {
+    return s < np ? p.pre_lse[(size_t)(first + s + j) * mla::kRowTile + r % mla::kRowTile]
+                  : p.own_lse[((size_t)b * p.splits + (s - np)) * g.rows_per_seq + local];
   };
   float m = -INFINITY;
-  for (int s = threadIdx.x; s < n; s += 128) {
-    const float x = (s < np ? p.pre_lse : p.own_lse)[row_of(s)];
-    w_s[s] = x;
-    m = fmaxf(m, x);
-  }
+  for (int s = lane; s < n; s += 32) m = fmaxf(m, lse_of(s));
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-  __syncthreads();
+  float4 acc[4] = {};
   float sum = 0.f;
-  for (int s = threadIdx.x; s < n; s += 128) {
-    const float e = w_s[s] == -INFINITY ? 0.f : expf(w_s[s] - m);
-    w_s[s] = e;
-    sum += e;
-  }
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = sum;
-  __syncthreads();
-  const float tot = (red[0] + red[1]) + (red[2] + red[3]);
-  if (threadIdx.x == 0) L_s = m == -INFINITY ? -INFINITY : m + logf(tot);
-  __syncthreads();
-  const float inv = m == -INFINITY ? 0.f : 1.f / tot;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s0 = 0; s0 < n; s0 += 4) {
-    float4 v[4];
-    float wt[4];
+  for (int s = warp; s < n; s += kWarps) {
+    const float x = lse_of(s);
+    if (x == -INFINITY) continue;  // an empty part: its row may hold anything
+    const float w = expf(x - m);
+    const float4* o = reinterpret_cast<const float4*>(
+        s < np ? p.pre_o + ((size_t)(first + s + j) * mla::kRowTile + r % mla::kRowTile) * mla::kDV
+               : p.own_o + (((size_t)b * p.splits + (s - np)) * g.rows_per_seq + local) * mla::kDV);
+    sum += w;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      const int s = s0 + u;
-      wt[u] = s < n ? w_s[s] * inv : 0.f;
-      // An empty part's row was never written: it is not read.
-      v[u] = wt[u] != 0.f
-                 ? reinterpret_cast<const float4*>((s < np ? p.pre_o : p.own_o) + row_of(s) * mla::kDV)[threadIdx.x]
-                 : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-#pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      acc.x += wt[u] * v[u].x;
-      acc.y += wt[u] * v[u].y;
-      acc.z += wt[u] * v[u].z;
-      acc.w += wt[u] * v[u].w;
+    for (int i = 0; i < 4; ++i) {
+      const float4 v = o[lane + 32 * i];
+      acc[i].x += w * v.x;
+      acc[i].y += w * v.y;
+      acc[i].z += w * v.z;
+      acc[i].w += w * v.w;
     }
   }
-  __nv_bfloat162 lo = __floats2bfloat162_rn(acc.x, acc.y);
-  __nv_bfloat162 hi = __floats2bfloat162_rn(acc.z, acc.w);
-  uint2 packed;
-  packed.x = *reinterpret_cast<uint32_t*>(&lo);
-  packed.y = *reinterpret_cast<uint32_t*>(&hi);
-  reinterpret_cast<uint2*>(p.out + (size_t)r * mla::kDV)[threadIdx.x] = packed;
-  if (threadIdx.x == 0) p.lse[r] = L_s;
+  if (kWarps > 1) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc_s[warp][lane + 32 * i] = acc[i];
+    if (lane == 0) sum_s[warp] = sum;
+    __syncthreads();
+    if (warp > 0) return;
+    for (int k = 1; k < min(kWarps, n); ++k) {
+      sum += sum_s[k];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float4 v = acc_s[k][lane + 32 * i];
+        acc[i].x += v.x;
+        acc[i].y += v.y;
+        acc[i].z += v.z;
+        acc[i].w += v.w;
+      }
+    }
+  }
+  float L = sum > 0.f ? m + logf(sum) : -INFINITY, inv = sum > 0.f ? 1.f / sum : 0.f;
+  if (m != m || sum != sum || g.sees_bad(b, g.visible(r, b))) L = inv = NAN;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
+    const __nv_bfloat162 hi = __floats2bfloat162_rn(acc[i].z * inv, acc[i].w * inv);
+    reinterpret_cast<uint2*>(p.out + (size_t)r * mla::kDV)[lane + 32 * i] =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+  }
+  if (lane == 0) p.lse[r] = L;
 }
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t a) { return ceil_div(a, 256) * 256; }
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Most sequences with rows in one 128-row block: a block that starts at a
+// sequence's last row still holds it.
+int block_seqs(int64_t rows, int rows_per_seq) {
+  const int64_t batch = rows / rows_per_seq;
+  if (mla::kRowTile % rows_per_seq == 0) return (int)std::min<int64_t>(batch, mla::kRowTile / rows_per_seq);
+  if (rows_per_seq % mla::kRowTile == 0) return 1;
+  return (int)std::min<int64_t>(batch, (mla::kRowTile + rows_per_seq - 2) / rows_per_seq + 1);
+}
+
+mla::PrefixShape shape_of(const mla_decode_prefix_plan_t& p, const int32_t* seq_lens, char* ws) {
+  mla::PrefixShape g;
+  std::memset(&g, 0, sizeof g);
+  g.seq_lens = seq_lens;
+  g.status = reinterpret_cast<int32_t*>(ws + p.ws_status_offset);
+  g.bad = g.status + 4;
+  g.first_tile = reinterpret_cast<int64_t*>(ws + p.ws_partition_offset);
+  g.pair_start = reinterpret_cast<int2*>(g.first_tile + p.row_blocks + 1);
+  g.own_off = reinterpret_cast<int32_t*>(g.pair_start + p.pairs);
+  g.rows = p.total_rows;
+  g.rows_per_seq = p.rows;
+  g.heads = p.num_heads;
+  g.sq = p.sq;
+  g.causal = p.causal;
+  g.batch = p.batch;
+  g.prefix_len = p.prefix_len;
+  g.max_ctx = p.max_ctx;
+  g.tiles = p.prefix_tiles;
+  g.pairs = p.pairs;
+  g.row_blocks = p.row_blocks;
+  g.fold = p.own_folded;
+  g.block_seqs = p.own_folded ? block_seqs(p.total_rows, p.rows) : 0;
+  g.block_keys = p.block_keys;
+  return g;
+}
+
+// Every size and offset that follows from the plan's choices (batch, heads,
+// lengths, pairs, own_folded, own_chunk and own_splits).
+void lay_out(mla_decode_prefix_plan_t* p) {
+  p->rows = p->num_heads * p->sq;
+  p->total_rows = p->batch * p->rows;
+  p->row_blocks = (int32_t)ceil_div(p->total_rows, mla::kRowTile);
+  p->prefix_tiles = (int32_t)ceil_div(p->prefix_len, mla::kPrefixTile);
+  p->key_tile = mla_small_rows_fit(p->rows, p->kv_dtype) ? mla::kKeyTileSmall : mla::kKeyTile;
+  const int seqs = block_seqs(p->total_rows, p->rows);
+  const int64_t own = std::max(0, p->max_ctx - p->prefix_len);
+  p->block_keys = p->own_folded ? (int32_t)(ceil_div(own * seqs, mla::kPrefixTile) * mla::kPrefixTile) : 0;
+  int64_t off = 0;
+  auto take = [&](int64_t bytes) {
+    const int64_t at = off;
+    off = align256(off + bytes);
+    return at;
+  };
+  const int64_t segments = p->prefix_tiles > 0 ? (int64_t)p->row_blocks + p->pairs : 0;
+  const int64_t keys = (int64_t)p->prefix_tiles * mla::kPrefixTile + (int64_t)p->row_blocks * p->block_keys;
+  p->ws_status_offset = take(16 + 4 * ((int64_t)p->batch + 1));
+  p->ws_partition_offset = take(8 * ((int64_t)p->row_blocks + 1) + 8 * (int64_t)p->pairs +
+                                (p->own_folded ? 4ll * p->row_blocks * seqs : 0));
+  p->ws_keys_offset = take(p->prefix_tiles > 0 ? keys * MLA_D_QK * 2 : 0);
+  p->ws_q_offset = take(p->prefix_tiles > 0 ? (int64_t)p->total_rows * MLA_D_QK * 2 : 0);
+  p->ws_prefix_o_offset = take(segments * mla::kRowTile * MLA_D_V * 4);
+  p->ws_prefix_lse_offset = take(segments * mla::kRowTile * 4);
+  p->ws_own_o_offset = take((int64_t)p->own_splits * p->total_rows * MLA_D_V * 4);
+  p->ws_own_lse_offset = take((int64_t)p->own_splits * p->total_rows * 4);
+  p->workspace_bytes = off;
+}
+
 int check_plan(const mla_decode_prefix_plan_t* p) {
   if (p == nullptr || p->version != MLA_DECODE_PREFIX_PLAN_VERSION) return MLA_ERR_INVALID_ARG;
-  if (p->batch < 1 || p->num_heads < 1 || p->num_heads > 128 || p->sq < 1 || p->sq > 16 ||
-      p->rows != p->num_heads * p->sq || p->rows > mla::kMaxRows ||
-      (int64_t)p->batch * p->rows != p->total_rows || p->total_rows > MLA_PREFIX_MAX_ROWS)
+  if (p->batch < 1 || p->batch > 65535 || p->num_heads < 1 || p->num_heads > 128 || p->sq < 1 ||
+      p->sq > 16 || p->num_heads * p->sq > mla::kMaxRows ||
+      (int64_t)p->batch * p->num_heads * p->sq > MLA_PREFIX_MAX_ROWS)
     return MLA_ERR_INVALID_ARG;
   if (p->page_size < 1 || p->page_size > 4096 || p->prefix_len < 0 ||
-      p->prefix_len > MLA_PREFIX_MAX_LEN || p->max_ctx < 0 || p->wait_limit_us < 0)
+      p->prefix_len > MLA_PREFIX_MAX_LEN || p->max_ctx < 0 || p->wait_limit_us < 0 ||
+      p->causal < 0 || p->causal > 1)
     return MLA_ERR_INVALID_ARG;
   if (p->kv_dtype != MLA_KV_BF16 && p->kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
-  if (p->prefix_tiles != (int32_t)ceil_div(p->prefix_len, mla::kPrefixTile) ||
-      p->row_blocks != (int32_t)ceil_div(p->total_rows, mla::kRowTile))
+  if (p->own_folded < 0 || p->own_folded > 1 || p->own_splits < 0 ||
+      p->own_splits > mla::kMaxSplits || p->own_chunk < 1 || p->own_chunk > (1 << 30))
     return MLA_ERR_INVALID_ARG;
-  if (p->prefix_tiles > 0 &&
-      (p->pairs < 1 || p->pairs > kMaxPairs || p->pairs > (int64_t)p->row_blocks * p->prefix_tiles || p->prefix_slots < 1 ||
-       p->prefix_slots > p->pairs))
+  const int64_t own = std::max(0, p->max_ctx - p->prefix_len);
+  if (p->own_folded ? p->prefix_len == 0 || p->own_splits != 0 ||
+                          ceil_div((int64_t)p->batch * p->num_heads * p->sq, mla::kRowTile) * own *
+                                  block_seqs((int64_t)p->batch * p->num_heads * p->sq, p->num_heads * p->sq) >
+                              kMaxOwnRows
+                    : (int64_t)p->own_splits * p->own_chunk < own)
     return MLA_ERR_INVALID_ARG;
-  if (p->own_splits < 0 || p->own_splits > mla::kMaxSplits || p->own_chunk < 1 ||
-      p->prefix_slots + p->own_splits > kMaxParts)
+  // Everything else is what lay_out makes of these: a plan whose other fields
+  // differ was edited.
+  mla_decode_prefix_plan_t want = *p;
+  lay_out(&want);
+  if (std::memcmp(&want, p, sizeof want) != 0) return MLA_ERR_INVALID_ARG;
+  if (p->prefix_tiles > 0
+          ? p->pairs < 1 || p->pairs > kMaxPairs || p->pairs > (int64_t)p->row_blocks * p->prefix_tiles
+          : p->pairs != 0)
     return MLA_ERR_INVALID_ARG;
-  if (p->key_tile != (mla_small_rows_fit(p->rows, p->kv_dtype) ? mla::kKeyTileSmall : mla::kKeyTile) ||
-      p->own_chunk % p->key_tile != 0)
-    return MLA_ERR_INVALID_ARG;
+  if (p->own_chunk % p->key_tile != 0) return MLA_ERR_INVALID_ARG;
   return MLA_OK;
 }
 
@@ -220,89 +452,101 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
   if (plan == nullptr || seq_lens_host == nullptr) return MLA_ERR_INVALID_ARG;
   if (batch < 1 || batch > 65535 || prefix_len < 0 || prefix_len > MLA_PREFIX_MAX_LEN)
     return MLA_ERR_INVALID_ARG;
-  std::vector<int32_t> own;
   try {
-    own.resize(batch);
+    std::vector<int32_t> own(batch);
+    int32_t max_ctx = 0;
+    for (int b = 0; b < batch; ++b) {
+      if (seq_lens_host[b] < 0) return MLA_ERR_INVALID_ARG;
+      max_ctx = std::max(max_ctx, seq_lens_host[b]);
+      own[b] = std::max(0, seq_lens_host[b] - prefix_len);
+    }
+    // The own keys as a decode of contexts ctx_b - P; that call checks the
+    // other arguments.
+    mla_decode_plan_t d;
+    const int st = mla_decode_plan(own.data(), batch, num_heads, sq, page_size, kv_dtype, causal,
+                                   num_sms, &d);
+    if (st != MLA_OK) return st;
+    const int64_t total_rows = (int64_t)batch * d.rows;
+    if (total_rows > MLA_PREFIX_MAX_ROWS) return MLA_ERR_UNSUPPORTED;
+
+    mla_decode_prefix_plan_t p;
+    std::memset(&p, 0, sizeof p);
+    p.version = MLA_DECODE_PREFIX_PLAN_VERSION;
+    p.batch = batch;
+    p.num_heads = num_heads;
+    p.sq = sq;
+    p.page_size = page_size;
+    p.kv_dtype = kv_dtype;
+    p.causal = causal;
+    p.prefix_len = prefix_len;
+    p.max_ctx = max_ctx;
+    p.num_sms = d.num_sms;
+    p.own_chunk = d.chunk_len;
+    p.own_splits = d.max_ctx > 0 ? d.num_splits : 0;
+    lay_out(&p);
+
+    // Measured on GB300 (us): a 256-key tile on one pair, a segment's query
+    // rows, first softmax, last values and output, and the merge of cut rows.
+    constexpr double kTile = 2.8, kSegment = 7.0, kMergeFixed = 4.0, kMergeRow = 4096.0 / 4.0e6;
+    const int pairs = std::min(std::max(1, d.num_sms / 2), kMaxPairs);
+    std::vector<int64_t> first(p.row_blocks + 1, 0);  // tiles before each row block, own folded in
+    const int seqs = block_seqs(total_rows, p.rows);
+    for (int j = 0; j < p.row_blocks; ++j) {
+      const int b0 = (int)((int64_t)j * mla::kRowTile / p.rows);
+      const int b1 = (int)((std::min<int64_t>((int64_t)(j + 1) * mla::kRowTile, total_rows) - 1) / p.rows);
+      int64_t keys = 0;
+      for (int b = b0; b <= b1; ++b) keys += own[b];
+      first[j + 1] = first[j] + p.prefix_tiles + ceil_div(keys, mla::kPrefixTile);
+    }
+    if (p.prefix_tiles > 0) {
+      // Own keys as further tiles, unless they need too much room or cost more
+      // than a launch of the decode kernels of their own (about 10 us and 2.2
+      // us a key tile for each unit, all pairs at work; batch 64 x 128 heads
+      // with up to 512 own keys: 24 us against 3).
+      double separate = 0.0, longest = 0.0;
+      for (int b = 0; b < batch; ++b) {
+        const double unit = 10.0 + 2.2 * (double)ceil_div(own[b], p.key_tile);
+        separate += unit * d.row_blocks;
+        longest = std::max(longest, unit);
+      }
+      separate = std::max(longest, separate / pairs) + kMergeFixed;
+      const double folded =
+          kTile * (double)(first[p.row_blocks] - (int64_t)p.row_blocks * p.prefix_tiles) / pairs;
+      const int64_t room = (int64_t)p.row_blocks * seqs * std::max(0, max_ctx - prefix_len);
+      p.own_folded = max_ctx > prefix_len && room <= kMaxOwnRows && folded <= separate;
+      if (p.own_folded) p.own_splits = 0;
+      else for (int j = 0; j <= p.row_blocks; ++j) first[j] = (int64_t)j * p.prefix_tiles;
+      // Pairs that share the tiles: the count with the smallest longest pair,
+      // merge included.  With many row blocks all pairs are busy anyway.
+      const int64_t total = first[p.row_blocks];
+      const int most = (int)std::min<int64_t>(pairs, (int64_t)p.row_blocks * p.prefix_tiles);
+      double best = 1e300;
+      for (int n = p.row_blocks > 1024 ? most : 1; n <= most; ++n) {
+        double worst = 0.0;
+        int64_t cut_parts = 0;
+        int j = 0;
+        for (int i = 0; i < n; ++i) {
+          const int64_t a = mla::prefix_share(total, n, i), z = mla::prefix_share(total, n, i + 1);
+          while (first[j + 1] <= a) ++j;
+          int64_t segs = 0;
+          for (int k = j; k < p.row_blocks && first[k] < z; ++k) {
+            ++segs;
+            cut_parts += a > first[k] || z < first[k + 1];
+          }
+          worst = std::max(worst, kTile * (double)(z - a) + kSegment * (double)segs);
+        }
+        if (cut_parts > 0) worst += kMergeFixed + kMergeRow * mla::kRowTile * (double)cut_parts;
+        if (worst < best) {
+          best = worst;
+          p.pairs = n;
+        }
+      }
+    }
+    lay_out(&p);
+    *plan = p;
   } catch (const std::bad_alloc&) {
     return MLA_ERR_CUDA;
   }
-  int32_t max_ctx = 0;
-  for (int b = 0; b < batch; ++b) {
-    if (seq_lens_host[b] < 0) return MLA_ERR_INVALID_ARG;
-    max_ctx = std::max(max_ctx, seq_lens_host[b]);
-    own[b] = std::max(0, seq_lens_host[b] - prefix_len);
-  }
-  // The own keys are planned as a decode of contexts ctx_b - P; that call
-  // checks the other arguments.
-  mla_decode_plan_t d;
-  const int st = mla_decode_plan(own.data(), batch, num_heads, sq, page_size, kv_dtype, causal,
-                                 num_sms, &d);
-  if (st != MLA_OK) return st;
-  const int64_t total_rows = (int64_t)batch * d.rows;
-  if (total_rows > MLA_PREFIX_MAX_ROWS) return MLA_ERR_UNSUPPORTED;
-
-  mla_decode_prefix_plan_t p;
-  std::memset(&p, 0, sizeof p);
-  p.version = MLA_DECODE_PREFIX_PLAN_VERSION;
-  p.batch = batch;
-  p.num_heads = num_heads;
-  p.sq = sq;
-  p.page_size = page_size;
-  p.kv_dtype = kv_dtype;
-  p.causal = causal;
-  p.rows = d.rows;
-  p.total_rows = (int32_t)total_rows;
-  p.prefix_len = prefix_len;
-  p.max_ctx = max_ctx;
-  p.num_sms = d.num_sms;
-  p.row_blocks = (int32_t)ceil_div(total_rows, mla::kRowTile);
-  p.prefix_tiles = (int32_t)ceil_div(prefix_len, mla::kPrefixTile);
-  p.key_tile = d.key_tile;
-  p.own_chunk = d.chunk_len;
-  p.own_splits = d.max_ctx > 0 ? d.num_splits : 0;
-  if (p.prefix_tiles > 0) {
-    // Pairs that share the tiles.  A segment (row block, tile range) costs its
-    // tiles and about kSegment more for its query rows, its exposed first
-    // softmax and last values and the write of its partial; the count with the
-    // smallest longest pair wins, fewer pairs (fewer partials) on a tie.
-    const int64_t total = (int64_t)p.row_blocks * p.prefix_tiles;
-    const int most = (int)std::min<int64_t>(std::min(std::max(1, d.num_sms / 2), kMaxPairs), total);
-    constexpr double kSegment = 2.0;
-    double best = 1e300;
-    for (int n = 1; n <= most; ++n) {
-      double longest = 0.0;
-      for (int i = 0; i < n; ++i) {
-        const int64_t a = mla::prefix_share(total, n, i), z = mla::prefix_share(total, n, i + 1);
-        const int64_t segs = (z - 1) / p.prefix_tiles - a / p.prefix_tiles + 1;
-        longest = std::max(longest, (double)(z - a) + kSegment * (double)segs);
-      }
-      if (longest < best) {
-        best = longest;
-        p.pairs = n;
-      }
-    }
-    for (int j = 0; j < p.row_blocks; ++j) {
-      const int64_t t0 = (int64_t)j * p.prefix_tiles;
-      p.prefix_slots = std::max(
-          p.prefix_slots, mla::prefix_pair_of(total, p.pairs, t0 + p.prefix_tiles - 1) -
-                              mla::prefix_pair_of(total, p.pairs, t0) + 1);
-    }
-  }
-  int64_t off = 0;
-  auto take = [&](int64_t bytes) {
-    const int64_t at = off;
-    off = align256(off + bytes);
-    return at;
-  };
-  p.ws_status_offset = take(16);
-  p.ws_keys_offset = take(p.prefix_tiles > 0 ? (int64_t)prefix_len * MLA_D_QK * 2 : 0);
-  p.ws_q_offset = take(p.prefix_tiles > 0 ? total_rows * MLA_D_QK * 2 : 0);
-  p.ws_prefix_o_offset = take(p.prefix_slots * total_rows * MLA_D_V * 4);
-  p.ws_prefix_lse_offset = take(p.prefix_slots * total_rows * 4);
-  p.ws_own_o_offset = take(p.own_splits * total_rows * MLA_D_V * 4);
-  p.ws_own_lse_offset = take(p.own_splits * total_rows * 4);
-  p.workspace_bytes = off;
-  *plan = p;
   return MLA_OK;
 }
 
@@ -318,68 +562,66 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   if (workspace == nullptr || !aligned(workspace, 256) ||
       (int64_t)workspace_bytes < plan->workspace_bytes)
     return MLA_ERR_WORKSPACE;
+  const bool owns = plan->own_folded || plan->own_splits > 0;
   if (!q || !kv_cache || !seq_lens || !out || !lse) return MLA_ERR_INVALID_ARG;
   if (plan->prefix_tiles > 0 && !prefix_table) return MLA_ERR_INVALID_ARG;
-  if (plan->own_splits > 0 && !block_table) return MLA_ERR_INVALID_ARG;
+  if (owns && !block_table) return MLA_ERR_INVALID_ARG;
   if (!aligned(q, 16) || !aligned(kv_cache, 16) || !aligned(out, 16) || !aligned(lse, 4) ||
       !aligned(prefix_table, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) ||
       !aligned(kv_scale, 4))
     return MLA_ERR_INVALID_ARG;
   if (num_pages < 1) return MLA_ERR_INVALID_ARG;
   if (num_pages * (int64_t)plan->page_size >= ((int64_t)1 << 31)) return MLA_ERR_UNSUPPORTED;
-  if (plan->own_splits > 0 &&
-      (bt_stride < 1 || bt_stride * (int64_t)plan->page_size < (int64_t)plan->max_ctx))
+  if (owns && (bt_stride < 1 || bt_stride * (int64_t)plan->page_size < (int64_t)plan->max_ctx))
     return MLA_ERR_INVALID_ARG;
   if (!(softmax_scale >= 0.f && softmax_scale <= 3.0e38f)) return MLA_ERR_INVALID_ARG;
 
   char* ws = static_cast<char*>(workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  int32_t* status = reinterpret_cast<int32_t*>(ws + plan->ws_status_offset);
+  const mla::PrefixShape g = shape_of(*plan, seq_lens, ws);
   const bool fp8 = plan->kv_dtype == MLA_KV_FP8_E4M3;
   const uint64_t wait_ns =
       plan->wait_limit_us > 0 ? (uint64_t)plan->wait_limit_us * 1000ull : kDefaultWaitNs;
-  float* pre_o = reinterpret_cast<float*>(ws + plan->ws_prefix_o_offset);
-  float* pre_lse = reinterpret_cast<float*>(ws + plan->ws_prefix_lse_offset);
-  float* own_o = reinterpret_cast<float*>(ws + plan->ws_own_o_offset);
-  float* own_lse = reinterpret_cast<float*>(ws + plan->ws_own_lse_offset);
-  if (cudaMemsetAsync(status, 0, sizeof(int32_t), s) != cudaSuccess) return MLA_ERR_CUDA;
+  // The status word and the keys that f16 cannot hold.
+  if (cudaMemsetAsync(g.status, 0, 16 + 4 * ((size_t)plan->batch + 1), s) != cudaSuccess)
+    return MLA_ERR_CUDA;
 
   if (plan->prefix_tiles > 0) {
-    StageParams g;
-    g.cache = kv_cache;
-    g.num_pages = num_pages;
-    g.table = prefix_table;
-    g.q = static_cast<const uint16_t*>(q);
-    g.k_out = reinterpret_cast<uint16_t*>(ws + plan->ws_keys_offset);
-    g.q_out = reinterpret_cast<uint16_t*>(ws + plan->ws_q_offset);
-    g.status = status;
-    g.prefix_len = plan->prefix_len;
-    g.rows = plan->total_rows;
-    g.page_size = plan->page_size;
-    g.fp8 = fp8;
-    const int64_t items = ((int64_t)plan->prefix_len + plan->total_rows) * kPieces;
-    stage_kernel<<<(unsigned)ceil_div(items, kStageThreads), kStageThreads, 0, s>>>(g);
+    StageParams t;
+    t.g = g;
+    t.cache = kv_cache;
+    t.num_pages = num_pages;
+    t.prefix_table = prefix_table;
+    t.block_table = block_table;
+    t.bt_stride = bt_stride;
+    t.q = static_cast<const uint16_t*>(q);
+    t.k_out = reinterpret_cast<uint16_t*>(ws + plan->ws_keys_offset);
+    t.q_out = reinterpret_cast<uint16_t*>(ws + plan->ws_q_offset);
+    t.page_size = plan->page_size;
+    t.fp8 = fp8;
+    t.prefix_chunks = plan->prefix_tiles * (mla::kPrefixTile / kChunk);
+    t.q_chunks = (int)ceil_div(plan->total_rows, kChunk);
+    t.own_chunks = plan->own_folded ? (int)ceil_div(plan->max_ctx - plan->prefix_len, kChunk) : 1;
+    const int64_t ctas = 1 + (int64_t)t.prefix_chunks + t.q_chunks +
+                         (plan->own_folded ? (int64_t)plan->row_blocks *
+                                                 ((int64_t)g.block_seqs * t.own_chunks + kPadChunks)
+                                           : 0);
+    stage_kernel<<<(unsigned)ctas, kStageThreads, 0, s>>>(t);
     if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
 
     mla::PrefixParams p;
+    p.g = g;
     p.kv_scale = fp8 ? kv_scale : nullptr;
-    p.seq_lens = seq_lens;
-    p.part_o = pre_o;
-    p.part_lse = pre_lse;
-    p.status = status;
+    p.out = static_cast<uint16_t*>(out);
+    p.lse = lse;
+    p.part_o = reinterpret_cast<float*>(ws + plan->ws_prefix_o_offset);
+    p.part_lse = reinterpret_cast<float*>(ws + plan->ws_prefix_lse_offset);
     p.wait_ns = wait_ns;
-    p.total_tiles = (int64_t)plan->row_blocks * plan->prefix_tiles;
     p.softmax_scale = softmax_scale;
-    p.rows = plan->total_rows;
-    p.rows_per_seq = plan->rows;
-    p.heads = plan->num_heads;
-    p.sq = plan->sq;
-    p.causal = plan->causal;
-    p.prefix_len = plan->prefix_len;
-    p.max_ctx = plan->max_ctx;
-    p.tiles = plan->prefix_tiles;
-    p.pairs = plan->pairs;
-    if (mla_launch_prefix_sm103(p, g.k_out, g.q_out, stream) != 0) return MLA_ERR_CUDA;
+    p.partials = plan->own_splits > 0;
+    const int64_t key_rows =
+        (int64_t)plan->prefix_tiles * mla::kPrefixTile + (int64_t)plan->row_blocks * plan->block_keys;
+    if (mla_launch_prefix_sm103(p, t.k_out, key_rows, t.q_out, stream) != 0) return MLA_ERR_CUDA;
   }
 
   if (plan->own_splits > 0) {
@@ -395,9 +637,9 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
     f.softmax_scale = softmax_scale;
     f.out = static_cast<uint16_t*>(out);
     f.lse = lse;
-    f.part_o = own_o;
-    f.part_lse = own_lse;
-    f.status = status;
+    f.part_o = reinterpret_cast<float*>(ws + plan->ws_own_o_offset);
+    f.part_lse = reinterpret_cast<float*>(ws + plan->ws_own_lse_offset);
+    f.status = g.status;
     f.wait_ns = wait_ns;
     f.key_tile = plan->key_tile;
     f.batch = plan->batch;
@@ -416,29 +658,32 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
     if (mla_launch_fwd(f, stream) != 0) return MLA_ERR_CUDA;
   }
 
+  // One row block per pair and the own keys folded in: nothing was cut as long
+  // as the row blocks stay of equal length, which only the device knows; the
+  // merge's CTAs return at once for whole blocks.
   MergeParams m;
-  m.pre_o = pre_o;
-  m.pre_lse = pre_lse;
-  m.own_o = own_o;
-  m.own_lse = own_lse;
+  m.g = g;
+  m.pre_o = reinterpret_cast<const float*>(ws + plan->ws_prefix_o_offset);
+  m.pre_lse = reinterpret_cast<const float*>(ws + plan->ws_prefix_lse_offset);
+  m.own_o = reinterpret_cast<const float*>(ws + plan->ws_own_o_offset);
+  m.own_lse = reinterpret_cast<const float*>(ws + plan->ws_own_lse_offset);
   m.out = static_cast<uint16_t*>(out);
   m.lse = lse;
-  m.total_tiles = (int64_t)plan->row_blocks * plan->prefix_tiles;
-  m.total_rows = plan->total_rows;
-  m.rows = plan->rows;
   m.splits = plan->own_splits;
-  m.tiles = plan->prefix_tiles;
-  m.pairs = plan->pairs;
+  // Many partials a row (few row blocks shared by many pairs): eight warps to
+  // a row; else one.
+  const bool wide = plan->pairs > 4 * plan->row_blocks || plan->own_splits > 4;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)plan->total_rows, 1, 1);
-  cfg.blockDim = dim3(128, 1, 1);
+  cfg.blockDim = dim3(wide ? 256 : 32, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, merge_kernel, m) != cudaSuccess) return MLA_ERR_CUDA;
+  if (cudaLaunchKernelEx(&cfg, wide ? merge_kernel<8> : merge_kernel<1>, m) != cudaSuccess)
+    return MLA_ERR_CUDA;
   return MLA_OK;
 }
 

@@ -4,19 +4,22 @@
 // The batch's B * Sq * H query rows are one [rows, 576] matrix and the shared
 // keys one [P, 576] matrix, so the scores are a plain product: a key is loaded
 // once per 128 rows instead of once per sequence.  Row r sees the first
-// min(P, n_r) keys, n_r its own causal or ragged limit:
+// min(P, n_r) shared keys, n_r its own causal or ragged limit.  The own keys
+// of the sequences in a 128-row block may follow as further tiles of that
+// block (laid end to end; each row sees its own sequence's stretch), so that
+// one softmax runs over both:
 //
-//   z_j = c <q_r, k_j>,  j < min(P, n_r);   lse = ln sum_j e^z_j
-//   o   = sum_j e^(z_j - lse) k_j[0:512]
+//   z_j = c <q_r, k_j>;   lse = ln sum_j e^z_j;   o = sum_j e^(z_j - lse) k_j[0:512]
 //
-// and (o, lse) go to the workspace as one partial of the row, merged with the
-// partials of the sequence's own keys by the combine.
+// A row block that one pair holds is finished here; the parts of a cut one go
+// to the workspace as partials (o, lse) for the merge.
 //
-// Both matrices come staged: contiguous f16 rows of 576 (the staging kernel
-// walks the block table and converts the cache once, instead of once per row
+// Queries and keys come staged: contiguous f16 rows of 576 (the staging kernel
+// walks the block tables and converts the cache once, instead of once per row
 // block).  f16 keeps every bf16 and e4m3 value of ordinary size exactly, and
 // gives the weights 11 significant bits, so no second pass for heavy keys is
-// needed; values beyond 65504 are flagged by the staging kernel.
+// needed.  Keys that f16 cannot hold are staged as zeros and remembered; rows
+// that see one come out NaN.
 //
 // Split over a CTA pair.  An fp32 accumulator of 128 rows x 512 value dims
 // fills the TMEM of one SM, so a pair shares the 128 rows: `cta_group::2` MMAs
@@ -37,14 +40,19 @@
 // then values of tile t, so the softmax of a tile has the length of both in
 // which to finish.
 //
-// Work: tiles of all row blocks laid end to end are dealt to the pairs in
-// equal contiguous shares; a pair walks its one to three segments (row block,
-// tile range) in one launch.
+// Work: the tiles of all row blocks laid end to end are dealt to the pairs in
+// equal contiguous shares (counted on the device, since the own keys grow); a
+// pair walks its segments (row block, tile range) in one launch.
 //
-// Every wait is bounded; one that runs out sets MLA_DEVFLAG_TIMEOUT, after
-// which the CTA's loops run to their end without waiting or issuing.
+// Every wait is bounded; one that runs out sets MLA_DEVFLAG_TIMEOUT.  Loads,
+// MMAs and their commits are issued only while every wait of their warp has
+// passed: a commit for MMAs that were not issued would free a slab whose copy
+// has not landed, and the load warp would arm its barrier twice in one phase.
+// The softmax warps, which share named barriers, run their loops to the end
+// without waiting.
 
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -84,6 +92,7 @@ constexpr uint32_t TM_COLS = 512;
 constexpr float kHead = 7.f, kLag = 8.f;
 constexpr float kMaxSentinel = -1.0e30f;
 constexpr uint64_t kDrainNs = 500000000ull;
+constexpr uint64_t kSettleNs = 100000ull;
 constexpr uint32_t kSleepNs = 20000;
 
 struct Bars {
@@ -108,15 +117,22 @@ struct Ctx {
   uint32_t sleep_ns;
 };
 
-// The rest of a wait whose first sleep passed in vain: the timer and the abort
-// word.  Out of line, so that the loops around the waits stay short (with this
-// inlined and the slab loops unrolled they ran from the instruction cache's
-// misses: 136 against 107 us at batch 64 x 8192).
+// A wait that does not pass at once.  It sleeps on its barrier (polling warps
+// slow the MMA and load loops down) and reads the timer, which costs hundreds
+// of cycles, only once a whole sleep has passed in vain; a limit below a sleep
+// is polled.  Out of line, so that the loops around the waits stay short: with
+// this inlined and the slab loops unrolled they ran from the instruction
+// cache's misses (136 against 107 us at batch 64 x 8192).
 __device__ __noinline__ bool wait_slow(const Ctx& c, uint32_t bar, uint32_t parity) {
+  auto done = [&] {
+    return c.sleep_ns > 0 ? ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns)
+                          : ptx::mbar_test_wait(bar, parity);
+  };
+  if (done()) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
   while (true) {
     if (*c.abort) return false;
-    if (ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns)) return true;
+    if (done()) return true;
     if (ptx::globaltimer_ns() - t0 > c.limit_ns) {
       atomicOr(c.status, MLA_DEVFLAG_TIMEOUT);
       *c.abort = 1;
@@ -127,7 +143,7 @@ __device__ __noinline__ bool wait_slow(const Ctx& c, uint32_t bar, uint32_t pari
 
 // True when the phase completed; false once any wait of this CTA has run out.
 __device__ __forceinline__ bool wait(const Ctx& c, uint32_t bar, uint32_t parity) {
-  return ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns) || wait_slow(c, bar, parity);
+  return ptx::mbar_test_wait(bar, parity) || wait_slow(c, bar, parity);
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -141,6 +157,25 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   return *reinterpret_cast<uint32_t*>(&v);
 }
 
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<uint32_t*>(&v);
+}
+
+__device__ __forceinline__ void st_shared(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+  asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d)
+               : "memory");
+}
+
+__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 // K-major, 128B-swizzled operand (8-row groups 1 KB apart).
 __device__ __forceinline__ uint64_t kdesc(uint32_t addr) { return ptx::smem_desc(addr, 16, 1024, 2); }
 // MN-major values: 64-dim halves of a slab 8 KB apart, 8-key groups 1 KB apart.
@@ -151,22 +186,33 @@ __device__ __forceinline__ void group_sync(int g) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
 }
 
-// A pair's walk over its segments: row block rb, tiles [t0, t1).
+// A pair's walk over its segments: tiles [t0, t1) of row block rb, which has n.
 struct Walk {
-  int64_t at, end;
-  int tiles;
-  int rb, t0, t1;
-  __device__ __forceinline__ Walk(const mla::PrefixParams& p, int pair)
-      : at(mla::prefix_share(p.total_tiles, p.pairs, pair)),
-        end(mla::prefix_share(p.total_tiles, p.pairs, pair + 1)),
-        tiles(p.tiles) {}
+  const mla::PrefixShape& g;
+  int64_t left;
+  int next_rb, next_t;
+  int rb, t0, t1, n;
+  __device__ __forceinline__ Walk(const mla::PrefixShape& shape, int pair) : g(shape) {
+    const int64_t total = g.first_tile[g.row_blocks];
+    const int2 s = g.pair_start[pair];
+    left = mla::prefix_share(total, g.pairs, pair + 1) - mla::prefix_share(total, g.pairs, pair);
+    next_rb = s.x;
+    next_t = s.y;
+  }
   __device__ __forceinline__ bool next() {
-    if (at >= end) return false;
-    rb = (int)(at / tiles);
-    t0 = (int)(at - (int64_t)rb * tiles);
-    t1 = (int)min((int64_t)tiles, t0 + (end - at));
-    at += t1 - t0;
+    if (left <= 0) return false;
+    rb = next_rb;
+    t0 = next_t;
+    n = (int)(g.first_tile[rb + 1] - g.first_tile[rb]);
+    t1 = (int)min((int64_t)n, t0 + left);
+    left -= t1 - t0;
+    next_rb = rb + 1;
+    next_t = 0;
     return true;
+  }
+  // The staged key that tile t starts at.
+  __device__ __forceinline__ int key_row(int t) const {
+    return t < g.tiles ? t * T : (t + rb * (g.block_keys / T)) * T;
   }
 };
 
@@ -209,9 +255,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   ptx::grid_dependency_wait();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
-  Ctx c{p.status, &bars.abort, p.wait_ns,
-        (uint32_t)(p.wait_ns < (uint64_t)kSleepNs ? p.wait_ns : (uint64_t)kSleepNs)};
-  Walk w(p, pair);
+  Ctx c{p.g.status, &bars.abort, p.wait_ns,
+        p.wait_ns < (uint64_t)kSleepNs ? 0u : kSleepNs};
+  Walk w(p.g, pair);
 
   if (warp == kLoadWarp) {
     // -------------------------------------------------------------- loads ---
@@ -234,7 +280,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
     };
     auto scores = [&](int t) {
-      const int y = t * T + 128 * (int)rank;
+      const int y = w.key_row(t) + 128 * (int)rank;
 #pragma unroll 1
       for (int d = 0; d < 9; ++d) {
         reserve();
@@ -255,11 +301,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       scores(w.t0);
       for (int t = w.t0; t < w.t1; ++t) {
         if (t + 1 < w.t1) scores(t + 1);
+        const int y = w.key_row(t);
 #pragma unroll 1
         for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, dims 128 (v % 2) of the CTA's half
           reserve();
           if (ok && leader)
-            ptx::tma_load_3d_pair(sbase + OFF_RING + slot * SLAB, &vmap, 0, t * T + 64 * (v >> 1),
+            ptx::tma_load_3d_pair(sbase + OFF_RING + slot * SLAB, &vmap, 0, y + 64 * (v >> 1),
                                   4 * (int)rank + 2 * (v & 1), full0 + 8 * slot);
           advance();
         }
@@ -300,7 +347,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         next = ptx::mbar_test_wait(wrap ? full0 : full0 + 8 * (slot + 1), wrap ? ph ^ 1u : ph);
       };
       auto advance = [&] {
-        if (leader) ptx::mma_commit_pair(empty0 + 8 * slot);
+        if (leader && ok) ptx::mma_commit_pair(empty0 + 8 * slot);
         if (++slot == kSlots) {
           slot = 0;
           ph ^= 1u;
@@ -321,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           advance();
         }
-        if (leader) ptx::mma_commit_pair(ptx::smem_u32(&bars.o_done));
+        if (leader && ok) ptx::mma_commit_pair(ptx::smem_u32(&bars.o_done));
       };
       for (int seg = 0; w.next(); ++seg) {
         ok = ok && wait(c, ptx::smem_u32(&bars.q_full), seg & 1);
@@ -339,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
               advance();
             }
-            if (leader) {
+            if (leader && ok) {
               ptx::mma_commit_pair(ptx::smem_u32(&bars.s_full[it & 1]));
               if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
             }
@@ -373,17 +420,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     uint32_t it = 0;
     while (w.next()) {
       const int row = w.rb * mla::kRowTile + 64 * (int)rank + r;
-      int limit = 0;  // shared keys this row sees
-      if (row < p.rows) {
-        const int b = row / p.rows_per_seq;
-        int ctx = p.seq_lens[b];
-        if (ctx < 0 || ctx > p.max_ctx) {
-          atomicOr(p.status, MLA_DEVFLAG_CTX_RANGE);
-          ctx = ctx < 0 ? 0 : p.max_ctx;
+      // The row sees the first `shared` keys of the prefix and, of its row
+      // block's own keys, [own0, own1).
+      int shared = 0, own0 = 0, own1 = 0, n_vis = 0, b = 0;
+      if (row < p.g.rows) {
+        b = row / p.g.rows_per_seq;
+        n_vis = p.g.visible(row, b);
+        shared = min(n_vis, p.g.prefix_len);
+        if (p.g.fold) {
+          own0 = p.g.own_off[w.rb * p.g.block_seqs + b - p.g.first_seq(w.rb)];
+          own1 = own0 + max(0, n_vis - p.g.prefix_len);
         }
-        const int tok = (row - b * p.rows_per_seq) / p.heads;
-        const int n = p.causal ? ctx - p.sq + tok + 1 : ctx;
-        limit = max(0, min(n, p.prefix_len));
       }
       float m = kMaxSentinel, l = 0.f;
       for (int t = w.t0; t < w.t1; ++t, ++it) {
@@ -394,14 +441,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ptx::tmem_ld32(tmem + lanes + TM_S + 128 * (it & 1) + 64 * ch, s[0]);
         ptx::tmem_ld32(tmem + lanes + TM_S + 128 * (it & 1) + 64 * ch + 32, s[1]);
         ptx::tmem_ld_wait();
-        const int lim = limit - t * T - 64 * kg;  // keys of this thread's 64 that the row sees
-        const bool all = __all_sync(0xffffffffu, lim >= 64);
+        // Of this thread's 64 keys the row sees [from, lim).
+        const int at = (t < p.g.tiles ? t : t - p.g.tiles) * T + 64 * kg;
+        const int from = (t < p.g.tiles ? 0 : own0) - at, lim = (t < p.g.tiles ? shared : own1) - at;
+        const bool all = __all_sync(0xffffffffu, from <= 0 && lim >= 64);
         if (!all) {
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (32 * h + i >= lim) s[h][i] = 0xFF800000u;  // -inf: weight 0
+              if (32 * h + i < from || 32 * h + i >= lim) s[h][i] = 0xFF800000u;  // -inf: weight 0
         }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -457,9 +506,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int v = 0; v < 8; ++v)
-          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(p_row + ((v ^ (r & 7)) * 16)),
-                       "r"(pk[4 * v]), "r"(pk[4 * v + 1]), "r"(pk[4 * v + 2]), "r"(pk[4 * v + 3])
-                       : "memory");
+          st_shared(p_row + ((v ^ (r & 7)) * 16), pk[4 * v], pk[4 * v + 1], pk[4 * v + 2], pk[4 * v + 3]);
         ptx::fence_proxy_async_smem();
         ptx::tc_fence_before();
         __syncwarp();
@@ -473,44 +520,66 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool good = wait(c, ptx::smem_u32(&bars.o_done), (it - 1) & 1);
       __syncwarp();
       ptx::tc_fence_after();
-      const int first = mla::prefix_pair_of(p.total_tiles, p.pairs, (int64_t)w.rb * p.tiles);
-      const size_t slot = (size_t)(pair - first) * p.rows + row;
-      const float inv = l > 0.f ? s_kv / l : 0.f;
+      // A row block that this pair holds whole is final; another's goes to the
+      // partial of this segment, pair + row block.
+      const bool final = !p.partials && w.t0 == 0 && w.t1 == w.n;
+      float inv = l > 0.f ? s_kv / l : 0.f;
+      float lse = l > 0.f ? (m - kHead + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (final && row < p.g.rows && p.g.sees_bad(b, n_vis)) inv = lse = NAN;
+      const size_t seg = (size_t)(pair + w.rb) * mla::kRowTile;
+      const int local0 = 64 * (int)rank + 32 * (q4 & 1);  // the warp's first row of the block
+      const int rows_left = good ? p.g.rows - w.rb * mla::kRowTile - local0 : 0;
       // A thread holds one row, so 32 columns at a time go through the warp's
-      // 4 KB of the weights' buffer (read by now), 16-byte chunks swizzled by the
-      // row, and leave as 128-byte pieces of rows: written straight from the
-      // registers, every store touched 32 lines (11 us a segment instead of 3).
+      // 4 KB of the weights' buffer (read by now), 16-byte chunks swizzled by
+      // the row, and leave as 128-byte (bf16: 64-byte) pieces of rows: written
+      // straight from the registers, every store touched 32 lines (11 us a
+      // segment instead of 3).
       const uint32_t stage = p_row - lane * 128;  // where this warp writes its weights
-      const int row0 = w.rb * mla::kRowTile + 64 * (int)rank + 32 * (q4 & 1);  // the warp's first
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t o[32];
         ptx::tmem_ld32(tmem + lanes + TM_O + 128 * ch + 32 * cc, o);
         ptx::tmem_ld_wait();
+        if (final) {
 #pragma unroll
-        for (int v = 0; v < 8; ++v)
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(
-                           stage + lane * 128 + ((v ^ (lane & 7)) * 16)),
-                       "f"(__uint_as_float(o[4 * v]) * inv), "f"(__uint_as_float(o[4 * v + 1]) * inv),
-                       "f"(__uint_as_float(o[4 * v + 2]) * inv), "f"(__uint_as_float(o[4 * v + 3]) * inv)
-                       : "memory");
-        __syncwarp();
+          for (int i = 0; i < 32; i += 2)
+            o[i / 2] = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          const int rr = 4 * v + (lane >> 3), c8 = lane & 7;
-          float4 x;
-          asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
-                       : "=f"(x.x), "=f"(x.y), "=f"(x.z), "=f"(x.w)
-                       : "r"(stage + rr * 128 + ((c8 ^ (rr & 7)) * 16))
-                       : "memory");
-          if (good && row0 + rr < p.rows)
-            *reinterpret_cast<float4*>(p.part_o + ((size_t)(pair - first) * p.rows + row0 + rr) * mla::kDV +
-                                       dim0 + 32 * cc + 4 * c8) = x;
+          for (int v = 0; v < 4; ++v)
+            st_shared(stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) * 16), o[4 * v], o[4 * v + 1],
+                      o[4 * v + 2], o[4 * v + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < 4; ++v) {
+            const int rr = 8 * v + (lane >> 2), c4 = lane & 3;
+            const uint4 x = ld_shared(stage + rr * 64 + ((c4 ^ ((rr >> 1) & 3)) * 16));
+            if (rr < rows_left)
+              *reinterpret_cast<uint4*>(p.out + ((size_t)w.rb * mla::kRowTile + local0 + rr) * mla::kDV +
+                                        dim0 + 32 * cc + 8 * c4) = x;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
+#pragma unroll
+          for (int v = 0; v < 8; ++v)
+            st_shared(stage + lane * 128 + ((v ^ (lane & 7)) * 16), o[4 * v], o[4 * v + 1],
+                      o[4 * v + 2], o[4 * v + 3]);
+          __syncwarp();
+#pragma unroll
+          for (int v = 0; v < 8; ++v) {
+            const int rr = 4 * v + (lane >> 3), c8 = lane & 7;
+            const uint4 x = ld_shared(stage + rr * 128 + ((c8 ^ (rr & 7)) * 16));
+            if (rr < rows_left)
+              *reinterpret_cast<uint4*>(p.part_o + (seg + local0 + rr) * mla::kDV + dim0 + 32 * cc +
+                                        4 * c8) = x;
+          }
         }
         __syncwarp();
       }
-      if (good && row < p.rows && kg == 0)
-        p.part_lse[slot] = l > 0.f ? (m - kHead + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      if (lane < rows_left && kg == 0) {
+        if (final) p.lse[row] = lse;
+        else p.part_lse[seg + local0 + lane] = lse;
+      }
       ptx::tc_fence_before();
       __syncwarp();
       if (lane == 0) ptx::mbar_arrive_cluster(o_free);
@@ -521,14 +590,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   // ------------------------------------------------------------ teardown ---
   ptx::tc_fence_before();
   __syncthreads();
-  if (warp == kMmaWarp && bars.abort && rank == 0) {
-    if (lane == 0) {
+  if (bars.abort) {
+    // Nothing is issued any more.  The MMAs in flight are waited for, and
+    // copies of either CTA still landing, or arrivals still on their way to
+    // the other CTA, get far longer than they take.
+    if (warp == kMmaWarp && rank == 0 && lane == 0) {
       ptx::mma_commit_pair(ptx::smem_u32(&bars.drain));
       const uint64_t start = ptx::globaltimer_ns();
       while (!ptx::mbar_try_wait(ptx::smem_u32(&bars.drain), 0))
         if (ptx::globaltimer_ns() - start > kDrainNs) break;
     }
     __syncwarp();
+    const uint64_t start = ptx::globaltimer_ns();
+    while (ptx::globaltimer_ns() - start < kSettleNs) __nanosleep(1000);
+    __syncthreads();
   }
   ptx::cluster_sync_all();  // no CTA leaves, or frees TMEM, while the pair still works
   if (warp == kMmaWarp) {
@@ -539,15 +614,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 }  // namespace
 
-int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, const void* rows,
-                            void* stream) {
+int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, int64_t key_rows,
+                            const void* rows, void* stream) {
   // Score slabs: 128 keys x 64 dims.  Value slabs: 64 keys x 2 x 64 dims and
   // query slabs: 64 rows x 3 x 64 dims, the 64-dim groups of a row as a third
   // dimension, so that one copy fills a slab group by group.
   CUtensorMap kmap, vmap, qmap;
-  if (!mla::tensor_map_rows(&kmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, keys, p.prefix_len, mla::kDQK, 128) ||
-      !mla::tensor_map_groups(&vmap, keys, p.prefix_len, 2) ||
-      !mla::tensor_map_groups(&qmap, rows, p.rows, 3))
+  if (!mla::tensor_map_rows(&kmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, keys, key_rows, mla::kDQK, 128) ||
+      !mla::tensor_map_groups(&vmap, keys, key_rows, 2) ||
+      !mla::tensor_map_groups(&qmap, rows, p.g.rows, 3))
     return (int)cudaErrorUnknown;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -555,7 +630,7 @@ int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, const 
   e = mla::opt_in_smem(reinterpret_cast<const void*>(prefix_kernel), SMEM_BYTES, dev, 8);
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(2 * p.pairs, 1, 1);
+  cfg.gridDim = dim3(2 * p.g.pairs, 1, 1);
   cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.dynamicSmemBytes = SMEM_BYTES;
   cfg.stream = static_cast<cudaStream_t>(stream);

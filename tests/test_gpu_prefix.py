@@ -33,6 +33,11 @@ CASES = {
     "no_own_keys": (4, 1, 64, [600] * 4, 600, 1, BF16, False),
     "long_own": (2, 1, 128, [3300, 400], 300, 16, BF16, False),
     "rows_two_blocks_a_sequence": (2, 2, 128, [900, 850], 800, 16, BF16, True),
+    "blocks_across_sequences": (9, 3, 20, [700 + 9 * i for i in range(9)], 700, 16, BF16, True),
+    "one_row_sequences": (150, 1, 1, [300 + i % 7 * 30 for i in range(150)], 300, 16, FP8, False),
+    "own_apart": (3, 1, 128, [100 + 9000, 100 + 90000, 90], 100, 16, BF16, False),
+    "own_apart_few_rows": (2, 2, 8, [100 + 140000, 100 + 400], 100, 64, BF16, True),
+    "own_exact_tiles": (2, 1, 128, [512 + 256, 512 + 512], 512, 16, BF16, False),
 }
 
 
@@ -61,7 +66,7 @@ def test_plan_of_every_pair_count():
     for sms in range(2, 56, 6):
         out, lse, plan, status = p.run(t=t, num_sms=sms)
         assert status == 0
-        assert_close(out, lse, *ref, f"sms {sms}, {plan.pairs} pairs, {plan.prefix_slots} slots")
+        assert_close(out, lse, *ref, f"sms {sms}, {plan.pairs} pairs")
 
 
 @pytest.mark.parametrize("heads,sq,dtype", [(16, 4, BF16), (128, 1, BF16), (16, 1, FP8)])
@@ -195,20 +200,55 @@ def test_bad_pages_and_contexts_are_flagged():
     assert_close(out[2:], lse[2:], ref[0][2:], ref[1][2:], "the other sequences")
 
 
-@pytest.mark.parametrize("what", ["cache", "cache_nan", "q"])
-def test_values_beyond_f16_are_flagged(what):
+@pytest.mark.parametrize("value", [70000.0, float("nan"), float("-inf")])
+@pytest.mark.parametrize("fold", [True, False])
+def test_keys_beyond_f16_spoil_the_rows_that_see_them(value, fold):
+    """A shared key: every row that sees it; an own key: its sequence's rows.  The others stay."""
+    import paged_mla_decode_latent_gb300 as mla
+    lens = [300, 290, 100, 280] if fold else [300, 290, 100, 80000]
+    p = PrefixProblem(4, 1, 16, lens, 256, 16, seed=13)
+    ref, t, plan = p.reference(), p.to_device(), p.plan()
+    assert plan.own_folded == fold
+    keep = t["cache"].clone()
+    t["cache"][int(p.prefix_table[200 // 16]), 200 % 16, 9] = value  # the third sequence has 100 keys
+    out, lse, _, status = p.run(t=t, plan=plan)
+    assert status == mla.DEVFLAG_KV_RANGE
+    for b in (0, 1, 3):
+        assert np.isnan(out[b]).all() and np.isnan(lse[b]).all()
+    assert_close(out[2], lse[2], ref[0][2], ref[1][2], "too short to see it")
+    if fold:
+        t["cache"].copy_(keep)
+        t["cache"][int(p.block_table[1, 270 // 16]), 270 % 16, 575] = value
+        out, lse, _, status = p.run(t=t, plan=plan)
+        assert status == mla.DEVFLAG_KV_RANGE
+        assert np.isnan(out[1]).all() and np.isnan(lse[1]).all()
+        for b in (0, 2, 3):
+            assert_close(out[b], lse[b], ref[0][b], ref[1][b], "another sequence")
+
+
+def test_a_causal_token_before_a_bad_key_stays():
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(3, 3, 16, [300, 290, 280], 256, 16, causal=True, seed=16)
+    ref, t = p.reference(), p.to_device()
+    t["cache"][int(p.block_table[1, 289 // 16]), 289 % 16, 0] = float("inf")  # the last token's key
+    out, lse, _, status = p.run(t=t)
+    assert status == mla.DEVFLAG_KV_RANGE
+    assert np.isnan(out[1, 2]).all()
+    for b, i in ((0, 0), (0, 2), (1, 0), (1, 1), (2, 2)):
+        assert_close(out[b, i], lse[b, i], ref[0][b, i], ref[1][b, i], f"{b} {i}")
+
+
+def test_queries_beyond_f16_spoil_their_row():
     import paged_mla_decode_latent_gb300 as mla
     p = PrefixProblem(2, 1, 16, [300, 290], 256, 16, seed=13)
-    t = p.to_device()
-    if what == "q":
-        t["q"][1, 0, 3, 5] = 70000.0
-    else:
-        t["cache"][int(p.prefix_table[2]), 4, 9] = 70000.0 if what == "cache" else float("nan")
+    ref, t = p.reference(), p.to_device()
+    t["q"][1, 0, 3, 5] = 70000.0
     out, lse, _, status = p.run(t=t)
-    assert status == (mla.DEVFLAG_Q_RANGE if what == "q" else mla.DEVFLAG_KV_RANGE)
-    if what == "q":  # only the row that holds it
-        ref = p.reference()
-        assert_close(out[0], lse[0], ref[0][0], ref[1][0], "the other sequence")
+    assert status == mla.DEVFLAG_Q_RANGE
+    assert not np.isfinite(out[1, 0, 3]).all()
+    rest = [h for h in range(16) if h != 3]
+    assert_close(out[1, 0, rest], lse[1, 0, rest], ref[0][1, 0, rest], ref[1][1, 0, rest], "the other heads")
+    assert_close(out[0], lse[0], ref[0][0], ref[1][0], "the other sequence")
 
 
 def test_small_values():

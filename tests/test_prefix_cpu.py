@@ -19,39 +19,50 @@ def share(total, pairs, i):
 @pytest.mark.parametrize("batch,heads,sq,prefix,own,sms", [
     (1, 1, 1, 1, 0, 152), (4, 16, 1, 512, 64, 152), (64, 128, 1, 8192, 512, 152),
     (13, 12, 3, 4999, 333, 152), (128, 128, 1, 23333, 512, 152), (3, 100, 1, 255, 1, 2),
-    (7, 128, 8, 100000, 10, 148), (2, 16, 1, 0, 90, 152), (5, 64, 1, 257, 0, 37)])
+    (7, 128, 8, 100000, 10, 148), (2, 16, 1, 0, 90, 152), (5, 64, 1, 257, 0, 37),
+    (64, 128, 1, 100, 20000, 152), (130, 1, 1, 600, 40, 152), (9, 5, 3, 700, 10, 152)])
 def test_plan(batch, heads, sq, prefix, own, sms):
     lens = [prefix + (own * (b + 1)) // batch for b in range(batch)]
     p = mla.prefix_plan(lens, prefix, heads, sq, 16, mla.KV_BF16, sq > 1, sms)
-    assert p.total_rows == batch * heads * sq and p.row_blocks == -(-p.total_rows // 128)
+    rows = heads * sq
+    assert p.total_rows == batch * rows and p.row_blocks == -(-p.total_rows // 128)
     assert p.prefix_tiles == -(-prefix // 256) and p.max_ctx == max(lens)
-    assert p.own_splits * p.own_chunk >= own and p.own_chunk % p.key_tile == 0
-    assert (p.own_splits == 0) == (own == 0)
-    total = p.row_blocks * p.prefix_tiles
+    most = max(lens) - prefix
+    seqs = max(min(batch - 1, (128 * j + 127) // rows) - 128 * j // rows + 1 for j in range(p.row_blocks))
+    if p.own_folded:
+        # Room for every sequence at its longest, in whole tiles; no decode of its own.
+        assert prefix > 0 and p.own_splits == 0
+        assert p.block_keys % 256 == 0 and p.block_keys >= seqs * most
+        assert p.row_blocks * p.block_keys * 1152 < 2 ** 30
+    else:
+        assert p.block_keys == 0 and p.own_splits * p.own_chunk >= most
+        assert p.own_chunk % p.key_tile == 0 and (p.own_splits == 0) == (most == 0)
     if prefix:
-        assert 1 <= p.pairs <= min(max(1, sms // 2), total)
-        # Every pair has a tile, every tile one pair, and the slots cover a row block's pairs.
-        edges = [share(total, p.pairs, i) for i in range(p.pairs + 1)]
-        assert edges[0] == 0 and edges[-1] == total and all(a < b for a, b in zip(edges, edges[1:]))
-        slots = 0
-        for j in range(p.row_blocks):
-            t0, t1 = j * p.prefix_tiles, (j + 1) * p.prefix_tiles
-            holders = [i for i in range(p.pairs) if edges[i] < t1 and edges[i + 1] > t0]
-            first = ((t0 + 1) * p.pairs - 1) // total
-            assert holders[0] == first and holders == list(range(holders[0], holders[-1] + 1))
-            slots = max(slots, len(holders))
-        assert p.prefix_slots == slots
-    offs = [p.ws_status_offset, p.ws_keys_offset, p.ws_q_offset, p.ws_prefix_o_offset,
-            p.ws_prefix_lse_offset, p.ws_own_o_offset, p.ws_own_lse_offset, p.workspace_bytes]
-    sizes = [16, prefix * 1152, p.total_rows * 1152 if prefix else 0,
-             p.prefix_slots * p.total_rows * 2048, p.prefix_slots * p.total_rows * 4,
+        assert 1 <= p.pairs <= min(max(1, sms // 2), p.row_blocks * p.prefix_tiles)
+    else:
+        assert p.pairs == 0 and not p.own_folded
+    segments = p.row_blocks + p.pairs if prefix else 0
+    keys = 256 * p.prefix_tiles + p.row_blocks * p.block_keys
+    offs = [p.ws_status_offset, p.ws_partition_offset, p.ws_keys_offset, p.ws_q_offset,
+            p.ws_prefix_o_offset, p.ws_prefix_lse_offset, p.ws_own_o_offset, p.ws_own_lse_offset,
+            p.workspace_bytes]
+    sizes = [16 + 4 * (batch + 1),
+             8 * (p.row_blocks + 1) + 8 * p.pairs + (4 * p.row_blocks * seqs if p.own_folded else 0),
+             keys * 1152 if prefix else 0, p.total_rows * 1152 if prefix else 0,
+             segments * 128 * 2048, segments * 128 * 4,
              p.own_splits * p.total_rows * 2048, p.own_splits * p.total_rows * 4]
     for a, b, n in zip(offs, offs[1:], sizes):
         assert a % 256 == 0 and b - a >= n
 
 
+def test_own_keys_fold_in_or_not():
+    """Short own keys become tiles of their row blocks, long ones are decoded apart."""
+    assert mla.prefix_plan([8192 + 80] * 64, 8192, 128, 1, 16, 0, False, 152).own_folded == 1
+    assert mla.prefix_plan([1024 + 100000] * 16, 1024, 128, 1, 16, 0, False, 152).own_folded == 0
+
+
 def test_struct_layout():
-    assert ctypes.sizeof(mla.PrefixPlan) == 20 * 4 + 8 * 8
+    assert ctypes.sizeof(mla.PrefixPlan) == 22 * 4 + 9 * 8
 
 
 @pytest.mark.parametrize("kw", [
@@ -97,8 +108,10 @@ def test_fwd_refuses(kw, status):
 
 @pytest.mark.parametrize("field,value", [
     ("version", 0), ("batch", 0), ("rows", 17), ("total_rows", 33), ("prefix_len", 600),
-    ("prefix_tiles", 2), ("pairs", 0), ("pairs", 100), ("prefix_slots", 5), ("own_splits", 400),
-    ("own_chunk", 100), ("key_tile", 64), ("wait_limit_us", -1), ("kv_dtype", 7), ("page_size", 0)])
+    ("prefix_tiles", 2), ("pairs", 0), ("pairs", 100), ("pairs", -1), ("own_splits", 400),
+    ("own_folded", 2), ("own_folded", 0), ("block_keys", 0), ("max_ctx", 1 << 29), ("own_chunk", 100),
+    ("key_tile", 64), ("wait_limit_us", -1), ("kv_dtype", 7), ("page_size", 0),
+    ("ws_q_offset", 256), ("workspace_bytes", 512)])
 def test_fwd_refuses_an_edited_plan(field, value):
     plan = mla.prefix_plan([100, 120], 64, 16, 1, 16, 0, False, 152)
     setattr(plan, field, value)
