@@ -84,7 +84,9 @@ __host__ __device__ inline int prefix_pair_of(int64_t total, int pairs, int64_t 
 struct PrefixShape {
   const int32_t* seq_lens;  // [B]
   int64_t* first_tile;      // [row blocks + 1]: the tiles before each row block
-  int2* pair_start;         // [pairs]: row block and tile at which a pair starts
+  // [pairs]: the row block and the tile of it at which a pair starts, the row
+  // block's tiles and the pair's share
+  int4* pair_start;
   int32_t* own_off;         // [row blocks, block_seqs]: a sequence's first own key in its block's
   // [B + 1]: 2^31 - 1 - (first key of the sequence's own, and of the shared
   // ones, that f16 cannot hold); 0: none

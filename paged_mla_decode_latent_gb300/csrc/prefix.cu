@@ -105,6 +105,7 @@ __device__ void partition(const StageParams& p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) carry_s = 0;
   __syncthreads();
+  int64_t mine = 0, mine_n = 0;
   for (int j0 = 0; j0 < g.row_blocks; j0 += kStageThreads) {
     const int j = j0 + threadIdx.x;
     int64_t n = 0;
@@ -129,6 +130,8 @@ __device__ void partition(const StageParams& p) {
     int64_t before = carry_s;
     for (int k = 0; k < warp; ++k) before += warp_sum[k];
     if (j < g.row_blocks) {
+      mine = before + x - n;
+      mine_n = n;
       g.first_tile[j] = before + x - n;
       if (j == g.row_blocks - 1) g.first_tile[j + 1] = before + x;
     }
@@ -137,12 +140,17 @@ __device__ void partition(const StageParams& p) {
     __syncthreads();
   }
   const int64_t total = carry_s;
-  for (int j = threadIdx.x; j < g.row_blocks; j += kStageThreads) {
-    const int64_t a = g.first_tile[j], z = g.first_tile[j + 1];
+  for (int j0 = 0; j0 < g.row_blocks; j0 += kStageThreads) {
+    const int j = j0 + threadIdx.x;
+    if (j >= g.row_blocks) break;
+    // One batch of row blocks is still in registers.
+    const int64_t a = g.row_blocks <= kStageThreads ? mine : g.first_tile[j];
+    const int64_t z = g.row_blocks <= kStageThreads ? mine + mine_n : g.first_tile[j + 1];
     for (int64_t i = (a * g.pairs + total - 1) / total; i < g.pairs; ++i) {
       const int64_t s = mla::prefix_share(total, g.pairs, (int)i);
       if (s >= z) break;
-      if (s >= a) g.pair_start[i] = make_int2(j, (int)(s - a));
+      g.pair_start[i] = make_int4(j, (int)(s - a), (int)(z - a),
+                                  (int)(mla::prefix_share(total, g.pairs, (int)i + 1) - s));
     }
   }
   // Contexts out of range, once per sequence.
@@ -219,24 +227,32 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
       who = b;
     }
   }
+  // All page ids, then all rows: two round trips for the nine pieces.
   uint4 v[kStageIters];
+  if (src != nullptr) {
 #pragma unroll
-  for (int i = 0; i < kStageIters; ++i) {
-    const int at = threadIdx.x + i * kStageThreads;
-    const int row = at / kPieces, piece = at % kPieces;
-    v[i] = make_uint4(0, 0, 0, 0);
-    if (row >= n_src) continue;
-    if (src != nullptr) {
-      v[i] = reinterpret_cast<const uint4*>(src)[at];
-      continue;
+    for (int i = 0; i < kStageIters; ++i) {
+      const int at = threadIdx.x + i * kStageThreads;
+      v[i] = at < n_src * kPieces ? reinterpret_cast<const uint4*>(src)[at] : make_uint4(0, 0, 0, 0);
     }
-    const uint32_t key = (uint32_t)(key0 + row), page_i = key / (uint32_t)p.page_size;
-    int64_t page = table[page_i];
-    if (page < 0 || page >= p.num_pages) {
-      if (piece == 0) atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
-      page = 0;
+  } else {
+    int32_t page[kStageIters];
+    bool bad = false;
+#pragma unroll
+    for (int i = 0; i < kStageIters; ++i) {
+      const int row = (threadIdx.x + i * kStageThreads) / kPieces;
+      page[i] = row < n_src ? __ldg(table + (uint32_t)(key0 + row) / (uint32_t)p.page_size) : 0;
     }
-    v[i] = load_piece(p, page * p.page_size + (key - page_i * (uint32_t)p.page_size), piece);
+#pragma unroll
+    for (int i = 0; i < kStageIters; ++i) {
+      const int at = threadIdx.x + i * kStageThreads;
+      const int row = at / kPieces, piece = at % kPieces;
+      const bool out = page[i] < 0 || page[i] >= p.num_pages;
+      bad |= out;
+      const int64_t at_row = (int64_t)(out ? 0 : page[i]) * p.page_size + (uint32_t)(key0 + row) % (uint32_t)p.page_size;
+      v[i] = row < n_src ? load_piece(p, at_row, piece) : make_uint4(0, 0, 0, 0);
+    }
+    if (bad) atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
   }
 #pragma unroll
   for (int i = 0; i < kStageIters; ++i) {
@@ -358,9 +374,9 @@ mla::PrefixShape shape_of(const mla_decode_prefix_plan_t& p, const int32_t* seq_
   g.seq_lens = seq_lens;
   g.status = reinterpret_cast<int32_t*>(ws + p.ws_status_offset);
   g.bad = g.status + 4;
-  g.first_tile = reinterpret_cast<int64_t*>(ws + p.ws_partition_offset);
-  g.pair_start = reinterpret_cast<int2*>(g.first_tile + p.row_blocks + 1);
-  g.own_off = reinterpret_cast<int32_t*>(g.pair_start + p.pairs);
+  g.pair_start = reinterpret_cast<int4*>(ws + p.ws_partition_offset);
+  g.first_tile = reinterpret_cast<int64_t*>(g.pair_start + p.pairs);
+  g.own_off = reinterpret_cast<int32_t*>(g.first_tile + p.row_blocks + 1);
   g.rows = p.total_rows;
   g.rows_per_seq = p.rows;
   g.heads = p.num_heads;
@@ -398,7 +414,7 @@ void lay_out(mla_decode_prefix_plan_t* p) {
   const int64_t segments = p->prefix_tiles > 0 ? (int64_t)p->row_blocks + p->pairs : 0;
   const int64_t keys = (int64_t)p->prefix_tiles * mla::kPrefixTile + (int64_t)p->row_blocks * p->block_keys;
   p->ws_status_offset = take(16 + 4 * ((int64_t)p->batch + 1));
-  p->ws_partition_offset = take(8 * ((int64_t)p->row_blocks + 1) + 8 * (int64_t)p->pairs +
+  p->ws_partition_offset = take(8 * ((int64_t)p->row_blocks + 1) + 16 * (int64_t)p->pairs +
                                 (p->own_folded ? 4ll * p->row_blocks * seqs : 0));
   p->ws_keys_offset = take(p->prefix_tiles > 0 ? keys * MLA_D_QK * 2 : 0);
   p->ws_q_offset = take(p->prefix_tiles > 0 ? (int64_t)p->total_rows * MLA_D_QK * 2 : 0);
@@ -487,7 +503,7 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
 
     // Measured on GB300 (us): a 256-key tile on one pair, a segment's query
     // rows, first softmax, last values and output, and the merge of cut rows.
-    constexpr double kTile = 2.8, kSegment = 7.0, kMergeFixed = 4.0, kMergeRow = 4096.0 / 4.0e6;
+    constexpr double kTile = 2.4, kSegment = 4.0, kMergeFixed = 1.5, kMergeRow = 4096.0 / 4.0e6;
     const int pairs = std::min(std::max(1, d.num_sms / 2), kMaxPairs);
     std::vector<int64_t> first(p.row_blocks + 1, 0);  // tiles before each row block, own folded in
     const int seqs = block_seqs(total_rows, p.rows);
@@ -658,9 +674,10 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
     if (mla_launch_fwd(f, stream) != 0) return MLA_ERR_CUDA;
   }
 
-  // One row block per pair and the own keys folded in: nothing was cut as long
-  // as the row blocks stay of equal length, which only the device knows; the
-  // merge's CTAs return at once for whole blocks.
+  // Which row blocks were cut only the device knows (the merge's CTAs return
+  // at once for the whole ones), unless there is one pair and one row block.
+  if (plan->prefix_tiles > 0 && plan->own_splits == 0 && plan->row_blocks == 1 && plan->pairs == 1)
+    return MLA_OK;
   MergeParams m;
   m.g = g;
   m.pre_o = reinterpret_cast<const float*>(ws + plan->ws_prefix_o_offset);

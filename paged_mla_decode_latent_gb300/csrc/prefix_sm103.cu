@@ -114,19 +114,19 @@ struct Ctx {
   int32_t* status;
   volatile int32_t* abort;
   uint64_t limit_ns;
-  uint32_t sleep_ns;
 };
 
-// A wait that does not pass at once.  It sleeps on its barrier (polling warps
-// slow the MMA and load loops down) and reads the timer, which costs hundreds
-// of cycles, only once a whole sleep has passed in vain; a limit below a sleep
-// is polled.  Out of line, so that the loops around the waits stay short: with
-// this inlined and the slab loops unrolled they ran from the instruction
-// cache's misses (136 against 107 us at batch 64 x 8192).
+// A wait that does not pass at its first try.  It sleeps on its barrier
+// (polling warps slow the MMA and load loops down) and reads the timer, which
+// costs hundreds of cycles, only once a whole sleep has passed in vain.  Out
+// of line, so that the loops around the waits stay short: with this inlined
+// and the slab loops unrolled they ran from the instruction cache's misses
+// (136 against 107 us at batch 64 x 8192).
+// kPoll: a limit below a sleep; every try returns at once.
+template <bool kPoll>
 __device__ __noinline__ bool wait_slow(const Ctx& c, uint32_t bar, uint32_t parity) {
   auto done = [&] {
-    return c.sleep_ns > 0 ? ptx::mbar_try_wait_sleep(bar, parity, c.sleep_ns)
-                          : ptx::mbar_test_wait(bar, parity);
+    return kPoll ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait_sleep(bar, parity, kSleepNs);
   };
   if (done()) return true;
   const uint64_t t0 = ptx::globaltimer_ns();
@@ -142,8 +142,10 @@ __device__ __noinline__ bool wait_slow(const Ctx& c, uint32_t bar, uint32_t pari
 }
 
 // True when the phase completed; false once any wait of this CTA has run out.
-__device__ __forceinline__ bool wait(const Ctx& c, uint32_t bar, uint32_t parity) {
-  return ptx::mbar_test_wait(bar, parity) || wait_slow(c, bar, parity);
+template <bool kPoll>
+__device__ __forceinline__ bool wait_for(const Ctx& c, uint32_t bar, uint32_t parity) {
+  return (kPoll ? ptx::mbar_test_wait(bar, parity) : ptx::mbar_try_wait(bar, parity)) ||
+         wait_slow<kPoll>(c, bar, parity);
 }
 
 __device__ __forceinline__ float fast_exp2(float x) {
@@ -186,28 +188,33 @@ __device__ __forceinline__ void group_sync(int g) {
   asm volatile("bar.sync %0, 128;" ::"r"(1 + g) : "memory");
 }
 
-// A pair's walk over its segments: tiles [t0, t1) of row block rb, which has n.
+// A loaded value that is the same in every lane, as a uniform one.
+__device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
+
+// A pair's walk over its segments (the whole warp's: loop bounds that are not
+// known to be uniform cost the MMA loop its uniform registers, 517 against
+// 459 us at batch 128 x 23333): tiles [t0, t1) of row block rb, which has n.
 struct Walk {
   const mla::PrefixShape& g;
-  int64_t left;
-  int next_rb, next_t;
+  int left, next_rb, next_t, next_n;
   int rb, t0, t1, n;
   __device__ __forceinline__ Walk(const mla::PrefixShape& shape, int pair) : g(shape) {
-    const int64_t total = g.first_tile[g.row_blocks];
-    const int2 s = g.pair_start[pair];
-    left = mla::prefix_share(total, g.pairs, pair + 1) - mla::prefix_share(total, g.pairs, pair);
-    next_rb = s.x;
-    next_t = s.y;
+    const int4 s = g.pair_start[pair];
+    next_rb = uniform(s.x);
+    next_t = uniform(s.y);
+    next_n = uniform(s.z);
+    left = uniform(s.w);
   }
   __device__ __forceinline__ bool next() {
     if (left <= 0) return false;
     rb = next_rb;
     t0 = next_t;
-    n = (int)(g.first_tile[rb + 1] - g.first_tile[rb]);
-    t1 = (int)min((int64_t)n, t0 + left);
+    n = next_n;
+    t1 = min(n, t0 + left);
     left -= t1 - t0;
     next_rb = rb + 1;
     next_t = 0;
+    if (left > 0) next_n = uniform((int)(g.first_tile[rb + 2] - g.first_tile[rb + 1]));
     return true;
   }
   // The staged key that tile t starts at.
@@ -216,6 +223,7 @@ struct Walk {
   }
 };
 
+template <bool kPoll>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_kernel(mla::PrefixParams p, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap,
@@ -232,6 +240,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int pair = blockIdx.x >> 1;
 
   if (threadIdx.x == 0) {
+    ptx::prefetch_tensormap(&kmap);
+    ptx::prefetch_tensormap(&vmap);
+    ptx::prefetch_tensormap(&qmap);
     for (int i = 0; i < kSlots; ++i) {
       ptx::mbar_init(ptx::smem_u32(&bars.full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars.empty[i]), 1);
@@ -255,8 +266,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   ptx::tc_fence_after();
   ptx::grid_dependency_wait();
   const uint32_t tmem = __shfl_sync(0xffffffffu, bars.tmem_base, 0);
-  Ctx c{p.g.status, &bars.abort, p.wait_ns,
-        p.wait_ns < (uint64_t)kSleepNs ? 0u : kSleepNs};
+  const Ctx c{p.g.status, &bars.abort, p.wait_ns};
+  auto wait = [](const Ctx& ctx, uint32_t bar, uint32_t parity) { return wait_for<kPoll>(ctx, bar, parity); };
   Walk w(p.g, pair);
 
   if (warp == kLoadWarp) {
@@ -335,50 +346,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const uint64_t dq = kdesc(sbase + OFF_Q), dp = kdesc(sbase + OFF_P);
       const uint64_t dk = kdesc(sbase + OFF_RING), dv = vdesc(sbase + OFF_RING);
       const uint32_t full0 = ptx::smem_u32(&bars.full[0]), empty0 = ptx::smem_u32(&bars.empty[0]);
-      bool ok = true;
       bool ready = false, next = false;  // the current slab, the one after it has landed
       int slot = 0;
       uint32_t ph = 0;
       uint32_t it = 0;  // tiles whose scores this pair has issued, over all segments
-      auto take = [&] {  // the current slab
-        if (!ready) ok = ok && wait(c, full0 + 8 * slot, ph);
+      // The current slab: false once a wait has run out (the same in all
+      // lanes, as a vote, which keeps the control flow uniform).
+      auto pass = [&](uint32_t bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait(c, bar, parity)) != 0;
+      };
+      auto take = [&] {
+        if (!ready && !pass(full0 + 8 * slot, ph)) return false;
         ptx::tc_fence_after();
         const bool wrap = slot == kSlots - 1;
         next = ptx::mbar_test_wait(wrap ? full0 : full0 + 8 * (slot + 1), wrap ? ph ^ 1u : ph);
+        return true;
       };
       auto advance = [&] {
-        if (leader && ok) ptx::mma_commit_pair(empty0 + 8 * slot);
+        if (leader) ptx::mma_commit_pair(empty0 + 8 * slot);
         if (++slot == kSlots) {
           slot = 0;
           ph ^= 1u;
         }
         ready = next;
       };
-      auto values = [&](uint32_t i, bool first) {
-        ok = ok && wait(c, ptx::smem_u32(&bars.p_full), i & 1);
-#pragma unroll 1
-        for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, O columns 128 (v % 2)
-          take();
-          if (leader && ok) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              ptx::mma_ss_pair(tmem + TM_O + 128 * (v & 1), dp + (v >> 1) * (PSLAB >> 4) + 2 * k,
-                               dv + slot * (SLAB >> 4) + k * (2048 >> 4), id_pv,
-                               !(first && v < 2 && k == 0));
-          }
-          advance();
-        }
-        if (leader && ok) ptx::mma_commit_pair(ptx::smem_u32(&bars.o_done));
-      };
       for (int seg = 0; w.next(); ++seg) {
-        ok = ok && wait(c, ptx::smem_u32(&bars.q_full), seg & 1);
+        if (!pass(ptx::smem_u32(&bars.q_full), seg & 1)) goto mma_end;
         const int n = w.t1 - w.t0;
         for (int t = 0; t <= n; ++t) {
           if (t < n) {
-#pragma unroll 1
+#pragma unroll 3
             for (int d = 0; d < 9; ++d) {
-              take();
-              if (leader && ok) {
+              if (!take()) goto mma_end;
+              if (leader) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
                   ptx::mma_ss_pair(tmem + TM_S + 128 * (it & 1), dq + d * (QSLAB >> 4) + 2 * k,
@@ -386,7 +386,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               }
               advance();
             }
-            if (leader && ok) {
+            if (leader) {
               ptx::mma_commit_pair(ptx::smem_u32(&bars.s_full[it & 1]));
               if (t == n - 1) ptx::mma_commit_pair(ptx::smem_u32(&bars.q_empty));
             }
@@ -394,11 +394,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (t == 0) continue;
           // O is free once the segment before is read.
-          if (t == 1 && seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.o_free), (seg - 1) & 1);
-          values(it - 1 - (t < n), t == 1);
+          if (t == 1 && seg > 0 && !pass(ptx::smem_u32(&bars.o_free), (seg - 1) & 1)) goto mma_end;
+          if (!pass(ptx::smem_u32(&bars.p_full), (it - 1 - (t < n)) & 1)) goto mma_end;
+#pragma unroll 4
+          for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, O columns 128 (v % 2)
+            if (!take()) goto mma_end;
+            if (leader) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                ptx::mma_ss_pair(tmem + TM_O + 128 * (v & 1), dp + (v >> 1) * (PSLAB >> 4) + 2 * k,
+                                 dv + slot * (SLAB >> 4) + k * (2048 >> 4), id_pv,
+                                 !(t == 1 && v < 2 && k == 0));
+            }
+            advance();
+          }
+          if (leader) ptx::mma_commit_pair(ptx::smem_u32(&bars.o_done));
         }
       }
     }
+  mma_end:
     __syncwarp();
   } else {
     // ------------------------------------------------------------ softmax ---
@@ -627,7 +641,9 @@ int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, int64_
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
-  e = mla::opt_in_smem(reinterpret_cast<const void*>(prefix_kernel), SMEM_BYTES, dev, 8);
+  const bool poll = p.wait_ns < (uint64_t)kSleepNs;
+  auto* kernel = poll ? prefix_kernel<true> : prefix_kernel<false>;
+  e = mla::opt_in_smem(reinterpret_cast<const void*>(kernel), SMEM_BYTES, dev, poll ? 9 : 8);
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * p.g.pairs, 1, 1);
@@ -639,5 +655,5 @@ int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, int64_
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return (int)cudaLaunchKernelEx(&cfg, prefix_kernel, p, kmap, vmap, qmap);
+  return (int)cudaLaunchKernelEx(&cfg, kernel, p, kmap, vmap, qmap);
 }

@@ -381,6 +381,11 @@ __device__ __forceinline__ void tma_load_3d_pair(uint32_t dst, const void* tmap,
       : "memory");
 }
 
+// Fetch a tensor map (a __grid_constant__ parameter) ahead of its first use.
+__device__ __forceinline__ void prefetch_tensormap(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // Arrive on a barrier of another CTA of the cluster, releasing this CTA's
 // writes at CTA scope: for operands that the other CTA's thread only hands to
 // an MMA, which reads them in this CTA's own shared memory (the writer's proxy
