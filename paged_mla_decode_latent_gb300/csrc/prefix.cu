@@ -34,6 +34,7 @@ constexpr int kMaxPairs = 256;
 constexpr int kChunk = 32;  // rows a staging CTA copies
 constexpr int kStageThreads = 256;
 constexpr int kStageIters = kChunk * kPieces / kStageThreads;  // 9 pieces a thread
+static_assert(kStageThreads == 8 * kChunk, "eight threads a row");
 constexpr int kPadChunks = mla::kPrefixTile / kChunk;
 constexpr int64_t kMaxOwnRows = 1 << 18;  // own keys that are folded in at most (302 MB staged)
 
@@ -62,14 +63,7 @@ __device__ __forceinline__ bool not_finite(uint32_t w) {
   return (w & 0x7C00u) == 0x7C00u || (w & 0x7C000000u) == 0x7C000000u;
 }
 
-__device__ __forceinline__ uint4 load_piece(const StageParams& p, int64_t row, int piece) {
-  if (!p.fp8)
-    return reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + row * MLA_D_QK)[piece];
-  const uint2 c = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + row * MLA_D_QK)[piece];
-  return make_uint4(c.x, c.y, 0, 0);
-}
-
-__device__ __forceinline__ uint4 to_f16(const StageParams& p, uint4 v, bool fp8) {
+__device__ __forceinline__ uint4 to_f16(uint4 v, bool fp8) {
   if (!fp8)
     return make_uint4(bf16x2_to_f16x2(v.x), bf16x2_to_f16x2(v.y), bf16x2_to_f16x2(v.z), bf16x2_to_f16x2(v.w));
   const uint32_t c[2] = {v.x, v.y};
@@ -227,44 +221,50 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
       who = b;
     }
   }
-  // All page ids, then all rows: two round trips for the nine pieces.
+  // Eight threads a row, nine pieces each: one page id and one division a row,
+  // and every access of eight lanes is a whole 128-byte line.
+  const int row = threadIdx.x >> 3, sub = threadIdx.x & 7;
+  if (row >= n) return;
   uint4 v[kStageIters];
-  if (src != nullptr) {
+  bool fp8 = false;
+  if (row < n_src && src != nullptr) {
+    const uint4* at = reinterpret_cast<const uint4*>(src + row * MLA_D_QK) + sub;
 #pragma unroll
-    for (int i = 0; i < kStageIters; ++i) {
-      const int at = threadIdx.x + i * kStageThreads;
-      v[i] = at < n_src * kPieces ? reinterpret_cast<const uint4*>(src)[at] : make_uint4(0, 0, 0, 0);
+    for (int i = 0; i < kStageIters; ++i) v[i] = at[8 * i];
+  } else if (row < n_src) {
+    const uint32_t key = (uint32_t)(key0 + row), page_i = key / (uint32_t)p.page_size;
+    int64_t page = __ldg(table + page_i);
+    if (page < 0 || page >= p.num_pages) {
+      atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
+      page = 0;
+    }
+    const int64_t at_row = page * p.page_size + (key - page_i * (uint32_t)p.page_size);
+    fp8 = p.fp8;
+    if (fp8) {
+      const uint2* at = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + at_row * MLA_D_QK) + sub;
+#pragma unroll
+      for (int i = 0; i < kStageIters; ++i) {
+        const uint2 c = at[8 * i];
+        v[i] = make_uint4(c.x, c.y, 0, 0);
+      }
+    } else {
+      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + at_row * MLA_D_QK) + sub;
+#pragma unroll
+      for (int i = 0; i < kStageIters; ++i) v[i] = at[8 * i];
     }
   } else {
-    int32_t page[kStageIters];
-    bool bad = false;
 #pragma unroll
-    for (int i = 0; i < kStageIters; ++i) {
-      const int row = (threadIdx.x + i * kStageThreads) / kPieces;
-      page[i] = row < n_src ? __ldg(table + (uint32_t)(key0 + row) / (uint32_t)p.page_size) : 0;
-    }
-#pragma unroll
-    for (int i = 0; i < kStageIters; ++i) {
-      const int at = threadIdx.x + i * kStageThreads;
-      const int row = at / kPieces, piece = at % kPieces;
-      const bool out = page[i] < 0 || page[i] >= p.num_pages;
-      bad |= out;
-      const int64_t at_row = (int64_t)(out ? 0 : page[i]) * p.page_size + (uint32_t)(key0 + row) % (uint32_t)p.page_size;
-      v[i] = row < n_src ? load_piece(p, at_row, piece) : make_uint4(0, 0, 0, 0);
-    }
-    if (bad) atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
+    for (int i = 0; i < kStageIters; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
+  uint4* out = reinterpret_cast<uint4*>(dst + (dst_row + row) * MLA_D_QK) + sub;
 #pragma unroll
   for (int i = 0; i < kStageIters; ++i) {
-    const int at = threadIdx.x + i * kStageThreads;
-    const int row = at / kPieces;
-    if (row >= n) continue;
-    v[i] = to_f16(p, v[i], src == nullptr && p.fp8);
+    v[i] = to_f16(v[i], fp8);
     if (any_bad(v[i])) {
       if (src == nullptr) v[i] = drop_bad(p, v[i], key0 + row, who);
       else atomicOr(g.status, MLA_DEVFLAG_Q_RANGE);  // spoils its own row only
     }
-    reinterpret_cast<uint4*>(dst + dst_row * MLA_D_QK)[at] = v[i];
+    out[8 * i] = v[i];
   }
 }
 
