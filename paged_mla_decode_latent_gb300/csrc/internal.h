@@ -70,14 +70,17 @@ struct CombineParams {
 
 constexpr int kPrefixTile = 256;  // keys per tile
 
-// A pair's share of `total` tiles: [share(i), share(i + 1)).
-__host__ __device__ inline int64_t prefix_share(int64_t total, int pairs, int i) {
-  return total * i / pairs;
-}
-// The pair whose share holds tile x.
-__host__ __device__ inline int prefix_pair_of(int64_t total, int pairs, int64_t x) {
-  return (int)(((x + 1) * pairs - 1) / total);
-}
+// `total` tiles dealt to pairs in contiguous shares that differ by at most
+// one: pair i takes [start(i), start(i + 1)).
+struct PrefixShares {
+  int64_t q, r;
+  __host__ __device__ PrefixShares(int64_t total, int pairs) : q(total / pairs), r(total % pairs) {}
+  __host__ __device__ int64_t start(int64_t i) const { return i * q + (i < r ? i : r); }
+  __host__ __device__ int pair_of(int64_t x) const {  // the pair that holds tile x
+    const int64_t big = r * (q + 1);  // the tiles of the longer shares
+    return (int)(x < big ? x / (q + 1) : r + (x - big) / q);
+  }
+};
 
 // What the staging, the attention and the merge of a shared-prefix call know
 // of its rows, keys and partition.
@@ -87,6 +90,7 @@ struct PrefixShape {
   // [pairs]: the row block and the tile of it at which a pair starts, the row
   // block's tiles and the pair's share
   int4* pair_start;
+  int2* parts;              // [row blocks]: the first pair that holds a part of one, and their number
   int32_t* own_off;         // [row blocks, block_seqs]: a sequence's first own key in its block's
   // [B + 1]: 2^31 - 1 - (first key of the sequence's own, and of the shared
   // ones, that f16 cannot hold); 0: none

@@ -36,6 +36,7 @@ constexpr int kStageThreads = 256;
 constexpr int kStageIters = kChunk * kPieces / kStageThreads;  // 9 pieces a thread
 static_assert(kStageThreads == 8 * kChunk, "eight threads a row");
 constexpr int kPadChunks = mla::kPrefixTile / kChunk;
+constexpr int kManyParts = 8;  // partials a row from which the merge takes eight warps a row
 constexpr int64_t kMaxOwnRows = 1 << 18;  // own keys that are folded in at most (302 MB staged)
 
 struct StageParams {
@@ -133,18 +134,17 @@ __device__ void partition(const StageParams& p) {
     if (threadIdx.x == kStageThreads - 1) carry_s = before + x;
     __syncthreads();
   }
-  const int64_t total = carry_s;
-  for (int j0 = 0; j0 < g.row_blocks; j0 += kStageThreads) {
-    const int j = j0 + threadIdx.x;
-    if (j >= g.row_blocks) break;
+  const mla::PrefixShares shares(carry_s, g.pairs);
+  for (int j = threadIdx.x; j < g.row_blocks; j += kStageThreads) {
     // One batch of row blocks is still in registers.
     const int64_t a = g.row_blocks <= kStageThreads ? mine : g.first_tile[j];
     const int64_t z = g.row_blocks <= kStageThreads ? mine + mine_n : g.first_tile[j + 1];
-    for (int64_t i = (a * g.pairs + total - 1) / total; i < g.pairs; ++i) {
-      const int64_t s = mla::prefix_share(total, g.pairs, (int)i);
-      if (s >= z) break;
-      g.pair_start[i] = make_int4(j, (int)(s - a), (int)(z - a),
-                                  (int)(mla::prefix_share(total, g.pairs, (int)i + 1) - s));
+    const int first = shares.pair_of(a), last = shares.pair_of(z - 1);
+    g.parts[j] = make_int2(first, last - first + 1);
+    for (int i = first; i <= last; ++i) {
+      const int64_t s = shares.start(i);
+      if (s >= a)
+        g.pair_start[i] = make_int4(j, (int)(s - a), (int)(z - a), (int)(shares.start(i + 1) - s));
     }
   }
   // Contexts out of range, once per sequence.
@@ -279,30 +279,46 @@ struct MergeParams {
   int splits;            // of the own keys, where they are not folded in
 };
 
-// kWarps warps a CTA, one CTA per row: warp w takes partials w, w + kWarps,
-// ... under the row's maximum, 16 value dims a lane, and the warps' sums are
-// added at the end.  Rows of blocks that one pair finished return at once.
+// kWarps warps a row, eight warps a CTA; rows of blocks that one pair finished
+// return at once.  Warp w of a row takes partials w, w + kWarps, ... under the
+// row's maximum, 16 value dims a lane, and the warps' sums are added through
+// shared memory.  A partial's row is loaded beside the log-sum-exps (its weight
+// is needed only afterwards).  Bound by the round trips to L2, 2 KB a partial:
+// a warp a row does best while there are few partials (batch 64 x 128 heads,
+// two or three: 12 us, 17 with four warps sharing the dims), eight with many
+// (512 rows of 18: 9 us, 13 with the dims shared).
 template <int kWarps>
-__global__ void __launch_bounds__(32 * kWarps) merge_kernel(MergeParams p) {
+__global__ void __launch_bounds__(256) merge_kernel(MergeParams p) {
   const mla::PrefixShape& g = p.g;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int r = blockIdx.x, b = r / g.rows_per_seq, local = r - b * g.rows_per_seq;
-  __shared__ float4 acc_s[kWarps > 1 ? kWarps : 1][128];
+  const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % kWarps;
+  const int r = blockIdx.x * (8 / kWarps) + (threadIdx.x >> 5) / kWarps;
+  __shared__ float4 acc_s[kWarps][kWarps > 1 ? 128 : 1];
   __shared__ float sum_s[kWarps];
   ptx::grid_dependency_wait();
-  int first = 0, np = 0;  // pairs that hold a part of the row's block
-  const int j = r / mla::kRowTile;
+  if (r >= g.rows) return;  // with one row a CTA: never
+  const int b = r / g.rows_per_seq, local = r - b * g.rows_per_seq, j = r / mla::kRowTile;
+  int2 part = make_int2(0, 0);  // pairs that hold a part of the row's block
   if (g.tiles > 0) {
-    const int64_t total = g.first_tile[g.row_blocks];
-    first = mla::prefix_pair_of(total, g.pairs, g.first_tile[j]);
-    np = mla::prefix_pair_of(total, g.pairs, g.first_tile[j + 1] - 1) - first + 1;
-    if (np == 1 && p.splits == 0) return;
+    part = g.parts[j];
+    if (part.y == 1 && p.splits == 0) return;  // the same in all warps of a row
   }
-  const int n = np + p.splits;
+  const int n = part.y + p.splits;
+  const size_t pre0 = (size_t)(part.x + j) * mla::kRowTile + r % mla::kRowTile;
+  const size_t own0 = (size_t)b * p.splits * g.rows_per_seq + local;
   auto lse_of = [&](int s) -> float {
-    return s < np ? p.pre_lse[(size_t)(first + s + j) * mla::kRowTile + r % mla::kRowTile]
-                  : p.own_lse[((size_t)b * p.splits + (s - np)) * g.rows_per_seq + local];
+    return s < part.y ? p.pre_lse[pre0 + (size_t)s * mla::kRowTile]
+                      : p.own_lse[own0 + (size_t)(s - part.y) * g.rows_per_seq];
   };
+  float4 v[4];
+  auto load = [&](int s) {
+    if (s >= n) return;
+    const float4* row = reinterpret_cast<const float4*>(
+        s < part.y ? p.pre_o + (pre0 + (size_t)s * mla::kRowTile) * mla::kDV
+                   : p.own_o + (own0 + (size_t)(s - part.y) * g.rows_per_seq) * mla::kDV);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = row[lane + 32 * i];
+  };
+  load(warp);
   float m = -INFINITY;
   for (int s = lane; s < n; s += 32) m = fmaxf(m, lse_of(s));
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
@@ -310,20 +326,18 @@ __global__ void __launch_bounds__(32 * kWarps) merge_kernel(MergeParams p) {
   float sum = 0.f;
   for (int s = warp; s < n; s += kWarps) {
     const float x = lse_of(s);
-    if (x == -INFINITY) continue;  // an empty part: its row may hold anything
-    const float w = expf(x - m);
-    const float4* o = reinterpret_cast<const float4*>(
-        s < np ? p.pre_o + ((size_t)(first + s + j) * mla::kRowTile + r % mla::kRowTile) * mla::kDV
-               : p.own_o + (((size_t)b * p.splits + (s - np)) * g.rows_per_seq + local) * mla::kDV);
-    sum += w;
+    if (x != -INFINITY) {  // an empty part's row may hold anything
+      const float w = expf(x - m);
+      sum += w;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float4 v = o[lane + 32 * i];
-      acc[i].x += w * v.x;
-      acc[i].y += w * v.y;
-      acc[i].z += w * v.z;
-      acc[i].w += w * v.w;
+      for (int i = 0; i < 4; ++i) {
+        acc[i].x += w * v[i].x;
+        acc[i].y += w * v[i].y;
+        acc[i].z += w * v[i].z;
+        acc[i].w += w * v[i].w;
+      }
     }
+    load(s + kWarps);
   }
   if (kWarps > 1) {
 #pragma unroll
@@ -335,16 +349,16 @@ __global__ void __launch_bounds__(32 * kWarps) merge_kernel(MergeParams p) {
       sum += sum_s[k];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float4 v = acc_s[k][lane + 32 * i];
-        acc[i].x += v.x;
-        acc[i].y += v.y;
-        acc[i].z += v.z;
-        acc[i].w += v.w;
+        const float4 x = acc_s[k][lane + 32 * i];
+        acc[i].x += x.x;
+        acc[i].y += x.y;
+        acc[i].z += x.z;
+        acc[i].w += x.w;
       }
     }
   }
   float L = sum > 0.f ? m + logf(sum) : -INFINITY, inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (m != m || sum != sum || g.sees_bad(b, g.visible(r, b))) L = inv = NAN;
+  if (sum != sum || g.sees_bad(b, g.visible(r, b))) L = inv = NAN;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
@@ -376,7 +390,8 @@ mla::PrefixShape shape_of(const mla_decode_prefix_plan_t& p, const int32_t* seq_
   g.bad = g.status + 4;
   g.pair_start = reinterpret_cast<int4*>(ws + p.ws_partition_offset);
   g.first_tile = reinterpret_cast<int64_t*>(g.pair_start + p.pairs);
-  g.own_off = reinterpret_cast<int32_t*>(g.first_tile + p.row_blocks + 1);
+  g.parts = reinterpret_cast<int2*>(g.first_tile + p.row_blocks + 1);
+  g.own_off = reinterpret_cast<int32_t*>(g.parts + p.row_blocks);
   g.rows = p.total_rows;
   g.rows_per_seq = p.rows;
   g.heads = p.num_heads;
@@ -414,7 +429,7 @@ void lay_out(mla_decode_prefix_plan_t* p) {
   const int64_t segments = p->prefix_tiles > 0 ? (int64_t)p->row_blocks + p->pairs : 0;
   const int64_t keys = (int64_t)p->prefix_tiles * mla::kPrefixTile + (int64_t)p->row_blocks * p->block_keys;
   p->ws_status_offset = take(16 + 4 * ((int64_t)p->batch + 1));
-  p->ws_partition_offset = take(8 * ((int64_t)p->row_blocks + 1) + 16 * (int64_t)p->pairs +
+  p->ws_partition_offset = take(16 * (int64_t)p->row_blocks + 8 + 16 * (int64_t)p->pairs +
                                 (p->own_folded ? 4ll * p->row_blocks * seqs : 0));
   p->ws_keys_offset = take(p->prefix_tiles > 0 ? keys * MLA_D_QK * 2 : 0);
   p->ws_q_offset = take(p->prefix_tiles > 0 ? (int64_t)p->total_rows * MLA_D_QK * 2 : 0);
@@ -541,8 +556,9 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
         double worst = 0.0;
         int64_t cut_parts = 0;
         int j = 0;
+        const mla::PrefixShares shares(total, n);
         for (int i = 0; i < n; ++i) {
-          const int64_t a = mla::prefix_share(total, n, i), z = mla::prefix_share(total, n, i + 1);
+          const int64_t a = shares.start(i), z = shares.start(i + 1);
           while (first[j + 1] <= a) ++j;
           int64_t segs = 0;
           for (int k = j; k < p.row_blocks && first[k] < z; ++k) {
@@ -687,19 +703,18 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   m.out = static_cast<uint16_t*>(out);
   m.lse = lse;
   m.splits = plan->own_splits;
-  // Many partials a row (few row blocks shared by many pairs): eight warps to
-  // a row; else one.
-  const bool wide = plan->pairs > 4 * plan->row_blocks || plan->own_splits > 4;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)plan->total_rows, 1, 1);
-  cfg.blockDim = dim3(wide ? 256 : 32, 1, 1);
+  const int64_t parts = (plan->row_blocks ? plan->pairs / plan->row_blocks : 0) + plan->own_splits;
+  const bool many = parts >= kManyParts;
+  cfg.gridDim = dim3((unsigned)ceil_div(plan->total_rows, many ? 1 : 8), 1, 1);
+  cfg.blockDim = dim3(256, 1, 1);
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, wide ? merge_kernel<8> : merge_kernel<1>, m) != cudaSuccess)
+  if (cudaLaunchKernelEx(&cfg, many ? merge_kernel<8> : merge_kernel<1>, m) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }
