@@ -186,20 +186,8 @@ def _raise(st, where):
 
 
 def _is_fp8(cache):
-    import torch
+    torch = _torch()
     return cache.dtype in (torch.uint8, torch.float8_e4m3fn)
-
-
-def _expect(where, t, dtype, shape, strided=False):
-    """Refuses (ERR_INVALID_ARG) a tensor that is not what the C ABI reads: its dtype (a name, or
-    None), its shape (None: any extent), rows or all of it contiguous, the current CUDA device."""
-    import torch
-    if (t is not None and t.is_cuda and t.device.index == torch.cuda.current_device()
-            and (dtype is None or t.dtype == getattr(torch, dtype)) and t.dim() == len(shape)
-            and all(n is None or n == m for n, m in zip(shape, t.shape))
-            and (t.stride(-1) == 1 or t.shape[-1] == 1 if strided else t.is_contiguous())):
-        return
-    raise MLADecodeError(ERR_INVALID_ARG, where)
 
 
 def _row_stride(table):
@@ -218,6 +206,31 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+
+
+def _torch():
+    """torch, imported once (this module loads without it)."""
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+_torch_module = None
+
+
+def _device(t) -> int:
+    """The index of a tensor's device if that is the current one, else -1."""
+    dev = t.get_device()
+    return dev if dev >= 0 and dev == _torch()._C._cuda_getDevice() else -1
+
+
+def _raw_stream(stream, device: int) -> int:
+    """A stream's handle as an integer; None: the current stream of `device`."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(device)
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def plan(seq_lens_host, num_heads: int, sq: int, page_size: int, kv_dtype: int = KV_BF16,
@@ -335,30 +348,39 @@ def rope_epilogue(ql_nope, q_pe, kv_c, k_pe, positions, cos_sin, slot_mapping, q
                   stream=None) -> None:
     """``mla_decode_rope_epilogue``: ``epilogue`` with the rope dims of q_pe and k_pe rotated by
     their positions.  The four inputs may be strided views (last dimension contiguous)."""
-    where = "mla_decode_rope_epilogue"
+    torch = _torch()
+    bf, dev = torch.bfloat16, _device(ql_nope)
     T, H, _ = ql_nope.shape
-    fp8 = _is_fp8(kv_cache)
-    _expect(where, ql_nope, "bfloat16", (T, H, D_V), strided=True)
-    _expect(where, q_pe, "bfloat16", (T, H, 64), strided=True)
-    _expect(where, kv_c, "bfloat16", (T, D_V), strided=True)
-    _expect(where, k_pe, "bfloat16", (T, 64), strided=True)
-    _expect(where, positions, "int64", (T,))
-    _expect(where, cos_sin, "float32", (None, 64))
-    _expect(where, slot_mapping, "int64", (T,))
-    _expect(where, q_out, "bfloat16", (T, H, D_QK))
-    _expect(where, kv_cache, None if fp8 else "bfloat16", (None, None, D_QK))
-    if fp8:
-        _expect(where, kv_scale, "float32", (1,))
-    if status is not None:
-        _expect(where, status, "int32", (1,))
+    # What the C ABI reads, and nothing else: types, shapes, rows or all of a tensor contiguous,
+    # the current device.
+    fp8 = kv_cache.dtype is not bf
+    if not (ql_nope.dtype is q_pe.dtype is kv_c.dtype is k_pe.dtype is q_out.dtype is bf
+            and positions.dtype is slot_mapping.dtype is torch.int64 and cos_sin.dtype is torch.float32
+            and ql_nope.shape[2] == D_V and q_pe.shape == (T, H, 64) and kv_c.shape == (T, D_V)
+            and k_pe.shape == (T, 64) and positions.shape == slot_mapping.shape == (T,)
+            and cos_sin.dim() == 2 and cos_sin.shape[1] == 64 and q_out.shape == (T, H, D_QK)
+            and kv_cache.dim() == 3 and kv_cache.shape[2] == D_QK
+            and ql_nope.stride(2) == q_pe.stride(2) == kv_c.stride(1) == k_pe.stride(1) == 1
+            and positions.is_contiguous() and slot_mapping.is_contiguous()
+            and cos_sin.is_contiguous() and q_out.is_contiguous() and kv_cache.is_contiguous()
+            and 0 <= dev == q_pe.get_device() == kv_c.get_device()
+            == k_pe.get_device() == positions.get_device() == slot_mapping.get_device()
+            == cos_sin.get_device() == q_out.get_device() == kv_cache.get_device()
+            and (not fp8 or _is_fp8(kv_cache) and kv_scale is not None
+                 and kv_scale.dtype is torch.float32 and kv_scale.numel() == 1
+                 and kv_scale.get_device() == dev)
+            and (status is None or status.dtype is torch.int32 and status.numel() == 1
+                 and status.get_device() == dev)):
+        raise MLADecodeError(ERR_INVALID_ARG, "mla_decode_rope_epilogue")
     st = lib().mla_decode_rope_epilogue(
         ql_nope.data_ptr(), ql_nope.stride(0), ql_nope.stride(1), q_pe.data_ptr(), q_pe.stride(0),
         q_pe.stride(1), kv_c.data_ptr(), kv_c.stride(0), k_pe.data_ptr(), k_pe.stride(0),
-        positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], int(bool(interleaved)),
+        positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], 1 if interleaved else 0,
         slot_mapping.data_ptr(), T, H, q_out.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
-        kv_cache.shape[1], KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale if fp8 else None),
-        int(bool(inputs_early)), _ptr(status), _stream(stream))
-    _raise(st, where)
+        kv_cache.shape[1], KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None,
+        1 if inputs_early else 0, None if status is None else status.data_ptr(),
+        _raw_stream(stream, dev))
+    _raise(st, "mla_decode_rope_epilogue")
 
 
 def step(p: Plan, ql_nope, q_pe, kv_c, k_pe, slot_mapping, q, kv_cache, kv_scale, block_table,
@@ -399,33 +421,38 @@ def prefix_plan(seq_lens_host, prefix_len: int, num_heads: int, sq: int, page_si
 def prefix_fwd(p: PrefixPlan, q, kv_cache, kv_scale, prefix_table, block_table, seq_lens,
                softmax_scale: float, out, lse, workspace, stream=None) -> None:
     """``mla_decode_prefix_fwd``: the shared keys for all rows, each sequence's own keys, merged."""
-    where = "mla_decode_prefix_fwd"
-    B, Sq, H = p.batch, p.sq, p.num_heads
-    _expect(where, q, "bfloat16", (B, Sq, H, D_QK))
-    fp8 = p.kv_dtype == KV_FP8_E4M3
-    _expect(where, kv_cache, None if fp8 else "bfloat16", (None, p.page_size, D_QK))
-    if _is_fp8(kv_cache) != fp8:
-        raise MLADecodeError(ERR_INVALID_ARG, where)
-    if kv_scale is not None:
-        _expect(where, kv_scale, "float32", (1,))
-    if p.prefix_tiles:
-        _expect(where, prefix_table, "int32", (None,))
-        if prefix_table.shape[0] * p.page_size < p.prefix_len:
-            raise MLADecodeError(ERR_INVALID_ARG, where)
-    if p.max_ctx > p.prefix_len:
-        _expect(where, block_table, "int32", (B, None), strided=True)
-        if block_table.shape[1] * p.page_size < p.max_ctx:
-            raise MLADecodeError(ERR_INVALID_ARG, where)
-    _expect(where, seq_lens, "int32", (B,))
-    _expect(where, out, "bfloat16", (B, Sq, H, D_V))
-    _expect(where, lse, "float32", (B, Sq, H))
-    _expect(where, workspace, None, (None,))
+    torch = _torch()
+    dev = _device(q)
+    rows, fp8 = (p.batch, p.sq, p.num_heads), p.kv_dtype == KV_FP8_E4M3
+    prefix, own = p.prefix_len > 0, p.max_ctx > p.prefix_len
+    # What the C ABI reads, and nothing else: types, shapes, contiguous, the current device.
+    if not (q.dtype is out.dtype is torch.bfloat16 and lse.dtype is torch.float32
+            and seq_lens.dtype is torch.int32 and q.shape == (*rows, D_QK)
+            and out.shape == (*rows, D_V) and lse.shape == rows and seq_lens.shape == (p.batch,)
+            and kv_cache.dim() == 3 and kv_cache.shape[1:] == (p.page_size, D_QK)
+            and (_is_fp8(kv_cache) if fp8 else kv_cache.dtype is torch.bfloat16)
+            and q.is_contiguous() and out.is_contiguous() and lse.is_contiguous()
+            and seq_lens.is_contiguous() and kv_cache.is_contiguous() and workspace.is_contiguous()
+            and 0 <= dev == out.get_device() == lse.get_device()
+            == seq_lens.get_device() == kv_cache.get_device() == workspace.get_device()
+            and (kv_scale is None or kv_scale.dtype is torch.float32 and kv_scale.numel() == 1
+                 and kv_scale.get_device() == dev)
+            and (not prefix or prefix_table is not None and prefix_table.dtype is torch.int32 and prefix_table.dim() == 1
+                 and prefix_table.is_contiguous() and prefix_table.get_device() == dev
+                 and prefix_table.shape[0] * p.page_size >= p.prefix_len)
+            and (not own or block_table is not None and block_table.dtype is torch.int32 and block_table.dim() == 2
+                 and block_table.shape[0] == p.batch and block_table.stride(1) == 1
+                 and block_table.get_device() == dev
+                 and block_table.shape[1] * p.page_size >= p.max_ctx)):
+        raise MLADecodeError(ERR_INVALID_ARG, "mla_decode_prefix_fwd")
     st = lib().mla_decode_prefix_fwd(
-        ctypes.byref(p), _ptr(q), _ptr(kv_cache), int(kv_cache.shape[0]), _ptr(kv_scale),
-        _ptr(prefix_table), _ptr(block_table),
-        _row_stride(block_table), _ptr(seq_lens), float(softmax_scale), _ptr(out), _ptr(lse),
-        _ptr(workspace), _ws_bytes(workspace), _stream(stream))
-    _raise(st, where)
+        p, q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
+        None if kv_scale is None else kv_scale.data_ptr(),
+        prefix_table.data_ptr() if prefix else None, block_table.data_ptr() if own else None,
+        _row_stride(block_table) if own else 0, seq_lens.data_ptr(), softmax_scale,
+        out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+        workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
+    _raise(st, "mla_decode_prefix_fwd")
 
 
 def prefix_check(p: PrefixPlan, workspace, stream=None) -> int:

@@ -8,10 +8,12 @@
 // sums are fp32; the result is rounded once, to bf16 or to the e4m3 code of
 // x / kv_scale.
 //
-// One thread per 16-byte piece of a 576-wide row, 72 a row, rows ordered
-// (token, H query rows + the cache row), as epilogue.cu.  Pieces 0..63 are the
-// latent dims (copied, or converted in the cache row), 64..71 the rope dims.
-
+// Eight threads a row, rows ordered (token, H query rows + the cache row):
+// thread `sub` takes the 16-byte pieces sub, sub + 8, ... of the row's 72, so
+// every access of the eight is a whole 128-byte line, and its last piece (64 +
+// sub) is its share of the rope dims.  All nine loads are issued before the
+// first store.  Bound by memory (2304 B in and out a query row).
+//
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -23,9 +25,8 @@
 
 namespace {
 
-constexpr int kPieces = 72;
-constexpr int kRows = 4;  // rows per CTA
-constexpr int kThreads = kRows * kPieces;
+constexpr int kRows = 32;  // rows per CTA
+constexpr int kThreads = 8 * kRows;
 
 struct RopeParams {
   const uint16_t *ql, *qp, *kc, *kp;
@@ -46,12 +47,12 @@ struct RopeParams {
 __device__ __forceinline__ float lo_f(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float hi_f(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
-// The 8 rotated values of rope piece e (dims 8e .. 8e + 7) of a row at `src`.
-__device__ __forceinline__ void rotate(const RopeParams& p, const uint16_t* src, const float* cs,
-                                       int e, float (&o)[8]) {
-  const uint4 a4 = reinterpret_cast<const uint4*>(src)[e];
-  const uint32_t a[4] = {a4.x, a4.y, a4.z, a4.w};
-  if (p.interleaved) {
+// The 8 rotated values of rope piece e (dims 8e .. 8e + 7) given as `mine`; the
+// other seven pieces are with the other lanes of the row's eight.
+__device__ __forceinline__ void rotate(bool interleaved, uint4 mine, const float* cs, int e,
+                                       float (&o)[8]) {
+  const uint32_t a[4] = {mine.x, mine.y, mine.z, mine.w};
+  if (interleaved) {
     const float4 c = __ldg(reinterpret_cast<const float4*>(cs) + e);
     const float4 s = __ldg(reinterpret_cast<const float4*>(cs + 32) + e);
     const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
@@ -63,8 +64,9 @@ __device__ __forceinline__ void rotate(const RopeParams& p, const uint16_t* src,
     }
     return;
   }
-  const uint4 b4 = reinterpret_cast<const uint4*>(src)[e ^ 4];  // the other half's piece
-  const uint32_t b[4] = {b4.x, b4.y, b4.z, b4.w};
+  uint32_t b[4];  // the other half's piece, e ^ 4
+#pragma unroll
+  for (int i = 0; i < 4; ++i) b[i] = __shfl_xor_sync(0xffffffffu, a[i], 4);
   const float sign = e < 4 ? -1.f : 1.f;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
@@ -92,8 +94,8 @@ __device__ __forceinline__ uint32_t e4m3x2(float first, float second) {
 }
 
 __global__ void __launch_bounds__(kThreads) rope_epilogue_kernel(RopeParams p) {
-  const int piece = (int)(threadIdx.x % kPieces);
-  const uint32_t row = blockIdx.x * kRows + threadIdx.x / kPieces;
+  const int sub = (int)(threadIdx.x & 7);
+  const uint32_t row = blockIdx.x * kRows + (threadIdx.x >> 3);
   // Only inputs that the caller declares older than the kernel before this
   // one may be read ahead of the dependency wait.
   if (!p.early) ptx::grid_dependency_wait();
@@ -104,61 +106,65 @@ __global__ void __launch_bounds__(kThreads) rope_epilogue_kernel(RopeParams p) {
   const float* cs = p.cos_sin;
   if (active) {
     if (cache_row) slot = p.slots[t];
-    if (piece >= 64) {
-      int64_t pos = p.positions[t];
-      if (pos < 0 || pos >= p.max_pos) {
-        if (cache_row && piece == 64 && slot >= 0 && p.status) atomicOr(p.status, MLA_DEVFLAG_POSITION);
-        pos = pos < 0 ? 0 : p.max_pos - 1;
-      }
-      cs += pos * 64;
+    int64_t pos = p.positions[t];
+    if (pos < 0 || pos >= p.max_pos) {
+      if (cache_row && sub == 0 && slot >= 0 && p.status) atomicOr(p.status, MLA_DEVFLAG_POSITION);
+      pos = pos < 0 ? 0 : p.max_pos - 1;
     }
+    cs += pos * 64;
   }
   if (p.early) ptx::grid_dependency_wait();
   ptx::launch_dependents();
-  if (!active) return;
-  if (!cache_row) {
-    uint4 v;
-    if (piece < 64) {
-      v = reinterpret_cast<const uint4*>(p.ql + (int64_t)t * p.ql_t + (int64_t)h * p.ql_h)[piece];
-    } else {
-      float o[8];
-      rotate(p, p.qp + (int64_t)t * p.qp_t + (int64_t)h * p.qp_h, cs, piece - 64, o);
-      v = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                     pack_bf16(o[6], o[7]));
-    }
-    reinterpret_cast<uint4*>(p.q_out + ((int64_t)t * p.heads + h) * MLA_D_QK)[piece] = v;
-    return;
+  uint4 v[9];
+  if (active) {
+    const uint16_t* latent = cache_row ? p.kc + (int64_t)t * p.kc_t
+                                       : p.ql + (int64_t)t * p.ql_t + (int64_t)h * p.ql_h;
+    const uint16_t* rope = cache_row ? p.kp + (int64_t)t * p.kp_t
+                                     : p.qp + (int64_t)t * p.qp_t + (int64_t)h * p.qp_h;
+    v[8] = reinterpret_cast<const uint4*>(rope)[sub];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = reinterpret_cast<const uint4*>(latent)[sub + 8 * i];
   }
-  if (slot < 0) return;  // padding token: no insert
-  if (slot >= p.num_slots) {
-    if (piece == 0 && p.status) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
-    return;
-  }
-  uint4 v = make_uint4(0, 0, 0, 0);
   float o[8];
-  if (piece < 64) {
-    v = reinterpret_cast<const uint4*>(p.kc + (int64_t)t * p.kc_t)[piece];
-    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      o[2 * i] = lo_f(w[i]);
-      o[2 * i + 1] = hi_f(w[i]);
+  rotate(p.interleaved, v[8], cs, sub, o);  // every lane takes part
+  if (!active) return;
+  if (cache_row) {
+    if (slot < 0) return;  // padding token: no insert
+    if (slot >= p.num_slots) {
+      if (sub == 0 && p.status) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
+      return;
     }
-  } else {
-    rotate(p, p.kp + (int64_t)t * p.kp_t, cs, piece - 64, o);
-    v = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
-                   pack_bf16(o[6], o[7]));
-  }
-  if (!p.fp8) {
-    reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.cache) + slot * MLA_D_QK)[piece] = v;
-    return;
-  }
-  const float s = *p.kv_scale;
+    if (p.fp8) {
+      const float s = *p.kv_scale;
+      uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.cache) + slot * MLA_D_QK) + sub;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) o[i] = __fdiv_rn(o[i], s);
-  reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.cache) + slot * MLA_D_QK)[piece] =
-      make_uint2(e4m3x2(o[0], o[1]) | e4m3x2(o[2], o[3]) << 16,
-                 e4m3x2(o[4], o[5]) | e4m3x2(o[6], o[7]) << 16);
+      for (int i = 0; i < 9; ++i) {
+        float x[8];
+        if (i < 8) {
+          const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            x[2 * k] = lo_f(w[k]);
+            x[2 * k + 1] = hi_f(w[k]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < 8; ++k) x[k] = o[k];
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = __fdiv_rn(x[k], s);
+        dst[8 * i] = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
+                                e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+      }
+      return;
+    }
+  }
+  v[8] = make_uint4(pack_bf16(o[0], o[1]), pack_bf16(o[2], o[3]), pack_bf16(o[4], o[5]),
+                    pack_bf16(o[6], o[7]));
+  uint4* dst = reinterpret_cast<uint4*>(cache_row ? static_cast<uint16_t*>(p.cache) + slot * MLA_D_QK
+                                                  : p.q_out + ((int64_t)t * p.heads + h) * MLA_D_QK) + sub;
+#pragma unroll
+  for (int i = 0; i < 9; ++i) dst[8 * i] = v[i];
 }
 
 bool misaligned(const void* x, uintptr_t a) { return (reinterpret_cast<uintptr_t>(x) % a) != 0; }

@@ -124,3 +124,14 @@ def test_plan_is_quick():
     for _ in range(3):
         mla.prefix_plan(np.full(128, 23500), 23333, 128, 1, 16, 0, False, 152)
     assert (time.perf_counter() - t0) / 3 < 0.25
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    p = mla.prefix_plan([100, 120], 64, 16, 1, 16, 0, False, 152)
+    z = lambda *s, t=torch.bfloat16: torch.zeros(*s, dtype=t)  # noqa: E731
+    with pytest.raises(mla.MLADecodeError) as e:
+        mla.prefix_fwd(p, z(2, 1, 16, 576), z(20, 16, 576), None, z(4, t=torch.int32), z(2, 8, t=torch.int32),
+                       z(2, t=torch.int32), 0.07, z(2, 1, 16, 512), z(2, 1, 16, t=torch.float32),
+                       z(int(p.workspace_bytes), t=torch.uint8))
+    assert e.value.status == mla.ERR_INVALID_ARG
