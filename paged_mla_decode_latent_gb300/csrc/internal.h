@@ -106,7 +106,7 @@ struct PrefixShape {
 
 #ifdef __CUDACC__
   __device__ __forceinline__ int context(int b) const {
-    const int ctx = seq_lens[b];
+    const int ctx = __ldg(seq_lens + b);
     return ctx < 0 ? 0 : min(ctx, max_ctx);
   }
   __device__ __forceinline__ int own(int b) const { return max(0, context(b) - prefix_len); }

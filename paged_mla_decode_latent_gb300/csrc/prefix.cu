@@ -108,9 +108,15 @@ __device__ void partition(const StageParams& p) {
       int own = 0;
       if (g.fold) {
         const int b0 = g.first_seq(j), b1 = g.last_seq(j);
-        for (int b = b0; b <= b1; ++b) {
-          g.own_off[j * g.block_seqs + b - b0] = own;
-          own += g.own(b);
+        for (int b = b0; b <= b1; b += 8) {  // eight loads in flight
+          int keys[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) keys[k] = b + k <= b1 ? g.own(b + k) : 0;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            if (b + k <= b1) g.own_off[j * g.block_seqs + b + k - b0] = own;
+            own += keys[k];
+          }
         }
       }
       n = g.tiles + (own + mla::kPrefixTile - 1) / mla::kPrefixTile;
@@ -147,6 +153,7 @@ __device__ void partition(const StageParams& p) {
         g.pair_start[i] = make_int4(j, (int)(s - a), (int)(z - a), (int)(shares.start(i + 1) - s));
     }
   }
+  ptx::grid_dependency_wait();  // the status word is cleared
   // Contexts out of range, once per sequence.
   for (int b = threadIdx.x; b < g.batch; b += kStageThreads)
     if (g.seq_lens[b] < 0 || g.seq_lens[b] > g.max_ctx) atomicOr(g.status, MLA_DEVFLAG_CTX_RANGE);
@@ -226,7 +233,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   const int row = threadIdx.x >> 3, sub = threadIdx.x & 7;
   if (row >= n) return;
   uint4 v[kStageIters];
-  bool fp8 = false;
+  bool fp8 = false, bad_page = false;
   if (row < n_src && src != nullptr) {
     const uint4* at = reinterpret_cast<const uint4*>(src + row * MLA_D_QK) + sub;
 #pragma unroll
@@ -234,10 +241,8 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   } else if (row < n_src) {
     const uint32_t key = (uint32_t)(key0 + row), page_i = key / (uint32_t)p.page_size;
     int64_t page = __ldg(table + page_i);
-    if (page < 0 || page >= p.num_pages) {
-      atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
-      page = 0;
-    }
+    bad_page = page < 0 || page >= p.num_pages;
+    if (bad_page) page = 0;
     const int64_t at_row = page * p.page_size + (key - page_i * (uint32_t)p.page_size);
     fp8 = p.fp8;
     if (fp8) {
@@ -256,6 +261,8 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
 #pragma unroll
     for (int i = 0; i < kStageIters; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
+  ptx::grid_dependency_wait();  // the words that flags go to are cleared
+  if (bad_page) atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
   uint4* out = reinterpret_cast<uint4*>(dst + (dst_row + row) * MLA_D_QK) + sub;
 #pragma unroll
   for (int i = 0; i < kStageIters; ++i) {
@@ -266,6 +273,15 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
     }
     out[8 * i] = v[i];
   }
+}
+
+// The status word and the bad keys' words.  A kernel, not a memset: the staging
+// is launched as its programmatic dependent and overlaps it (3 us a call).
+// It is itself launched plainly, so everything before this call is done when
+// it starts, and what follows may read the call's inputs at once.
+__global__ void __launch_bounds__(256) clear_kernel(int32_t* words, int n) {
+  ptx::launch_dependents();
+  for (int i = threadIdx.x; i < n; i += 256) words[i] = 0;
 }
 
 struct MergeParams {
@@ -614,9 +630,15 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   const bool fp8 = plan->kv_dtype == MLA_KV_FP8_E4M3;
   const uint64_t wait_ns =
       plan->wait_limit_us > 0 ? (uint64_t)plan->wait_limit_us * 1000ull : kDefaultWaitNs;
-  // The status word and the keys that f16 cannot hold.
-  if (cudaMemsetAsync(g.status, 0, 16 + 4 * ((size_t)plan->batch + 1), s) != cudaSuccess)
-    return MLA_ERR_CUDA;
+  clear_kernel<<<1, 256, 0, s>>>(g.status, 4 + plan->batch + 1);
+  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  cudaLaunchAttribute attr[1];  // of the launches that overlap the one before them
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
 
   if (plan->prefix_tiles > 0) {
     StageParams t;
@@ -638,8 +660,9 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
                          (plan->own_folded ? (int64_t)plan->row_blocks *
                                                  ((int64_t)g.block_seqs * t.own_chunks + kPadChunks)
                                            : 0);
-    stage_kernel<<<(unsigned)ctas, kStageThreads, 0, s>>>(t);
-    if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+    cfg.gridDim = dim3((unsigned)ctas, 1, 1);
+    cfg.blockDim = dim3(kStageThreads, 1, 1);
+    if (cudaLaunchKernelEx(&cfg, stage_kernel, t) != cudaSuccess) return MLA_ERR_CUDA;
 
     mla::PrefixParams p;
     p.g = g;
@@ -703,17 +726,10 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   m.out = static_cast<uint16_t*>(out);
   m.lse = lse;
   m.splits = plan->own_splits;
-  cudaLaunchConfig_t cfg = {};
-  const int64_t parts = (plan->row_blocks ? plan->pairs / plan->row_blocks : 0) + plan->own_splits;
+  const int64_t parts = plan->pairs / plan->row_blocks + plan->own_splits;
   const bool many = parts >= kManyParts;
   cfg.gridDim = dim3((unsigned)ceil_div(plan->total_rows, many ? 1 : 8), 1, 1);
   cfg.blockDim = dim3(256, 1, 1);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, many ? merge_kernel<8> : merge_kernel<1>, m) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;

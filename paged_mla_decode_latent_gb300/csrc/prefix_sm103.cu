@@ -169,15 +169,6 @@ __device__ __forceinline__ void st_shared(uint32_t addr, uint32_t a, uint32_t b,
                : "memory");
 }
 
-__device__ __forceinline__ uint4 ld_shared(uint32_t addr) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-               : "r"(addr)
-               : "memory");
-  return v;
-}
-
 // K-major, 128B-swizzled operand (8-row groups 1 KB apart).
 __device__ __forceinline__ uint64_t kdesc(uint32_t addr) { return ptx::smem_desc(addr, 16, 1024, 2); }
 // MN-major values: 64-dim halves of a slab 8 KB apart, 8-key groups 1 KB apart.
@@ -543,52 +534,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const size_t seg = (size_t)(pair + w.rb) * mla::kRowTile;
       const int local0 = 64 * (int)rank + 32 * (q4 & 1);  // the warp's first row of the block
       const int rows_left = good ? p.g.rows - w.rb * mla::kRowTile - local0 : 0;
-      // A thread holds one row, so 32 columns at a time go through the warp's
-      // 4 KB of the weights' buffer (read by now), 16-byte chunks swizzled by
-      // the row, and leave as 128-byte (bf16: 64-byte) pieces of rows: written
-      // straight from the registers, every store touched 32 lines (11 us a
-      // segment instead of 3).
-      const uint32_t stage = p_row - lane * 128;  // where this warp writes its weights
+      // The 16x256b shape gives a lane pairs of columns of two rows, four lanes 32
+      // contiguous bytes of a row: whole sectors, without a detour through shared
+      // memory (through the 32x32b shape, one row a lane, every store touched 32
+      // lines: 11 us a segment instead of 3).
+      const int cq = lane & 3;
+      float inv4[4];  // of rows 8 i + lane / 4
+#pragma unroll
+      for (int i = 0; i < 4; ++i) inv4[i] = __shfl_sync(0xffffffffu, inv, 8 * i + (lane >> 2));
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
+        const int half = cc & 1, col = 64 * (cc >> 1);  // 16 rows x 64 columns
         uint32_t o[32];
-        ptx::tmem_ld32(tmem + lanes + TM_O + 128 * ch + 32 * cc, o);
+        ptx::tmem_ld16x256b_x8(tmem + lanes + ((uint32_t)(16 * half) << 16) + TM_O + 128 * ch + col, o);
         ptx::tmem_ld_wait();
-        if (final) {
 #pragma unroll
-          for (int i = 0; i < 32; i += 2)
-            o[i / 2] = pack_bf16(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+        for (int e = 0; e < 2; ++e) {
+          const int rr = 16 * half + 8 * e + (lane >> 2);
+          const float by = half ? inv4[2 + e] : inv4[e];
+          if (rr >= rows_left) continue;
+          if (final) {
+            uint16_t* dst = p.out + ((size_t)w.rb * mla::kRowTile + local0 + rr) * mla::kDV + dim0 + col + 2 * cq;
 #pragma unroll
-          for (int v = 0; v < 4; ++v)
-            st_shared(stage + lane * 64 + ((v ^ ((lane >> 1) & 3)) * 16), o[4 * v], o[4 * v + 1],
-                      o[4 * v + 2], o[4 * v + 3]);
-          __syncwarp();
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<uint32_t*>(dst + 8 * j) =
+                  pack_bf16(__uint_as_float(o[4 * j + 2 * e]) * by, __uint_as_float(o[4 * j + 2 * e + 1]) * by);
+          } else {
+            float* dst = p.part_o + (seg + local0 + rr) * mla::kDV + dim0 + col + 2 * cq;
 #pragma unroll
-          for (int v = 0; v < 4; ++v) {
-            const int rr = 8 * v + (lane >> 2), c4 = lane & 3;
-            const uint4 x = ld_shared(stage + rr * 64 + ((c4 ^ ((rr >> 1) & 3)) * 16));
-            if (rr < rows_left)
-              *reinterpret_cast<uint4*>(p.out + ((size_t)w.rb * mla::kRowTile + local0 + rr) * mla::kDV +
-                                        dim0 + 32 * cc + 8 * c4) = x;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * inv);
-#pragma unroll
-          for (int v = 0; v < 8; ++v)
-            st_shared(stage + lane * 128 + ((v ^ (lane & 7)) * 16), o[4 * v], o[4 * v + 1],
-                      o[4 * v + 2], o[4 * v + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int v = 0; v < 8; ++v) {
-            const int rr = 4 * v + (lane >> 3), c8 = lane & 7;
-            const uint4 x = ld_shared(stage + rr * 128 + ((c8 ^ (rr & 7)) * 16));
-            if (rr < rows_left)
-              *reinterpret_cast<uint4*>(p.part_o + (seg + local0 + rr) * mla::kDV + dim0 + 32 * cc +
-                                        4 * c8) = x;
+            for (int j = 0; j < 8; ++j)
+              *reinterpret_cast<float2*>(dst + 8 * j) =
+                  make_float2(__uint_as_float(o[4 * j + 2 * e]) * by, __uint_as_float(o[4 * j + 2 * e + 1]) * by);
           }
         }
-        __syncwarp();
       }
       if (lane < rows_left && kg == 0) {
         if (final) p.lse[row] = lse;
