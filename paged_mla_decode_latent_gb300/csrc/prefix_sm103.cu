@@ -283,7 +283,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     };
     auto scores = [&](int t) {
       const int y = w.key_row(t) + 128 * (int)rank;
-#pragma unroll 1
+#pragma unroll 3
       for (int d = 0; d < 9; ++d) {
         reserve();
         if (ok && leader)
@@ -304,7 +304,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int t = w.t0; t < w.t1; ++t) {
         if (t + 1 < w.t1) scores(t + 1);
         const int y = w.key_row(t);
-#pragma unroll 1
+#pragma unroll 4
         for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, dims 128 (v % 2) of the CTA's half
           reserve();
           if (ok && leader)
@@ -387,7 +387,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           // O is free once the segment before is read.
           if (t == 1 && seg > 0 && !pass(ptx::smem_u32(&bars.o_free), (seg - 1) & 1)) goto mma_end;
           if (!pass(ptx::smem_u32(&bars.p_full), (it - 1 - (t < n)) & 1)) goto mma_end;
-#pragma unroll 4
+#pragma unroll 8
           for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, O columns 128 (v % 2)
             if (!take()) goto mma_end;
             if (leader) {
