@@ -449,7 +449,7 @@ def prefix_fwd(p: PrefixPlan, q, kv_cache, kv_scale, prefix_table, block_table, 
         p, q.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
         None if kv_scale is None else kv_scale.data_ptr(),
         prefix_table.data_ptr() if prefix else None, block_table.data_ptr() if own else None,
-        _row_stride(block_table) if own else 0, seq_lens.data_ptr(), softmax_scale,
+        _row_stride(block_table) if own else 0, seq_lens.data_ptr(), float(softmax_scale),
         out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
         workspace.numel() * workspace.element_size(), _raw_stream(stream, dev))
     _raise(st, "mla_decode_prefix_fwd")

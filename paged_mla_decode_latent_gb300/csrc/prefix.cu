@@ -319,6 +319,8 @@ __global__ void __launch_bounds__(256) merge_kernel(MergeParams p) {
     if (part.y == 1 && p.splits == 0) return;  // the same in all warps of a row
   }
   const int n = part.y + p.splits;
+  if (n == 0 && lane == 0 && (g.seq_lens[b] < 0 || g.seq_lens[b] > g.max_ctx))
+    atomicOr(g.status, MLA_DEVFLAG_CTX_RANGE);  // no other kernel has looked
   const size_t pre0 = (size_t)(part.x + j) * mla::kRowTile + r % mla::kRowTile;
   const size_t own0 = (size_t)b * p.splits * g.rows_per_seq + local;
   auto lse_of = [&](int s) -> float {
@@ -490,6 +492,12 @@ int check_plan(const mla_decode_prefix_plan_t* p) {
   return MLA_OK;
 }
 
+// A pair counts its share of the tiles in 32 bits.
+bool share_fits(const mla_decode_prefix_plan_t& p) {
+  return p.prefix_tiles == 0 ||
+         (int64_t)p.row_blocks * (p.prefix_tiles + p.block_keys / mla::kPrefixTile) / p.pairs < (1 << 30);
+}
+
 }  // namespace
 
 extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batch,
@@ -591,6 +599,7 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
       }
     }
     lay_out(&p);
+    if (!share_fits(p)) return MLA_ERR_UNSUPPORTED;
     *plan = p;
   } catch (const std::bad_alloc&) {
     return MLA_ERR_CUDA;
@@ -607,6 +616,7 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
                                      void* stream) {
   const int st = check_plan(plan);
   if (st != MLA_OK) return st;
+  if (!share_fits(*plan)) return MLA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned(workspace, 256) ||
       (int64_t)workspace_bytes < plan->workspace_bytes)
     return MLA_ERR_WORKSPACE;
@@ -630,7 +640,12 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   const bool fp8 = plan->kv_dtype == MLA_KV_FP8_E4M3;
   const uint64_t wait_ns =
       plan->wait_limit_us > 0 ? (uint64_t)plan->wait_limit_us * 1000ull : kDefaultWaitNs;
-  clear_kernel<<<1, 256, 0, s>>>(g.status, 4 + plan->batch + 1);
+  // Without shared keys the next launch is a decode kernel or the merge; the
+  // former flags contexts before its dependency wait, so nothing may overlap.
+  if (plan->prefix_tiles > 0)
+    clear_kernel<<<1, 256, 0, s>>>(g.status, 4 + plan->batch + 1);
+  else if (cudaMemsetAsync(g.status, 0, 16 + 4 * ((size_t)plan->batch + 1), s) != cudaSuccess)
+    return MLA_ERR_CUDA;
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   cudaLaunchAttribute attr[1];  // of the launches that overlap the one before them
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -37,6 +37,7 @@ CASES = {
     "one_row_sequences": (150, 1, 1, [300 + i % 7 * 30 for i in range(150)], 300, 16, FP8, False),
     "own_apart": (3, 1, 128, [100 + 9000, 100 + 90000, 90], 100, 16, BF16, False),
     "own_apart_few_rows": (2, 2, 8, [100 + 140000, 100 + 400], 100, 64, BF16, True),
+    "rows_200_a_sequence": (5, 2, 100, [420 + 60 * i for i in range(5)], 400, 16, BF16, True),
     "own_exact_tiles": (2, 1, 128, [512 + 256, 512 + 512], 512, 16, BF16, False),
 }
 
@@ -271,3 +272,131 @@ def test_a_wait_that_runs_out():
     out, lse, _, status = p.run(t=t, plan=plan, workspace=ws)
     assert status == 0
     assert_close(out, lse, *p.reference(), "after the timeout")
+
+
+@pytest.mark.parametrize("seed", range(16))
+def test_random_shapes(seed):
+    """Heads, tokens, pages, types, prefixes and ragged, short and empty contexts drawn at random."""
+    rng = np.random.default_rng(1000 + seed)
+    heads = int(rng.choice([1, 3, 8, 16, 20, 33, 64, 100, 128]))
+    sq = int(rng.integers(1, 5)) if heads <= 100 else int(rng.integers(1, 3))
+    batch = int(rng.integers(1, 9))
+    prefix = int(np.exp(rng.uniform(0, np.log(1500))))
+    own = int(np.exp(rng.uniform(0, np.log(700))))
+    lens = prefix + rng.integers(0, own + 1, batch)
+    if seed % 3 == 0:
+        lens[int(rng.integers(batch))] = int(rng.integers(0, prefix + 1))
+    p = PrefixProblem(batch, sq, heads, lens, prefix, int(rng.choice([1, 5, 16, 64])),
+                      FP8 if rng.random() < 0.4 else BF16, bool(rng.random() < 0.6), seed=seed,
+                      outlier_frac=0.01 if rng.random() < 0.3 else 0.0)
+    ref, t = p.reference(), p.to_device()
+    for sms in (0, int(rng.integers(2, 40))):
+        out, lse, plan, status = p.run(t=t, num_sms=sms)
+        assert status == 0
+        assert_close(out, lse, *ref, f"seed {seed} {plan.as_dict()}")
+
+
+def test_many_row_blocks():
+    """40960 query rows: 320 row blocks, more than the partition keeps in registers."""
+    p = PrefixProblem(320, 1, 128, [64 + i % 5 for i in range(320)], 64, 16, seed=17)
+    out, lse, plan, status = p.run()
+    assert status == 0 and plan.row_blocks == 320
+    assert_close(out, lse, *p.reference(), "320 row blocks")
+
+
+def test_long_prefix():
+    """70001 shared keys, against the formula in 64 bits on the GPU."""
+    import torch
+    p = PrefixProblem(3, 1, 16, [70001, 70040, 69000], 70001, 64, FP8, seed=18)
+    out, lse, _, status = p.run()
+    assert status == 0
+    flat = torch.from_numpy(p.cache).view(torch.float8_e4m3fn).cuda().reshape(-1, 576)
+    q = torch.from_numpy(p.q_bits.view(np.int16)).view(torch.bfloat16).cuda().double()
+    for b in range(3):
+        k = flat[torch.from_numpy(p.slots[b, :p.lens[b]].astype(np.int64)).cuda()].double() * p.kv_scale
+        z = q[b, 0] @ k.t() * p.scale
+        ref_l = torch.logsumexp(z, 1)
+        ref_o = torch.exp(z - ref_l[:, None]) @ k[:, :512]
+        assert_close(out[b, 0], lse[b, 0], ref_o.cpu().numpy(), ref_l.cpu().numpy(), f"sequence {b}")
+
+
+def test_cache_beyond_4_gb():
+    """Pages whose byte offsets pass 32 bits, shared and own."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(2, 1, 16, [300, 333], 290, 16, seed=19)
+    t, plan = p.to_device(), p.plan()
+    n, shift = t["cache"].shape[0], 240_000
+    big = torch.zeros(shift + n, 16, 576, dtype=torch.bfloat16, device="cuda")
+    big[shift:] = t["cache"]
+    t["cache"] = big
+    t["pt"] += shift
+    t["bt"][t["bt"] >= 0] += shift
+    out, lse, _, status = p.run(t=t, plan=plan)
+    assert status == 0
+    assert_close(out, lse, *p.reference(), "far pages")
+
+
+def test_two_streams_at_once():
+    """Two calls in flight, each with its workspace."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    ps = [PrefixProblem(6, 1, 128, [2000 + 7 * i for i in range(6)], 1990, 16, seed=20 + k) for k in range(2)]
+    ts, plans = [p.to_device() for p in ps], [p.plan() for p in ps]
+    wss = [mla.workspace_for(x) for x in plans]
+    outs = [torch.empty(6, 1, 128, 512, dtype=torch.bfloat16, device="cuda") for _ in ps]
+    lses = [torch.empty(6, 1, 128, device="cuda") for _ in ps]
+    streams = [torch.cuda.Stream() for _ in ps]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for k, p in enumerate(ps):
+            mla.prefix_fwd(plans[k], ts[k]["q"], ts[k]["cache"], None, ts[k]["pt"], ts[k]["bt"],
+                           ts[k]["lens"], p.scale, outs[k], lses[k], wss[k], stream=streams[k])
+    for k, p in enumerate(ps):
+        assert mla.prefix_check(plans[k], wss[k], stream=streams[k]) == 0
+        assert_close(outs[k].double().cpu().numpy(), lses[k].double().cpu().numpy(), *p.reference(), f"stream {k}")
+
+
+def test_contexts_are_flagged_without_a_prefix_too():
+    import paged_mla_decode_latent_gb300 as mla
+    for lens in ([40, 60], [0, 0]):
+        p = PrefixProblem(2, 1, 16, lens, 0, 16, seed=23)
+        t, plan = p.to_device(), p.plan()
+        t["lens"][1] = 61
+        assert p.run(t=t, plan=plan)[3] == mla.DEVFLAG_CTX_RANGE
+        t["lens"][1] = -1
+        out, lse, _, status = p.run(t=t, plan=plan)
+        assert status == mla.DEVFLAG_CTX_RANGE
+        assert np.all(out[1] == 0) and np.all(np.isneginf(lse[1]))
+
+
+def test_refusals_of_the_binding():
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(2, 1, 16, [300, 290], 256, 16, seed=24)
+    plan = p.plan()
+    good = p.to_device()
+    out = torch.empty(2, 1, 16, 512, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(2, 1, 16, device="cuda")
+    ws = mla.workspace_for(plan)
+
+    def call(**kw):
+        a = dict(good, out=out, lse=lse, ws=ws)
+        a.update(kw)
+        mla.prefix_fwd(plan, a["q"], a["cache"], None, a["pt"], a["bt"], a["lens"], p.scale, a["out"],
+                       a["lse"], a["ws"])
+
+    call()
+    bad = [dict(q=good["q"].float()), dict(q=good["q"][:1]), dict(q=good["q"].cpu()),
+           dict(q=good["q"].expand(2, 1, 16, 576).transpose(0, 2).contiguous().transpose(0, 2)),
+           dict(cache=good["cache"][:, :8]), dict(cache=good["cache"].to(torch.float16)),
+           dict(pt=good["pt"][:15]), dict(pt=good["pt"].long()), dict(pt=None), dict(bt=None),
+           dict(bt=good["bt"][:, :18]), dict(bt=good["bt"][:1]), dict(lens=good["lens"].long()),
+           dict(lens=good["lens"][:1]), dict(out=out.float()), dict(lse=lse.half()), dict(out=out[..., :511])]
+    for kw in bad:
+        with pytest.raises(mla.MLADecodeError) as e:
+            call(**kw)
+        assert e.value.status == mla.ERR_INVALID_ARG, kw
+    with pytest.raises(mla.MLADecodeError) as e:
+        call(ws=ws[:1000])
+    assert e.value.status == mla.ERR_WORKSPACE
