@@ -75,20 +75,12 @@ __device__ __forceinline__ uint4 to_f16(uint4 v, bool fp8) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// A value that f16 cannot hold is staged as zero, and its key remembered.
-__device__ __noinline__ uint4 drop_bad(const StageParams& p, uint4 v, int key, int who) {
-  uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  for (int i = 0; i < 4; ++i) {
-    if ((w[i] & 0x7C00u) == 0x7C00u) w[i] &= 0xFFFF0000u;
-    if ((w[i] & 0x7C000000u) == 0x7C000000u) w[i] &= 0xFFFFu;
-  }
-  atomicOr(p.g.status, MLA_DEVFLAG_KV_RANGE);
-  atomicMax(p.g.bad + who, 0x7FFFFFFF - key);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
+__device__ __forceinline__ __half2 abs2(uint32_t w) { return __habs2(*reinterpret_cast<const __half2*>(&w)); }
 
-__device__ __forceinline__ bool any_bad(uint4 v) {
-  return not_finite(v.x) || not_finite(v.y) || not_finite(v.z) || not_finite(v.w);
+__device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
+  if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
+  if ((w & 0x7C000000u) == 0x7C000000u) w &= 0xFFFFu;
+  return w;
 }
 
 // The tiles before each row block, where each pair starts and where each
@@ -264,14 +256,26 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   ptx::grid_dependency_wait();  // the words that flags go to are cleared
   if (bad_page) atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
   uint4* out = reinterpret_cast<uint4*>(dst + (dst_row + row) * MLA_D_QK) + sub;
+  __half2 top = __floats2half2_rn(0.f, 0.f);  // largest magnitude; NaN if there is one
 #pragma unroll
   for (int i = 0; i < kStageIters; ++i) {
-    v[i] = to_f16(v[i], fp8);
-    if (any_bad(v[i])) {
-      if (src == nullptr) v[i] = drop_bad(p, v[i], key0 + row, who);
-      else atomicOr(g.status, MLA_DEVFLAG_Q_RANGE);  // spoils its own row only
-    }
-    out[8 * i] = v[i];
+    const uint4 w = to_f16(v[i], fp8);
+    out[8 * i] = w;
+    top = __hmax2_nan(top, __hmax2_nan(__hmax2_nan(abs2(w.x), abs2(w.y)), __hmax2_nan(abs2(w.z), abs2(w.w))));
+  }
+  if (!not_finite(*reinterpret_cast<const uint32_t*>(&top))) return;
+  // Rare: a query value spoils its own row only; a key is staged anew without
+  // what f16 cannot hold.
+  if (src != nullptr) {
+    atomicOr(g.status, MLA_DEVFLAG_Q_RANGE);
+    return;
+  }
+  atomicOr(g.status, MLA_DEVFLAG_KV_RANGE);
+  atomicMax(g.bad + who, 0x7FFFFFFF - (key0 + row));
+#pragma unroll 1
+  for (int i = 0; i < kStageIters; ++i) {
+    const uint4 w = out[8 * i];
+    out[8 * i] = make_uint4(finite_or_zero(w.x), finite_or_zero(w.y), finite_or_zero(w.z), finite_or_zero(w.w));
   }
 }
 
