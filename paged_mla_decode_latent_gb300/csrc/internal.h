@@ -74,11 +74,16 @@ constexpr int kPrefixTile = 256;  // keys per tile
 // one: pair i takes [start(i), start(i + 1)).
 struct PrefixShares {
   int64_t q, r;
-  __host__ __device__ PrefixShares(int64_t total, int pairs) : q(total / pairs), r(total % pairs) {}
+  // A 64-bit division takes about a thousand cycles on the device; few totals need one.
+  __host__ __device__ static int64_t div(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+  }
+  __host__ __device__ PrefixShares(int64_t total, int pairs)
+      : q(div(total, pairs)), r(total - div(total, pairs) * pairs) {}
   __host__ __device__ int64_t start(int64_t i) const { return i * q + (i < r ? i : r); }
   __host__ __device__ int pair_of(int64_t x) const {  // the pair that holds tile x
     const int64_t big = r * (q + 1);  // the tiles of the longer shares
-    return (int)(x < big ? x / (q + 1) : r + (x - big) / q);
+    return (int)(x < big ? div(x, q + 1) : r + div(x - big, q));
   }
 };
 
@@ -121,11 +126,10 @@ struct PrefixShape {
     return n > 0x7FFFFFFF - max(bad[b], bad[batch]);
   }
   __device__ __forceinline__ int first_seq(int block) const {
-    return (int)((int64_t)block * kRowTile / rows_per_seq);
+    return (int)((uint32_t)(block * kRowTile) / (uint32_t)rows_per_seq);
   }
   __device__ __forceinline__ int last_seq(int block) const {
-    const int64_t r = (int64_t)(block + 1) * kRowTile - 1;
-    return (int)((r < rows ? r : rows - 1) / rows_per_seq);
+    return (int)((uint32_t)(min((block + 1) * kRowTile, rows) - 1) / (uint32_t)rows_per_seq);
   }
 #endif
 };
