@@ -70,7 +70,12 @@ struct CombineParams {
 
 constexpr int kPrefixTile = 256;  // keys per tile
 
-// `total` tiles dealt to pairs in contiguous shares that differ by at most
+// A pair that meets a row block's start inside its share pays for one more
+// segment (output of the one before, query rows, first softmax: 4.5 us, the
+// time of two tiles, measured), so a row block of n tiles counts for n + 2.
+constexpr int kSegmentTiles = 2;
+
+// `total` such units dealt to pairs in contiguous shares that differ by at most
 // one: pair i takes [start(i), start(i + 1)).
 struct PrefixShares {
   int64_t q, r;
@@ -81,8 +86,8 @@ struct PrefixShares {
   __host__ __device__ PrefixShares(int64_t total, int pairs)
       : q(div(total, pairs)), r(total - div(total, pairs) * pairs) {}
   __host__ __device__ int64_t start(int64_t i) const { return i * q + (i < r ? i : r); }
-  __host__ __device__ int pair_of(int64_t x) const {  // the pair that holds tile x
-    const int64_t big = r * (q + 1);  // the tiles of the longer shares
+  __host__ __device__ int pair_of(int64_t x) const {  // the pair that holds unit x
+    const int64_t big = r * (q + 1);  // the units of the longer shares
     return (int)(x < big ? div(x, q + 1) : r + div(x - big, q));
   }
 };
@@ -91,10 +96,11 @@ struct PrefixShares {
 // of its rows, keys and partition.
 struct PrefixShape {
   const int32_t* seq_lens;  // [B]
-  int64_t* first_tile;      // [row blocks + 1]: the tiles before each row block
-  // [pairs]: the row block and the tile of it at which a pair starts, the row
-  // block's tiles and the pair's share
+  // [pairs + 1]: the row block and the tile of it at which a pair starts, and
+  // the row block's tiles; the end
   int4* pair_start;
+  int64_t* first_unit;      // [row blocks]: the units before each
+  int32_t* block_tiles;     // [row blocks]
   int2* parts;              // [row blocks]: the first pair that holds a part of one, and their number
   int32_t* own_off;         // [row blocks, block_seqs]: a sequence's first own key in its block's
   // [B + 1]: 2^31 - 1 - (first key of the sequence's own, and of the shared

@@ -83,8 +83,8 @@ __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
   return w;
 }
 
-// The tiles before each row block, where each pair starts and where each
-// sequence's own keys lie in its row blocks' regions.
+// The tiles of each row block, where each pair starts and where each sequence's
+// own keys lie in its row blocks' regions.
 __device__ void partition(const StageParams& p) {
   __shared__ int64_t warp_sum[kStageThreads / 32];
   __shared__ int64_t carry_s;
@@ -92,7 +92,8 @@ __device__ void partition(const StageParams& p) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) carry_s = 0;
   __syncthreads();
-  int64_t mine = 0, mine_n = 0;
+  int64_t mine = 0;
+  int mine_n = 0;
   for (int j0 = 0; j0 < g.row_blocks; j0 += kStageThreads) {
     const int j = j0 + threadIdx.x;
     int64_t n = 0;
@@ -111,7 +112,9 @@ __device__ void partition(const StageParams& p) {
           }
         }
       }
-      n = g.tiles + (own + mla::kPrefixTile - 1) / mla::kPrefixTile;
+      const int tiles = g.tiles + (own + mla::kPrefixTile - 1) / mla::kPrefixTile;
+      g.block_tiles[j] = tiles;
+      n = tiles + mla::kSegmentTiles;
     }
     int64_t x = n;  // inclusive scan over the threads
     for (int o = 1; o < 32; o <<= 1) {
@@ -124,9 +127,8 @@ __device__ void partition(const StageParams& p) {
     for (int k = 0; k < warp; ++k) before += warp_sum[k];
     if (j < g.row_blocks) {
       mine = before + x - n;
-      mine_n = n;
-      g.first_tile[j] = before + x - n;
-      if (j == g.row_blocks - 1) g.first_tile[j + 1] = before + x;
+      mine_n = (int)n;
+      g.first_unit[j] = mine;
     }
     __syncthreads();
     if (threadIdx.x == kStageThreads - 1) carry_s = before + x;
@@ -135,16 +137,21 @@ __device__ void partition(const StageParams& p) {
   const mla::PrefixShares shares(carry_s, g.pairs);
   for (int j = threadIdx.x; j < g.row_blocks; j += kStageThreads) {
     // One batch of row blocks is still in registers.
-    const int64_t a = g.row_blocks <= kStageThreads ? mine : g.first_tile[j];
-    const int64_t z = g.row_blocks <= kStageThreads ? mine + mine_n : g.first_tile[j + 1];
-    const int first = shares.pair_of(a), last = shares.pair_of(z - 1);
+    const bool here = g.row_blocks <= kStageThreads;
+    const int64_t a = here ? mine : g.first_unit[j];
+    const int tiles = here ? mine_n - mla::kSegmentTiles : g.block_tiles[j];
+    // Tile t of the block is unit a + kSegmentTiles + t; a share that starts in
+    // the units before starts at tile 0.
+    const int first = shares.pair_of(a + mla::kSegmentTiles);
+    const int last = shares.pair_of(a + mla::kSegmentTiles + tiles - 1);
     g.parts[j] = make_int2(first, last - first + 1);
-    for (int i = first; i <= last; ++i) {
+    for (int i = last; i >= 0; --i) {
       const int64_t s = shares.start(i);
-      if (s >= a)
-        g.pair_start[i] = make_int4(j, (int)(s - a), (int)(z - a), (int)(shares.start(i + 1) - s));
+      if (s < a) break;
+      g.pair_start[i] = make_int4(j, (int)max((int64_t)0, s - a - mla::kSegmentTiles), tiles, 0);
     }
   }
+  if (threadIdx.x == 0) g.pair_start[g.pairs] = make_int4(g.row_blocks, 0, 0, 0);
   ptx::grid_dependency_wait();  // the status word is cleared
   // Contexts out of range, once per sequence.
   for (int b = threadIdx.x; b < g.batch; b += kStageThreads)
@@ -411,9 +418,10 @@ mla::PrefixShape shape_of(const mla_decode_prefix_plan_t& p, const int32_t* seq_
   g.status = reinterpret_cast<int32_t*>(ws + p.ws_status_offset);
   g.bad = g.status + 4;
   g.pair_start = reinterpret_cast<int4*>(ws + p.ws_partition_offset);
-  g.first_tile = reinterpret_cast<int64_t*>(g.pair_start + p.pairs);
-  g.parts = reinterpret_cast<int2*>(g.first_tile + p.row_blocks + 1);
-  g.own_off = reinterpret_cast<int32_t*>(g.parts + p.row_blocks);
+  g.first_unit = reinterpret_cast<int64_t*>(g.pair_start + p.pairs + 1);
+  g.parts = reinterpret_cast<int2*>(g.first_unit + p.row_blocks);
+  g.block_tiles = reinterpret_cast<int32_t*>(g.parts + p.row_blocks);
+  g.own_off = g.block_tiles + p.row_blocks;
   g.rows = p.total_rows;
   g.rows_per_seq = p.rows;
   g.heads = p.num_heads;
@@ -451,7 +459,7 @@ void lay_out(mla_decode_prefix_plan_t* p) {
   const int64_t segments = p->prefix_tiles > 0 ? (int64_t)p->row_blocks + p->pairs : 0;
   const int64_t keys = (int64_t)p->prefix_tiles * mla::kPrefixTile + (int64_t)p->row_blocks * p->block_keys;
   p->ws_status_offset = take(16 + 4 * ((int64_t)p->batch + 1));
-  p->ws_partition_offset = take(16 * (int64_t)p->row_blocks + 8 + 16 * (int64_t)p->pairs +
+  p->ws_partition_offset = take(20 * (int64_t)p->row_blocks + 16 * ((int64_t)p->pairs + 1) +
                                 (p->own_folded ? 4ll * p->row_blocks * seqs : 0));
   p->ws_keys_offset = take(p->prefix_tiles > 0 ? keys * MLA_D_QK * 2 : 0);
   p->ws_q_offset = take(p->prefix_tiles > 0 ? (int64_t)p->total_rows * MLA_D_QK * 2 : 0);
@@ -494,12 +502,6 @@ int check_plan(const mla_decode_prefix_plan_t* p) {
     return MLA_ERR_INVALID_ARG;
   if (p->own_chunk % p->key_tile != 0) return MLA_ERR_INVALID_ARG;
   return MLA_OK;
-}
-
-// A pair counts its share of the tiles in 32 bits.
-bool share_fits(const mla_decode_prefix_plan_t& p) {
-  return p.prefix_tiles == 0 ||
-         (int64_t)p.row_blocks * (p.prefix_tiles + p.block_keys / mla::kPrefixTile) / p.pairs < (1 << 30);
 }
 
 }  // namespace
@@ -546,7 +548,7 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
 
     // Measured on GB300 (us): a 256-key tile on one pair, a segment's query
     // rows, first softmax, last values and output, and the merge of cut rows.
-    constexpr double kTile = 2.4, kSegment = 4.0, kMergeFixed = 1.5, kMergeRow = 4096.0 / 4.0e6;
+    constexpr double kTile = 2.4, kSegment = 4.7, kMergeFixed = 1.5, kMergeRow = 4096.0 / 4.0e6;
     const int pairs = std::min(std::max(1, d.num_sms / 2), kMaxPairs);
     std::vector<int64_t> first(p.row_blocks + 1, 0);  // tiles before each row block, own folded in
     const int seqs = block_seqs(total_rows, p.rows);
@@ -577,23 +579,29 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
       else for (int j = 0; j <= p.row_blocks; ++j) first[j] = (int64_t)j * p.prefix_tiles;
       // Pairs that share the tiles: the count with the smallest longest pair,
       // merge included.  With many row blocks all pairs are busy anyway.
-      const int64_t total = first[p.row_blocks];
       const int most = (int)std::min<int64_t>(pairs, (int64_t)p.row_blocks * p.prefix_tiles);
+      const int64_t total = first[p.row_blocks] + (int64_t)p.row_blocks * mla::kSegmentTiles;
       double best = 1e300;
       for (int n = p.row_blocks > 1024 ? most : 1; n <= most; ++n) {
+        const mla::PrefixShares shares(total, n);
         double worst = 0.0;
         int64_t cut_parts = 0;
-        int j = 0;
-        const mla::PrefixShares shares(total, n);
+        int j = 0;  // row block of the unit where a share starts
+        auto unit = [&](int k) { return first[k] + (int64_t)k * mla::kSegmentTiles; };
+        auto tile_at = [&](int k, int64_t u) {  // tiles of row block k before unit u
+          return std::min(std::max<int64_t>(0, u - unit(k) - mla::kSegmentTiles), first[k + 1] - first[k]);
+        };
         for (int i = 0; i < n; ++i) {
           const int64_t a = shares.start(i), z = shares.start(i + 1);
-          while (first[j + 1] <= a) ++j;
-          int64_t segs = 0;
-          for (int k = j; k < p.row_blocks && first[k] < z; ++k) {
-            ++segs;
-            cut_parts += a > first[k] || z < first[k + 1];
+          while (j + 1 < p.row_blocks && unit(j + 1) <= a) ++j;
+          double cost = 0.0;
+          for (int k = j; k < p.row_blocks && unit(k) < z; ++k) {
+            const int64_t tiles = tile_at(k, z) - tile_at(k, a);
+            if (tiles == 0) continue;
+            cost += kTile * (double)tiles + kSegment;
+            cut_parts += tiles < first[k + 1] - first[k];
           }
-          worst = std::max(worst, kTile * (double)(z - a) + kSegment * (double)segs);
+          worst = std::max(worst, cost);
         }
         if (cut_parts > 0) worst += kMergeFixed + kMergeRow * mla::kRowTile * (double)cut_parts;
         if (worst < best) {
@@ -603,7 +611,6 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
       }
     }
     lay_out(&p);
-    if (!share_fits(p)) return MLA_ERR_UNSUPPORTED;
     *plan = p;
   } catch (const std::bad_alloc&) {
     return MLA_ERR_CUDA;
@@ -620,7 +627,6 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
                                      void* stream) {
   const int st = check_plan(plan);
   if (st != MLA_OK) return st;
-  if (!share_fits(*plan)) return MLA_ERR_UNSUPPORTED;
   if (workspace == nullptr || !aligned(workspace, 256) ||
       (int64_t)workspace_bytes < plan->workspace_bytes)
     return MLA_ERR_WORKSPACE;

@@ -187,25 +187,28 @@ __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, 
 // 459 us at batch 128 x 23333): tiles [t0, t1) of row block rb, which has n.
 struct Walk {
   const mla::PrefixShape& g;
-  int left, next_rb, next_t, next_n;
+  int next_rb, next_t, next_n, end_rb, end_t;
   int rb, t0, t1, n;
   __device__ __forceinline__ Walk(const mla::PrefixShape& shape, int pair) : g(shape) {
-    const int4 s = g.pair_start[pair];
+    const int4 s = g.pair_start[pair], e = g.pair_start[pair + 1];
     next_rb = uniform(s.x);
     next_t = uniform(s.y);
     next_n = uniform(s.z);
-    left = uniform(s.w);
+    end_rb = uniform(e.x);
+    end_t = uniform(e.y);
+  }
+  __device__ __forceinline__ bool more() const {
+    return next_rb < end_rb || (next_rb == end_rb && next_t < end_t);
   }
   __device__ __forceinline__ bool next() {
-    if (left <= 0) return false;
+    if (!more()) return false;
     rb = next_rb;
     t0 = next_t;
     n = next_n;
-    t1 = min(n, t0 + left);
-    left -= t1 - t0;
+    t1 = rb == end_rb ? end_t : n;
     next_rb = rb + 1;
     next_t = 0;
-    if (left > 0) next_n = uniform((int)(g.first_tile[rb + 2] - g.first_tile[rb + 1]));
+    if (more()) next_n = uniform(g.block_tiles[next_rb]);
     return true;
   }
   // The staged key that tile t starts at.

@@ -47,7 +47,7 @@ def test_plan(batch, heads, sq, prefix, own, sms):
             p.ws_prefix_o_offset, p.ws_prefix_lse_offset, p.ws_own_o_offset, p.ws_own_lse_offset,
             p.workspace_bytes]
     sizes = [16 + 4 * (batch + 1),
-             16 * p.row_blocks + 8 + 16 * p.pairs + (4 * p.row_blocks * seqs if p.own_folded else 0),
+             20 * p.row_blocks + 16 * (p.pairs + 1) + (4 * p.row_blocks * seqs if p.own_folded else 0),
              keys * 1152 if prefix else 0, p.total_rows * 1152 if prefix else 0,
              segments * 128 * 2048, segments * 128 * 4,
              p.own_splits * p.total_rows * 2048, p.own_splits * p.total_rows * 4]
