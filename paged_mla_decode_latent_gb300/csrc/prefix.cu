@@ -387,7 +387,7 @@ __global__ void __launch_bounds__(256) merge_kernel(MergeParams p) {
     }
   }
   float L = sum > 0.f ? m + logf(sum) : -INFINITY, inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (sum != sum || g.sees_bad(b, g.visible(r, b))) L = inv = NAN;
+  if (sum != sum || g.sees_bad(b, g.visible(r, b))) L = inv = NAN;  // a NaN partial, a bad key
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);

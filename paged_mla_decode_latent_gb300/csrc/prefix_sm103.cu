@@ -531,8 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // A row block that this pair holds whole is final; another's goes to the
       // partial of this segment, pair + row block.
       const bool final = !p.partials && w.t0 == 0 && w.t1 == w.n;
-      float inv = l > 0.f ? s_kv / l : 0.f;
-      float lse = l > 0.f ? (m - kHead + log2f(l)) * 0.6931471805599453f : -INFINITY;
+      // No key: 0 and -inf.  A sum that is NaN (a query that f16 cannot hold) stays so.
+      float inv = l == 0.f ? 0.f : s_kv / l;
+      float lse = l == 0.f ? -INFINITY : (m - kHead + log2f(l)) * 0.6931471805599453f;
       if (final && row < p.g.rows && p.g.sees_bad(b, n_vis)) inv = lse = NAN;
       const size_t seg = (size_t)(pair + w.rb) * mla::kRowTile;
       const int local0 = 64 * (int)rank + 32 * (q4 & 1);  // the warp's first row of the block

@@ -239,14 +239,17 @@ def test_a_causal_token_before_a_bad_key_stays():
         assert_close(out[b, i], lse[b, i], ref[0][b, i], ref[1][b, i], f"{b} {i}")
 
 
-def test_queries_beyond_f16_spoil_their_row():
+@pytest.mark.parametrize("value", [70000.0, float("nan"), float("inf")])
+@pytest.mark.parametrize("prefix,sms", [(256, 0), (256, 2), (3000, 0)])
+def test_queries_beyond_f16_spoil_their_row(value, prefix, sms):
+    """NaN, not an empty row's zeros; in a whole row block and in a cut one."""
     import paged_mla_decode_latent_gb300 as mla
-    p = PrefixProblem(2, 1, 16, [300, 290], 256, 16, seed=13)
+    p = PrefixProblem(2, 1, 16, [prefix + 44, prefix + 34], prefix, 16, seed=13)
     ref, t = p.reference(), p.to_device()
-    t["q"][1, 0, 3, 5] = 70000.0
-    out, lse, _, status = p.run(t=t)
+    t["q"][1, 0, 3, 5] = value
+    out, lse, _, status = p.run(t=t, num_sms=sms)
     assert status == mla.DEVFLAG_Q_RANGE
-    assert not np.isfinite(out[1, 0, 3]).all()
+    assert np.isnan(out[1, 0, 3]).all() and np.isnan(lse[1, 0, 3])
     rest = [h for h in range(16) if h != 3]
     assert_close(out[1, 0, rest], lse[1, 0, rest], ref[0][1, 0, rest], ref[1][1, 0, rest], "the other heads")
     assert_close(out[0], lse[0], ref[0][0], ref[1][0], "the other sequence")
