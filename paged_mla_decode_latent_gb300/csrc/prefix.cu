@@ -37,7 +37,9 @@ constexpr int kStageIters = kChunk * kPieces / kStageThreads;  // 9 pieces a thr
 static_assert(kStageThreads == 8 * kChunk, "eight threads a row");
 constexpr int kPadChunks = mla::kPrefixTile / kChunk;
 constexpr int kManyParts = 8;  // partials a row from which the merge takes eight warps a row
-constexpr int64_t kMaxOwnRows = 1 << 18;  // own keys that are folded in at most (302 MB staged)
+// Own keys are folded in while they are at most this many, and their row
+// blocks' regions (whole tiles) at most that many rows of 1152 bytes.
+constexpr int64_t kMaxOwnRows = 1 << 18, kMaxRegionRows = 1 << 20;
 
 struct StageParams {
   mla::PrefixShape g;
@@ -411,6 +413,13 @@ int block_seqs(int64_t rows, int rows_per_seq) {
   return (int)std::min<int64_t>(batch, (mla::kRowTile + rows_per_seq - 2) / rows_per_seq + 1);
 }
 
+bool room_to_fold(int64_t batch, int rows, int64_t own) {
+  const int64_t blocks = ceil_div(batch * rows, mla::kRowTile);
+  const int64_t keys = own * block_seqs(batch * rows, rows);
+  return blocks * keys <= kMaxOwnRows &&
+         blocks * ceil_div(keys, mla::kPrefixTile) * mla::kPrefixTile <= kMaxRegionRows;
+}
+
 mla::PrefixShape shape_of(const mla_decode_prefix_plan_t& p, const int32_t* seq_lens, char* ws) {
   mla::PrefixShape g;
   std::memset(&g, 0, sizeof g);
@@ -486,9 +495,7 @@ int check_plan(const mla_decode_prefix_plan_t* p) {
     return MLA_ERR_INVALID_ARG;
   const int64_t own = std::max(0, p->max_ctx - p->prefix_len);
   if (p->own_folded ? p->prefix_len == 0 || p->own_splits != 0 ||
-                          ceil_div((int64_t)p->batch * p->num_heads * p->sq, mla::kRowTile) * own *
-                                  block_seqs((int64_t)p->batch * p->num_heads * p->sq, p->num_heads * p->sq) >
-                              kMaxOwnRows
+                          !room_to_fold(p->batch, p->num_heads * p->sq, own)
                     : (int64_t)p->own_splits * p->own_chunk < own)
     return MLA_ERR_INVALID_ARG;
   // Everything else is what lay_out makes of these: a plan whose other fields
@@ -551,7 +558,6 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
     constexpr double kTile = 2.4, kSegment = 4.7, kMergeFixed = 1.5, kMergeRow = 4096.0 / 4.0e6;
     const int pairs = std::min(std::max(1, d.num_sms / 2), kMaxPairs);
     std::vector<int64_t> first(p.row_blocks + 1, 0);  // tiles before each row block, own folded in
-    const int seqs = block_seqs(total_rows, p.rows);
     for (int j = 0; j < p.row_blocks; ++j) {
       const int b0 = (int)((int64_t)j * mla::kRowTile / p.rows);
       const int b1 = (int)((std::min<int64_t>((int64_t)(j + 1) * mla::kRowTile, total_rows) - 1) / p.rows);
@@ -573,8 +579,8 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
       separate = std::max(longest, separate / pairs) + kMergeFixed;
       const double folded =
           kTile * (double)(first[p.row_blocks] - (int64_t)p.row_blocks * p.prefix_tiles) / pairs;
-      const int64_t room = (int64_t)p.row_blocks * seqs * std::max(0, max_ctx - prefix_len);
-      p.own_folded = max_ctx > prefix_len && room <= kMaxOwnRows && folded <= separate;
+      p.own_folded = max_ctx > prefix_len && folded <= separate &&
+                     room_to_fold(batch, p.rows, max_ctx - prefix_len);
       if (p.own_folded) p.own_splits = 0;
       else for (int j = 0; j <= p.row_blocks; ++j) first[j] = (int64_t)j * p.prefix_tiles;
       // Pairs that share the tiles: the count with the smallest longest pair,

@@ -61,6 +61,13 @@ def test_own_keys_fold_in_or_not():
     assert mla.prefix_plan([1024 + 100000] * 16, 1024, 128, 1, 16, 0, False, 152).own_folded == 0
 
 
+def test_folded_regions_stay_small():
+    """Thousands of row blocks: a tile each for a key each would take gigabytes."""
+    assert mla.prefix_plan([101] * 4000, 100, 128, 1, 16, 0, False, 152).own_folded == 1
+    p = mla.prefix_plan([101] * 8000, 100, 128, 1, 16, 0, False, 152)
+    assert p.own_folded == 0 and p.own_splits == 1
+
+
 def test_struct_layout():
     assert ctypes.sizeof(mla.PrefixPlan) == 22 * 4 + 9 * 8
 
