@@ -531,7 +531,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // A row block that this pair holds whole is final; another's goes to the
       // partial of this segment, pair + row block.
       const bool final = !p.partials && w.t0 == 0 && w.t1 == w.n;
-      // No key: 0 and -inf.  A sum that is NaN (a query that f16 cannot hold) stays so.
+      // No key: 0 and -inf.  A sum that is NaN (a query that f16 cannot hold) stays
+      // so, and one of zero over keys that the row sees (scores of minus infinity
+      // only, from such a query) becomes it.
+      const int key0 = w.t0 * T, key1 = w.t1 * T, own = p.g.tiles * T;
+      if (l == 0.f && (key0 < min(shared, key1) || max(own + own0, key0) < min(own + own1, key1))) l = NAN;
       float inv = l == 0.f ? 0.f : s_kv / l;
       float lse = l == 0.f ? -INFINITY : (m - kHead + log2f(l)) * 0.6931471805599453f;
       if (final && row < p.g.rows && p.g.sees_bad(b, n_vis)) inv = lse = NAN;

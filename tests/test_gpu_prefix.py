@@ -255,6 +255,22 @@ def test_queries_beyond_f16_spoil_their_row(value, prefix, sms):
     assert_close(out[0], lse[0], ref[0][0], ref[1][0], "the other sequence")
 
 
+@pytest.mark.parametrize("prefix,sms,own", [(256, 0, 44), (256, 2, 44), (3000, 0, 44), (3000, 0, 0), (1, 0, 0)])
+def test_a_query_whose_scores_are_all_minus_infinity_is_no_empty_row(prefix, sms, own):
+    """-70000 times keys that are positive there: f16 makes every score -inf, and the row NaN."""
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(2, 1, 16, [prefix + own, 0], prefix, 16, seed=17)
+    t = p.to_device()
+    t["cache"][:, :, 5] = 1.0
+    t["q"][0, 0, 3, 5] = -70000.0
+    out, lse, _, status = p.run(t=t, num_sms=sms)
+    assert status == mla.DEVFLAG_Q_RANGE
+    assert np.isnan(out[0, 0, 3]).all() and np.isnan(lse[0, 0, 3])
+    rest = [h for h in range(16) if h != 3]
+    assert np.isfinite(out[0, 0, rest]).all() and np.isfinite(lse[0, 0, rest]).all()
+    assert np.all(out[1] == 0) and np.all(np.isneginf(lse[1]))  # no key: still empty
+
+
 def test_small_values():
     """Below 2^-14 the staged values keep an absolute 2^-25: q and cache scaled down."""
     p = PrefixProblem(2, 1, 64, [400, 380], 300, 1, seed=14, q_mult=2.0 ** -9)
