@@ -93,7 +93,34 @@ __device__ __forceinline__ uint32_t e4m3x2(float first, float second) {
   return r;
 }
 
-__global__ void __launch_bounds__(kThreads) rope_epilogue_kernel(RopeParams p) {
+__device__ __noinline__ uint2 divided(float4 a, float4 b, float s) {
+  return make_uint2(e4m3x2(__fdiv_rn(a.x, s), __fdiv_rn(a.y, s)) | e4m3x2(__fdiv_rn(a.z, s), __fdiv_rn(a.w, s)) << 16,
+                    e4m3x2(__fdiv_rn(b.x, s), __fdiv_rn(b.y, s)) | e4m3x2(__fdiv_rn(b.z, s), __fdiv_rn(b.w, s)) << 16);
+}
+
+// The e4m3 codes of the fp32 quotients x / s, without the divisions (72 a
+// thread were 2 of the kernel's 5.4 us at 64 tokens x 128 heads).  With inv the
+// rounded 1 / s, x inv is off by at most 2^-23 of itself and the rounded
+// quotient by 2^-24, so the quotient lies between x inv (1 - 2^-21) and x inv
+// (1 + 2^-21); where both have the same code, it has that one too, since
+// rounding never swaps two values.  Near a border of two codes it is divided
+// out, as with an s whose reciprocal leaves the range (inv = NaN then).  A power
+// of two, whose quotients often are ties, needs no margin: x inv is exact.
+__device__ __forceinline__ uint2 codes(const float (&x)[8], float s, float inv, float margin) {
+  uint32_t lo[4], hi[4];
+  bool differ = inv != inv;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float a = x[2 * k] * inv, b = x[2 * k + 1] * inv;
+    lo[k] = e4m3x2(a * (1.f - margin), b * (1.f - margin));
+    hi[k] = e4m3x2(a * (1.f + margin), b * (1.f + margin));
+    differ |= lo[k] != hi[k];
+  }
+  if (differ) return divided(make_float4(x[0], x[1], x[2], x[3]), make_float4(x[4], x[5], x[6], x[7]), s);
+  return make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
+}
+
+__global__ void __launch_bounds__(kThreads, 4) rope_epilogue_kernel(RopeParams p) {
   const int sub = (int)(threadIdx.x & 7);
   const uint32_t row = blockIdx.x * kRows + (threadIdx.x >> 3);
   // Only inputs that the caller declares older than the kernel before this
@@ -136,6 +163,9 @@ __global__ void __launch_bounds__(kThreads) rope_epilogue_kernel(RopeParams p) {
     }
     if (p.fp8) {
       const float s = *p.kv_scale;
+      const bool near = fabsf(s) >= 0x1p-100f && fabsf(s) <= 0x1p100f;
+      const float inv = near ? __frcp_rn(s) : NAN;
+      const float margin = (__float_as_uint(s) & 0x7FFFFFu) == 0 ? 0.f : 0x1p-21f;
       uint2* dst = reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.cache) + slot * MLA_D_QK) + sub;
 #pragma unroll
       for (int i = 0; i < 9; ++i) {
@@ -151,10 +181,7 @@ __global__ void __launch_bounds__(kThreads) rope_epilogue_kernel(RopeParams p) {
 #pragma unroll
           for (int k = 0; k < 8; ++k) x[k] = o[k];
         }
-#pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = __fdiv_rn(x[k], s);
-        dst[8 * i] = make_uint2(e4m3x2(x[0], x[1]) | e4m3x2(x[2], x[3]) << 16,
-                                e4m3x2(x[4], x[5]) | e4m3x2(x[6], x[7]) << 16);
+        dst[8 * i] = codes(x, s, inv, margin);
       }
       return;
     }

@@ -191,6 +191,28 @@ def test_graph_and_side_stream():
     check(d, q, before, True, True)
 
 
+# Generic scales, powers of two and sums of two (their quotients are ties often), ones whose
+# reciprocal leaves the fp32 range, infinite, negative.
+@pytest.mark.parametrize("scale", [0.0123, 1.0, 2.0 ** -7, 0.75, 1.0 / 448, 2.0 ** -101, 2.0 ** 101, 3e38,
+                                   1e-40, float("inf"), -0.3])
+def test_every_bf16_value_gets_the_code_of_its_fp32_quotient(scale):
+    """Bit for bit: all 65536 values as latents of 128 tokens, NaN and infinities among them."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    d = inputs(128, 1, 16, True, seed=3, layout="packed")
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(128, 512)
+    d["kc"].copy_(every)
+    d["scale"].fill_(scale)
+    q = torch.empty(128, 1, 576, dtype=torch.bfloat16, device="cuda")
+    mla.rope_epilogue(d["ql"], d["qp"], d["kc"], d["kp"], d["pos"], d["cs"], d["slots"], q, d["cache"], d["scale"])
+    got = d["cache"].view(-1, 576)[d["slots"]][:, :512].cpu().view(torch.uint8)
+    want = every.float() / torch.tensor(scale, dtype=torch.float32)
+    want = torch.where(want.isnan(), want, want.clamp(-448, 448)).to(torch.float8_e4m3fn).view(torch.uint8)
+    nan = want & 0x7F == 0x7F
+    assert torch.equal(got & 0x7F == 0x7F, nan)
+    assert torch.equal(got[~nan], want[~nan])
+
+
 @pytest.mark.parametrize("fp8", [False, True])
 def test_append_then_prefix_decode(fp8):
     """The two as a decode step uses them, captured: the new tokens of every sequence are rotated
