@@ -350,17 +350,20 @@ def rope_epilogue(ql_nope, q_pe, kv_c, k_pe, positions, cos_sin, slot_mapping, q
     their positions.  The four inputs may be strided views (last dimension contiguous)."""
     torch = _torch()
     bf, dev = torch.bfloat16, _device(ql_nope)
+    if ql_nope.dim() != 3:
+        raise MLADecodeError(ERR_INVALID_ARG, "mla_decode_rope_epilogue")
     T, H, _ = ql_nope.shape
+    ql_s, qp_s, kc_s, kp_s = ql_nope.stride(), q_pe.stride(), kv_c.stride(), k_pe.stride()
+    fp8 = kv_cache.dtype is not bf
     # What the C ABI reads, and nothing else: types, shapes, rows or all of a tensor contiguous,
     # the current device.
-    fp8 = kv_cache.dtype is not bf
     if not (ql_nope.dtype is q_pe.dtype is kv_c.dtype is k_pe.dtype is q_out.dtype is bf
             and positions.dtype is slot_mapping.dtype is torch.int64 and cos_sin.dtype is torch.float32
             and ql_nope.shape[2] == D_V and q_pe.shape == (T, H, 64) and kv_c.shape == (T, D_V)
             and k_pe.shape == (T, 64) and positions.shape == slot_mapping.shape == (T,)
             and cos_sin.dim() == 2 and cos_sin.shape[1] == 64 and q_out.shape == (T, H, D_QK)
             and kv_cache.dim() == 3 and kv_cache.shape[2] == D_QK
-            and ql_nope.stride(2) == q_pe.stride(2) == kv_c.stride(1) == k_pe.stride(1) == 1
+            and ql_s[2] == qp_s[2] == kc_s[1] == kp_s[1] == 1
             and positions.is_contiguous() and slot_mapping.is_contiguous()
             and cos_sin.is_contiguous() and q_out.is_contiguous() and kv_cache.is_contiguous()
             and 0 <= dev == q_pe.get_device() == kv_c.get_device()
@@ -373,8 +376,8 @@ def rope_epilogue(ql_nope, q_pe, kv_c, k_pe, positions, cos_sin, slot_mapping, q
                  and status.get_device() == dev)):
         raise MLADecodeError(ERR_INVALID_ARG, "mla_decode_rope_epilogue")
     st = lib().mla_decode_rope_epilogue(
-        ql_nope.data_ptr(), ql_nope.stride(0), ql_nope.stride(1), q_pe.data_ptr(), q_pe.stride(0),
-        q_pe.stride(1), kv_c.data_ptr(), kv_c.stride(0), k_pe.data_ptr(), k_pe.stride(0),
+        ql_nope.data_ptr(), ql_s[0], ql_s[1], q_pe.data_ptr(), qp_s[0], qp_s[1],
+        kv_c.data_ptr(), kc_s[0], k_pe.data_ptr(), kp_s[0],
         positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], 1 if interleaved else 0,
         slot_mapping.data_ptr(), T, H, q_out.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
         kv_cache.shape[1], KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None,
