@@ -117,7 +117,7 @@ struct PrefixShape {
 
 #ifdef __CUDACC__
   __device__ __forceinline__ int context(int b) const {
-    const int ctx = __ldg(seq_lens + b);
+    const int ctx = __ldcg(seq_lens + b);  // the staging may not read it from L1
     return ctx < 0 ? 0 : min(ctx, max_ctx);
   }
   __device__ __forceinline__ int own(int b) const { return max(0, context(b) - prefix_len); }

@@ -163,7 +163,8 @@ __device__ void partition(const StageParams& p) {
 // CTA 0: the partition.  Then one CTA per 32 rows: shared keys (with zeros up
 // to the tile's end), query rows, own keys (row block by row block, sequence
 // by sequence, then the zeros up to the last tile's end).  Bound by memory:
-// 1152 or 576 B in and 1152 B out a row, 9 loads in flight a thread.
+// 1152 or 576 B in and 1152 B out a row, 9 loads in flight a thread.  What it
+// reads before its dependency wait it reads from L2 (clear_kernel says why).
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   ptx::launch_dependents();
   const mla::PrefixShape& g = p.g;
@@ -238,10 +239,10 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   if (row < n_src && src != nullptr) {
     const uint4* at = reinterpret_cast<const uint4*>(src + row * MLA_D_QK) + sub;
 #pragma unroll
-    for (int i = 0; i < kStageIters; ++i) v[i] = at[8 * i];
+    for (int i = 0; i < kStageIters; ++i) v[i] = __ldcg(at + 8 * i);
   } else if (row < n_src) {
     const uint32_t key = (uint32_t)(key0 + row), page_i = key / (uint32_t)p.page_size;
-    int64_t page = __ldg(table + page_i);
+    int64_t page = __ldcg(table + page_i);
     bad_page = page < 0 || page >= p.num_pages;
     if (bad_page) page = 0;
     const int64_t at_row = page * p.page_size + (key - page_i * (uint32_t)p.page_size);
@@ -250,13 +251,13 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
       const uint2* at = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + at_row * MLA_D_QK) + sub;
 #pragma unroll
       for (int i = 0; i < kStageIters; ++i) {
-        const uint2 c = at[8 * i];
+        const uint2 c = __ldcg(at + 8 * i);
         v[i] = make_uint4(c.x, c.y, 0, 0);
       }
     } else {
       const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + at_row * MLA_D_QK) + sub;
 #pragma unroll
-      for (int i = 0; i < kStageIters; ++i) v[i] = at[8 * i];
+      for (int i = 0; i < kStageIters; ++i) v[i] = __ldcg(at + 8 * i);
     }
   } else {
 #pragma unroll
@@ -289,10 +290,14 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
 }
 
 // The status word and the bad keys' words.  A kernel, not a memset: the staging
-// is launched as its programmatic dependent and overlaps it (3 us a call).
-// It is itself launched plainly, so everything before this call is done when
-// it starts, and what follows may read the call's inputs at once.
+// is launched as its programmatic dependent and overlaps it (3 us a call), and
+// it as one of whatever precedes the call (another 2 us where calls are
+// launched one by one).  It lets the staging start once everything before the
+// call is done and visible in L2.  No launch boundary need have emptied the L1s
+// since, so the staging passes them by (0.6 us at 18 MB of keys; an acquire
+// fence in each of its CTAs: 1.3).
 __global__ void __launch_bounds__(256) clear_kernel(int32_t* words, int n) {
+  ptx::grid_dependency_wait();
   ptx::launch_dependents();
   for (int i = threadIdx.x; i < n; i += 256) words[i] = 0;
 }
@@ -656,13 +661,6 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   const bool fp8 = plan->kv_dtype == MLA_KV_FP8_E4M3;
   const uint64_t wait_ns =
       plan->wait_limit_us > 0 ? (uint64_t)plan->wait_limit_us * 1000ull : kDefaultWaitNs;
-  // Without shared keys the next launch is a decode kernel or the merge; the
-  // former flags contexts before its dependency wait, so nothing may overlap.
-  if (plan->prefix_tiles > 0)
-    clear_kernel<<<1, 256, 0, s>>>(g.status, 4 + plan->batch + 1);
-  else if (cudaMemsetAsync(g.status, 0, 16 + 4 * ((size_t)plan->batch + 1), s) != cudaSuccess)
-    return MLA_ERR_CUDA;
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   cudaLaunchAttribute attr[1];  // of the launches that overlap the one before them
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -670,6 +668,17 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
+
+  // Without shared keys the next launch is a decode kernel or the merge; the
+  // former flags contexts before its dependency wait, so nothing may overlap.
+  const int words = 4 + plan->batch + 1;
+  if (plan->prefix_tiles > 0) {
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    if (cudaLaunchKernelEx(&cfg, clear_kernel, g.status, words) != cudaSuccess) return MLA_ERR_CUDA;
+  } else if (cudaMemsetAsync(g.status, 0, 4 * (size_t)words, s) != cudaSuccess) {
+    return MLA_ERR_CUDA;
+  }
 
   if (plan->prefix_tiles > 0) {
     StageParams t;

@@ -258,3 +258,50 @@ def test_append_then_prefix_decode(fp8):
     got = q[..., 512:].double().cpu().numpy()
     assert np.all(np.abs(got - ref) <= step_half(np.abs(ref) + fp32, 7, -126) + fp32)
     assert_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), *p.reference(), "step")
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_steps_back_to_back_read_what_the_step_before_left(captured):
+    """Forty steps over the same buffers (rows inserted at the same slots, lengths and query rows
+    rewritten) with nothing between them, against the same steps one at a time: the same bits."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    B, H, P, ps, N = 40, 16, 1000, 16, 40
+    p = PrefixProblem(B, 1, H, [P + 20 + b for b in range(B)], P, ps, syn.KV_BF16, seed=23)
+    t, plan = p.to_device(), p.plan()
+    ws = mla.workspace_for(plan)
+    g = torch.Generator(device="cuda").manual_seed(24)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    ql, qp, kc, kp = rnd(N, B, H, 512), rnd(N, B, H, 64), rnd(N, B, 512), rnd(N, B, 64)
+    cs = torch.randn(5000, 64, generator=g, device="cuda")
+    slots = torch.tensor([p.slots[b, P + 3] for b in range(B)], dtype=torch.int64, device="cuda")
+    pos = torch.randint(0, 5000, (N, B), generator=g, device="cuda")
+    lens = torch.stack([t["lens"] - int(i) for i in torch.randint(0, 20, (N,))])  # at least P + 1
+    q = torch.empty(B, H, 576, dtype=torch.bfloat16, device="cuda")
+    keep = t["cache"].clone()
+
+    def steps(out, lse, wait):
+        t["cache"].copy_(keep)
+        for i in range(N):
+            torch.add(lens[i], 0, out=t["lens"])
+            mla.rope_epilogue(ql[i], qp[i], kc[i], kp[i], pos[i], cs, slots, q, t["cache"])
+            mla.prefix_fwd(plan, q.view(B, 1, H, 576), t["cache"], None, t["pt"], t["bt"], t["lens"],
+                           p.scale, out[i], lse[i], ws)
+            if wait:
+                torch.cuda.synchronize()
+
+    new = lambda *s, dt: torch.full((N, B, 1, H, *s), float("nan"), dtype=dt, device="cuda")  # noqa: E731
+    one, one_lse = new(512, dt=torch.bfloat16), new(dt=torch.float32)
+    steps(one, one_lse, True)
+    assert torch.isfinite(one_lse).all() and torch.isfinite(one).all()
+    run, run_lse = new(512, dt=torch.bfloat16), new(dt=torch.float32)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            steps(run, run_lse, False)
+        graph.replay()
+    else:
+        steps(run, run_lse, False)
+    torch.cuda.synchronize()
+    assert mla.prefix_check(plan, ws) == 0
+    assert torch.equal(run, one) and torch.equal(run_lse, one_lse)
