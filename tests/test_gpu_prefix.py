@@ -419,3 +419,59 @@ def test_refusals_of_the_binding():
     with pytest.raises(mla.MLADecodeError) as e:
         call(ws=ws[:1000])
     assert e.value.status == mla.ERR_WORKSPACE
+
+
+@pytest.mark.parametrize("before", ["nothing", "copy", "kernel", "fill", "join of two kernels",
+                                    "join of a kernel and a copy", "event of a kernel"])
+def test_captured_behind(before):
+    """The call as the first work after other nodes of a graph, which write its inputs."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = PrefixProblem(5, 1, 16, [1024 + 3 * b for b in range(5)], 1024, 16, seed=29)
+    t, plan = p.to_device(), p.plan()
+    ws = mla.workspace_for(plan)
+    out = torch.full((5, 1, 16, 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    lse = torch.full((5, 1, 16), float("nan"), device="cuda")
+    q, lens = t["q"].clone(), t["lens"].clone()
+    main, side = torch.cuda.Stream(), torch.cuda.Stream()
+
+    def work():
+        if before.startswith("join"):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                t["lens"].copy_(lens) if before.endswith("copy") else torch.add(lens, 0, out=t["lens"])
+            torch.mul(q, 1.0, out=t["q"])
+            main.wait_stream(side)
+        elif before == "event of a kernel":
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                torch.mul(q, 1.0, out=t["q"])
+                torch.add(lens, 0, out=t["lens"])
+            main.wait_stream(side)
+        else:
+            if before in ("kernel", "fill"):
+                torch.mul(q, 1.0, out=t["q"])
+            if before == "fill":
+                out.zero_()
+            if before == "copy":
+                t["q"].copy_(q)
+                t["lens"].copy_(lens)
+        mla.prefix_fwd(plan, t["q"], t["cache"], None, t["pt"], t["bt"], t["lens"], p.scale, out, lse, ws)
+
+    main.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(main):
+        work()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        work()
+    if before not in ("nothing", "kernel", "fill"):
+        t["lens"].fill_(7)
+    if before != "nothing":
+        t["q"].zero_()
+    out.fill_(float("nan"))
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    assert mla.prefix_check(plan, ws) == 0
+    assert_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), *p.reference(), before)
