@@ -521,7 +521,7 @@ typedef struct mla_decode_prefix_plan_t {
   int32_t own_splits;    /* splits of the longest sequence's own keys (0: folded, or none) */
   int32_t wait_limit_us; /* as mla_decode_plan_t: 0 = 2 s; the one field a caller may set */
   int32_t reserved0;
-  int64_t ws_status_offset;     /* int32 status word [4], int32 [B + 1] */
+  int64_t ws_status_offset;     /* int32 status word [4], a byte per staged row */
   int64_t ws_partition_offset;  /* the device's partition of the tiles */
   int64_t ws_keys_offset;       /* f16 [256 prefix_tiles + row_blocks * block_keys, 576] */
   int64_t ws_q_offset;          /* f16 [total_rows, 576] */

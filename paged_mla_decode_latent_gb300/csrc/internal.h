@@ -103,10 +103,10 @@ struct PrefixShape {
   int32_t* block_tiles;     // [row blocks]
   int2* parts;              // [row blocks]: the first pair that holds a part of one, and their number
   int32_t* own_off;         // [row blocks, block_seqs]: a sequence's first own key in its block's
-  // [B + 1]: 2^31 - 1 - (first key of the sequence's own, and of the shared
-  // ones, that f16 cannot hold); 0: none
-  int32_t* bad;
   int32_t* status;
+  // Status bits of each staged key and query row (a bad page, values that f16
+  // cannot hold), for the attention to act on and to report.
+  uint8_t *key_flags, *row_flags;
   int rows, rows_per_seq, heads, sq, causal, batch;
   int prefix_len, max_ctx;
   int tiles;       // of the shared keys
@@ -117,7 +117,7 @@ struct PrefixShape {
 
 #ifdef __CUDACC__
   __device__ __forceinline__ int context(int b) const {
-    const int ctx = __ldcg(seq_lens + b);  // the staging may not read it from L1
+    const int ctx = seq_lens[b];
     return ctx < 0 ? 0 : min(ctx, max_ctx);
   }
   __device__ __forceinline__ int own(int b) const { return max(0, context(b) - prefix_len); }
@@ -126,10 +126,6 @@ struct PrefixShape {
     const int ctx = context(b);
     const int tok = (r - b * rows_per_seq) / heads;
     return causal ? max(0, min(ctx, ctx - sq + tok + 1)) : ctx;
-  }
-  // Whether one of them is a key that f16 cannot hold.
-  __device__ __forceinline__ bool sees_bad(int b, int n) const {
-    return n > 0x7FFFFFFF - max(bad[b], bad[batch]);
   }
   __device__ __forceinline__ int first_seq(int block) const {
     return (int)((uint32_t)(block * kRowTile) / (uint32_t)rows_per_seq);

@@ -92,7 +92,10 @@ __device__ void partition(const StageParams& p) {
   __shared__ int64_t carry_s;
   const mla::PrefixShape& g = p.g;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) carry_s = 0;
+  if (threadIdx.x == 0) {
+    carry_s = 0;
+    *g.status = 0;  // the only bits that the staging sets itself are below
+  }
   __syncthreads();
   int64_t mine = 0;
   int mine_n = 0;
@@ -154,7 +157,6 @@ __device__ void partition(const StageParams& p) {
     }
   }
   if (threadIdx.x == 0) g.pair_start[g.pairs] = make_int4(g.row_blocks, 0, 0, 0);
-  ptx::grid_dependency_wait();  // the status word is cleared
   // Contexts out of range, once per sequence.
   for (int b = threadIdx.x; b < g.batch; b += kStageThreads)
     if (g.seq_lens[b] < 0 || g.seq_lens[b] > g.max_ctx) atomicOr(g.status, MLA_DEVFLAG_CTX_RANGE);
@@ -163,10 +165,12 @@ __device__ void partition(const StageParams& p) {
 // CTA 0: the partition.  Then one CTA per 32 rows: shared keys (with zeros up
 // to the tile's end), query rows, own keys (row block by row block, sequence
 // by sequence, then the zeros up to the last tile's end).  Bound by memory:
-// 1152 or 576 B in and 1152 B out a row, 9 loads in flight a thread.  What it
-// reads before its dependency wait it reads from L2 (clear_kernel says why).
+// 1152 or 576 B in and 1152 B out a row, 9 loads in flight a thread.  Flags go
+// out as a byte for every row, not into words that something would have to
+// clear first: a clearing kernel before this one cost 1 us, and 2 of host time.
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   ptx::launch_dependents();
+  ptx::grid_dependency_wait();
   const mla::PrefixShape& g = p.g;
   if (blockIdx.x == 0) {
     partition(p);
@@ -175,7 +179,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   int u = blockIdx.x - 1;
   // Rows [0, n) of this CTA go to `dst`; the first n_src of them come from
   // `src` or through a page table (from key `key0` of it), the rest are zero.
-  int n = kChunk, n_src = 0, key0 = 0, who = -1;
+  int n = kChunk, n_src = 0, key0 = 0;
   const uint16_t* src = nullptr;
   const int32_t* table = nullptr;
   int64_t dst_row = 0;
@@ -185,7 +189,6 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
     dst_row = key0;
     n_src = min(kChunk, max(0, g.prefix_len - key0));
     table = p.prefix_table;
-    who = g.batch;
   } else if ((u -= p.prefix_chunks) < p.q_chunks) {
     const int r0 = u * kChunk;
     n = n_src = min(kChunk, g.rows - r0);
@@ -227,7 +230,6 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
       table = p.block_table + (int64_t)b * p.bt_stride;
       key0 = g.prefix_len + first_key;
       dst_row = region + sum_s + first_key;
-      who = b;
     }
   }
   // Eight threads a row, nine pieces each: one page id and one division a row,
@@ -239,10 +241,10 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   if (row < n_src && src != nullptr) {
     const uint4* at = reinterpret_cast<const uint4*>(src + row * MLA_D_QK) + sub;
 #pragma unroll
-    for (int i = 0; i < kStageIters; ++i) v[i] = __ldcg(at + 8 * i);
+    for (int i = 0; i < kStageIters; ++i) v[i] = at[8 * i];
   } else if (row < n_src) {
     const uint32_t key = (uint32_t)(key0 + row), page_i = key / (uint32_t)p.page_size;
-    int64_t page = __ldcg(table + page_i);
+    int64_t page = table[page_i];
     bad_page = page < 0 || page >= p.num_pages;
     if (bad_page) page = 0;
     const int64_t at_row = page * p.page_size + (key - page_i * (uint32_t)p.page_size);
@@ -251,20 +253,18 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
       const uint2* at = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + at_row * MLA_D_QK) + sub;
 #pragma unroll
       for (int i = 0; i < kStageIters; ++i) {
-        const uint2 c = __ldcg(at + 8 * i);
+        const uint2 c = at[8 * i];
         v[i] = make_uint4(c.x, c.y, 0, 0);
       }
     } else {
       const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + at_row * MLA_D_QK) + sub;
 #pragma unroll
-      for (int i = 0; i < kStageIters; ++i) v[i] = __ldcg(at + 8 * i);
+      for (int i = 0; i < kStageIters; ++i) v[i] = at[8 * i];
     }
   } else {
 #pragma unroll
     for (int i = 0; i < kStageIters; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
-  ptx::grid_dependency_wait();  // the words that flags go to are cleared
-  if (bad_page) atomicOr(g.status, MLA_DEVFLAG_BAD_PAGE);
   uint4* out = reinterpret_cast<uint4*>(dst + (dst_row + row) * MLA_D_QK) + sub;
   __half2 top = __floats2half2_rn(0.f, 0.f);  // largest magnitude; NaN if there is one
 #pragma unroll
@@ -273,33 +273,20 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
     out[8 * i] = w;
     top = __hmax2_nan(top, __hmax2_nan(__hmax2_nan(abs2(w.x), abs2(w.y)), __hmax2_nan(abs2(w.z), abs2(w.w))));
   }
-  if (!not_finite(*reinterpret_cast<const uint32_t*>(&top))) return;
+  const bool over = not_finite(*reinterpret_cast<const uint32_t*>(&top));
+  const bool any = __any_sync(0xFFu << (threadIdx.x & 24), over);  // in the row
+  if (sub == 0)
+    (src != nullptr ? g.row_flags : g.key_flags)[dst_row + row] =
+        (uint8_t)((bad_page ? MLA_DEVFLAG_BAD_PAGE : 0) |
+                  (any ? src != nullptr ? MLA_DEVFLAG_Q_RANGE : MLA_DEVFLAG_KV_RANGE : 0));
   // Rare: a query value spoils its own row only; a key is staged anew without
-  // what f16 cannot hold.
-  if (src != nullptr) {
-    atomicOr(g.status, MLA_DEVFLAG_Q_RANGE);
-    return;
-  }
-  atomicOr(g.status, MLA_DEVFLAG_KV_RANGE);
-  atomicMax(g.bad + who, 0x7FFFFFFF - (key0 + row));
+  // what f16 cannot hold (0 x NaN would spoil rows that do not see it).
+  if (!over || src != nullptr) return;
 #pragma unroll 1
   for (int i = 0; i < kStageIters; ++i) {
     const uint4 w = out[8 * i];
     out[8 * i] = make_uint4(finite_or_zero(w.x), finite_or_zero(w.y), finite_or_zero(w.z), finite_or_zero(w.w));
   }
-}
-
-// The status word and the bad keys' words.  A kernel, not a memset: the staging
-// is launched as its programmatic dependent and overlaps it (3 us a call), and
-// it as one of whatever precedes the call (another 2 us where calls are
-// launched one by one).  It lets the staging start once everything before the
-// call is done and visible in L2.  No launch boundary need have emptied the L1s
-// since, so the staging passes them by (0.6 us at 18 MB of keys; an acquire
-// fence in each of its CTAs: 1.3).
-__global__ void __launch_bounds__(256) clear_kernel(int32_t* words, int n) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
-  for (int i = threadIdx.x; i < n; i += 256) words[i] = 0;
 }
 
 struct MergeParams {
@@ -394,7 +381,7 @@ __global__ void __launch_bounds__(256) merge_kernel(MergeParams p) {
     }
   }
   float L = sum > 0.f ? m + logf(sum) : -INFINITY, inv = sum > 0.f ? 1.f / sum : 0.f;
-  if (sum != sum || g.sees_bad(b, g.visible(r, b))) L = inv = NAN;  // a NaN partial, a bad key
+  if (sum != sum) L = inv = NAN;  // a NaN partial
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const __nv_bfloat162 lo = __floats2bfloat162_rn(acc[i].x * inv, acc[i].y * inv);
@@ -425,12 +412,18 @@ bool room_to_fold(int64_t batch, int rows, int64_t own) {
          blocks * ceil_div(keys, mla::kPrefixTile) * mla::kPrefixTile <= kMaxRegionRows;
 }
 
+// Staged rows of keys: the shared ones and each row block's own, in whole tiles.
+int64_t staged_keys(const mla_decode_prefix_plan_t& p) {
+  return (int64_t)p.prefix_tiles * mla::kPrefixTile + (int64_t)p.row_blocks * p.block_keys;
+}
+
 mla::PrefixShape shape_of(const mla_decode_prefix_plan_t& p, const int32_t* seq_lens, char* ws) {
   mla::PrefixShape g;
   std::memset(&g, 0, sizeof g);
   g.seq_lens = seq_lens;
   g.status = reinterpret_cast<int32_t*>(ws + p.ws_status_offset);
-  g.bad = g.status + 4;
+  g.key_flags = reinterpret_cast<uint8_t*>(g.status + 4);
+  g.row_flags = g.key_flags + staged_keys(p);
   g.pair_start = reinterpret_cast<int4*>(ws + p.ws_partition_offset);
   g.first_unit = reinterpret_cast<int64_t*>(g.pair_start + p.pairs + 1);
   g.parts = reinterpret_cast<int2*>(g.first_unit + p.row_blocks);
@@ -471,8 +464,8 @@ void lay_out(mla_decode_prefix_plan_t* p) {
     return at;
   };
   const int64_t segments = p->prefix_tiles > 0 ? (int64_t)p->row_blocks + p->pairs : 0;
-  const int64_t keys = (int64_t)p->prefix_tiles * mla::kPrefixTile + (int64_t)p->row_blocks * p->block_keys;
-  p->ws_status_offset = take(16 + 4 * ((int64_t)p->batch + 1));
+  const int64_t keys = staged_keys(*p);
+  p->ws_status_offset = take(16 + (p->prefix_tiles > 0 ? keys + p->total_rows : 0));
   p->ws_partition_offset = take(20 * (int64_t)p->row_blocks + 16 * ((int64_t)p->pairs + 1) +
                                 (p->own_folded ? 4ll * p->row_blocks * seqs : 0));
   p->ws_keys_offset = take(p->prefix_tiles > 0 ? keys * MLA_D_QK * 2 : 0);
@@ -669,17 +662,9 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
   cfg.attrs = attr;
   cfg.numAttrs = 1;
 
-  // Without shared keys the next launch is a decode kernel or the merge; the
-  // former flags contexts before its dependency wait, so nothing may overlap.
-  const int words = 4 + plan->batch + 1;
-  if (plan->prefix_tiles > 0) {
-    cfg.gridDim = dim3(1, 1, 1);
-    cfg.blockDim = dim3(256, 1, 1);
-    if (cudaLaunchKernelEx(&cfg, clear_kernel, g.status, words) != cudaSuccess) return MLA_ERR_CUDA;
-  } else if (cudaMemsetAsync(g.status, 0, 4 * (size_t)words, s) != cudaSuccess) {
-    return MLA_ERR_CUDA;
-  }
-
+  // The staging clears the status word.  Without shared keys the first launch is
+  // a decode kernel, which flags contexts before its dependency wait, or the merge.
+  if (plan->prefix_tiles == 0 && cudaMemsetAsync(g.status, 0, 16, s) != cudaSuccess) return MLA_ERR_CUDA;
   if (plan->prefix_tiles > 0) {
     StageParams t;
     t.g = g;
@@ -714,9 +699,7 @@ extern "C" int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const
     p.wait_ns = wait_ns;
     p.softmax_scale = softmax_scale;
     p.partials = plan->own_splits > 0;
-    const int64_t key_rows =
-        (int64_t)plan->prefix_tiles * mla::kPrefixTile + (int64_t)plan->row_blocks * plan->block_keys;
-    if (mla_launch_prefix_sm103(p, t.k_out, key_rows, t.q_out, stream) != 0) return MLA_ERR_CUDA;
+    if (mla_launch_prefix_sm103(p, t.k_out, staged_keys(*plan), t.q_out, stream) != 0) return MLA_ERR_CUDA;
   }
 
   if (plan->own_splits > 0) {

@@ -217,6 +217,20 @@ struct Walk {
   }
 };
 
+// Reports the flags of a warp's 64 keys (four in each of 16 lanes, twice);
+// returns the row's sum of weights, NaN if it sees a key that f16 cannot hold,
+// [from, lim) being those that it sees.  Rare, so out of line.
+__device__ __noinline__ float flagged_keys(const mla::PrefixShape& g, uint32_t flags, int from, int lim, float l) {
+  uint32_t all = 0;
+  for (int i = 0; i < 64; ++i) {
+    const uint32_t f = __shfl_sync(0xffffffffu, flags, i / 4) >> (8 * (i % 4)) & 0xFFu;
+    all |= f;
+    if ((f & MLA_DEVFLAG_KV_RANGE) && i >= from && i < lim) l = NAN;
+  }
+  if ((threadIdx.x & 31) == 0) atomicOr(g.status, (int)all);
+  return l;
+}
+
 template <bool kPoll>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     prefix_kernel(mla::PrefixParams p, const __grid_constant__ CUtensorMap kmap,
@@ -425,23 +439,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t o_free = ptx::mapa(ptx::smem_u32(&bars.o_free), 0);
     volatile float* xch = reinterpret_cast<volatile float*>(smem + OFF_X);
     const uint32_t p_row = sbase + OFF_P + kg * PSLAB + r * 128;
+    const uint32_t* key_flags = reinterpret_cast<const uint32_t*>(p.g.key_flags + 64 * kg) + (lane & 15);
     uint32_t it = 0;
     while (w.next()) {
       const int row = w.rb * mla::kRowTile + 64 * (int)rank + r;
       // The row sees the first `shared` keys of the prefix and, of its row
       // block's own keys, [own0, own1).
-      int shared = 0, own0 = 0, own1 = 0, n_vis = 0, b = 0;
+      int shared = 0, own0 = 0, own1 = 0;
       if (row < p.g.rows) {
-        b = row / p.g.rows_per_seq;
-        n_vis = p.g.visible(row, b);
+        const int b = row / p.g.rows_per_seq, n_vis = p.g.visible(row, b);
         shared = min(n_vis, p.g.prefix_len);
         if (p.g.fold) {
           own0 = p.g.own_off[w.rb * p.g.block_seqs + b - p.g.first_seq(w.rb)];
           own1 = own0 + max(0, n_vis - p.g.prefix_len);
         }
       }
+      if (kg == 0 && row < p.g.rows && p.g.row_flags[row] != 0) atomicOr(p.g.status, p.g.row_flags[row]);
       float m = kMaxSentinel, l = 0.f;
       for (int t = w.t0; t < w.t1; ++t, ++it) {
+        const uint32_t flags = key_flags[w.key_row(t) / 4];  // of four of this warp's 64 keys
         wait(c, ptx::smem_u32(&bars.s_full[it & 1]), (it >> 1) & 1);
         __syncwarp();
         ptx::tc_fence_after();
@@ -491,6 +507,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             pk[16 * h + i / 2] = pack_f16(a, b2);
           }
         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (__any_sync(0xffffffffu, flags != 0)) l = flagged_keys(p.g, flags, from, lim, l);
         // The weights' buffer and O are free once the values of the tile
         // before are accumulated (a segment's first tile waited for that at
         // the end of the segment before).
@@ -538,7 +555,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (l == 0.f && (key0 < min(shared, key1) || max(own + own0, key0) < min(own + own1, key1))) l = NAN;
       float inv = l == 0.f ? 0.f : s_kv / l;
       float lse = l == 0.f ? -INFINITY : (m - kHead + log2f(l)) * 0.6931471805599453f;
-      if (final && row < p.g.rows && p.g.sees_bad(b, n_vis)) inv = lse = NAN;
       const size_t seg = (size_t)(pair + w.rb) * mla::kRowTile;
       const int local0 = 64 * (int)rank + 32 * (q4 & 1);  // the warp's first row of the block
       const int rows_left = good ? p.g.rows - w.rb * mla::kRowTile - local0 : 0;
