@@ -98,7 +98,6 @@ constexpr uint32_t kSleepNs = 20000;
 struct Bars {
   uint64_t full[kSlots];   // slab landed in both CTAs (even CTA)
   uint64_t empty[kSlots];  // slab read by the MMAs (both)
-  uint64_t q_full;         // a segment's query rows landed in both CTAs (even CTA)
   uint64_t q_empty;        // the segment's last score MMA is done (both)
   uint64_t s_full[2];      // scores written (both)
   uint64_t p_full;         // weights written by the 16 softmax warps of the pair (even CTA)
@@ -255,7 +254,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::mbar_init(ptx::smem_u32(&bars.full[i]), 1);
       ptx::mbar_init(ptx::smem_u32(&bars.empty[i]), 1);
     }
-    ptx::mbar_init(ptx::smem_u32(&bars.q_full), 1);
     ptx::mbar_init(ptx::smem_u32(&bars.q_empty), 1);
     for (int i = 0; i < 2; ++i) ptx::mbar_init(ptx::smem_u32(&bars.s_full[i]), 1);
     ptx::mbar_init(ptx::smem_u32(&bars.p_full), 2 * kSoftmaxWarps);
@@ -287,9 +285,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int slot = 0, issued = 0;
     uint32_t ph = 1;  // a fresh barrier passes the wait for the phase before its first
     bool ok = true;
-    auto reserve = [&] {
+    auto reserve = [&](int bytes) {
       ok = ok && wait(c, empty_own + 8 * slot, ph);
-      if (ok && leader && rank == 0) ptx::mbar_arrive_expect_tx(full_own + 8 * slot, 2 * SLAB);
+      if (ok && leader && rank == 0) ptx::mbar_arrive_expect_tx(full_own + 8 * slot, 2 * bytes);
     };
     auto advance = [&] {
       issued += ok;
@@ -298,32 +296,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ph ^= 1u;
       }
     };
-    auto scores = [&](int t) {
-      const int y = w.key_row(t) + 128 * (int)rank;
+    // A segment's first score slabs bring the same dims of its query rows along.
+    auto scores = [&](int t, bool head) {
+      const int y = w.key_row(t) + 128 * (int)rank, rows = w.rb * mla::kRowTile + 64 * (int)rank;
 #pragma unroll 3
       for (int d = 0; d < 9; ++d) {
-        reserve();
-        if (ok && leader)
+        reserve(head ? SLAB + QSLAB : SLAB);
+        if (ok && leader) {
+          if (head) ptx::tma_load_3d_pair(sbase + OFF_Q + d * QSLAB, &qmap, 0, rows, d, full0 + 8 * slot);
           ptx::tma_load_2d_pair(sbase + OFF_RING + slot * SLAB, &kmap, 64 * d, y, full0 + 8 * slot);
+        }
         advance();
       }
     };
     for (int seg = 0; w.next(); ++seg) {
       if (seg > 0) ok = ok && wait(c, ptx::smem_u32(&bars.q_empty), (seg - 1) & 1);
-      if (ok && leader) {
-        if (rank == 0) ptx::mbar_arrive_expect_tx(ptx::smem_u32(&bars.q_full), 2 * 9 * QSLAB);
-        const uint32_t bar = ptx::mapa(ptx::smem_u32(&bars.q_full), 0);
-        for (int d = 0; d < 9; d += 3)
-          ptx::tma_load_3d_pair(sbase + OFF_Q + d * QSLAB, &qmap, 0,
-                                w.rb * mla::kRowTile + 64 * (int)rank, d, bar);
-      }
-      scores(w.t0);
+      scores(w.t0, true);
       for (int t = w.t0; t < w.t1; ++t) {
-        if (t + 1 < w.t1) scores(t + 1);
+        if (t + 1 < w.t1) scores(t + 1, false);
         const int y = w.key_row(t);
 #pragma unroll 4
         for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, dims 128 (v % 2) of the CTA's half
-          reserve();
+          reserve(SLAB);
           if (ok && leader)
             ptx::tma_load_3d_pair(sbase + OFF_RING + slot * SLAB, &vmap, 0, y + 64 * (v >> 1),
                                   4 * (int)rank + 2 * (v & 1), full0 + 8 * slot);
@@ -379,7 +373,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         ready = next;
       };
       for (int seg = 0; w.next(); ++seg) {
-        if (!pass(ptx::smem_u32(&bars.q_full), seg & 1)) goto mma_end;
         const int n = w.t1 - w.t0;
         for (int t = 0; t <= n; ++t) {
           if (t < n) {
@@ -633,12 +626,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 int mla_launch_prefix_sm103(const mla::PrefixParams& p, const void* keys, int64_t key_rows,
                             const void* rows, void* stream) {
   // Score slabs: 128 keys x 64 dims.  Value slabs: 64 keys x 2 x 64 dims and
-  // query slabs: 64 rows x 3 x 64 dims, the 64-dim groups of a row as a third
+  // query slabs: 64 rows x 64 dims, the 64-dim groups of a row as a third
   // dimension, so that one copy fills a slab group by group.
   CUtensorMap kmap, vmap, qmap;
   if (!mla::tensor_map_rows(&kmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, keys, key_rows, mla::kDQK, 128) ||
       !mla::tensor_map_groups(&vmap, keys, key_rows, 2) ||
-      !mla::tensor_map_groups(&qmap, rows, p.g.rows, 3))
+      !mla::tensor_map_groups(&qmap, rows, p.g.rows, 1))
     return (int)cudaErrorUnknown;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
