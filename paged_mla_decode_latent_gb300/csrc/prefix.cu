@@ -156,7 +156,9 @@ __device__ void partition(const StageParams& p) {
       g.pair_start[i] = make_int4(j, (int)max((int64_t)0, s - a - mla::kSegmentTiles), tiles, 0);
     }
   }
-  if (threadIdx.x == 0) g.pair_start[g.pairs] = make_int4(g.row_blocks, 0, 0, 0);
+  // The end, and pairs past the last unit (own keys that the plan counted on).
+  for (int i = (int)min((int64_t)g.pairs, carry_s) + threadIdx.x; i <= g.pairs; i += kStageThreads)
+    g.pair_start[i] = make_int4(g.row_blocks, 0, 0, 0);
   // Contexts out of range, once per sequence.
   for (int b = threadIdx.x; b < g.batch; b += kStageThreads)
     if (g.seq_lens[b] < 0 || g.seq_lens[b] > g.max_ctx) atomicOr(g.status, MLA_DEVFLAG_CTX_RANGE);
@@ -501,10 +503,7 @@ int check_plan(const mla_decode_prefix_plan_t* p) {
   mla_decode_prefix_plan_t want = *p;
   lay_out(&want);
   if (std::memcmp(&want, p, sizeof want) != 0) return MLA_ERR_INVALID_ARG;
-  if (p->prefix_tiles > 0
-          ? p->pairs < 1 || p->pairs > kMaxPairs || p->pairs > (int64_t)p->row_blocks * p->prefix_tiles
-          : p->pairs != 0)
-    return MLA_ERR_INVALID_ARG;
+  if (p->prefix_tiles > 0 ? p->pairs < 1 || p->pairs > kMaxPairs : p->pairs != 0) return MLA_ERR_INVALID_ARG;
   if (p->own_chunk % p->key_tile != 0) return MLA_ERR_INVALID_ARG;
   return MLA_OK;
 }
@@ -583,7 +582,7 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
       else for (int j = 0; j <= p.row_blocks; ++j) first[j] = (int64_t)j * p.prefix_tiles;
       // Pairs that share the tiles: the count with the smallest longest pair,
       // merge included.  With many row blocks all pairs are busy anyway.
-      const int most = (int)std::min<int64_t>(pairs, (int64_t)p.row_blocks * p.prefix_tiles);
+      const int most = (int)std::min<int64_t>(pairs, first[p.row_blocks]);
       const int64_t total = first[p.row_blocks] + (int64_t)p.row_blocks * mla::kSegmentTiles;
       double best = 1e300;
       for (int n = p.row_blocks > 1024 ? most : 1; n <= most; ++n) {

@@ -475,3 +475,27 @@ def test_captured_behind(before):
     torch.cuda.synchronize()
     assert mla.prefix_check(plan, ws) == 0
     assert_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), *p.reference(), before)
+
+
+@pytest.mark.parametrize("heads,planned", [(16, [3000]), (16, [900, 40, 2000, 700, 10, 0, 1500, 300, 299]), (128, [2500, 1])])
+def test_contexts_shorter_than_the_plan_leave_pairs_without_work(heads, planned):
+    """Planned with long own keys and hardly any shared ones, called with short contexts, down to empty."""
+    import paged_mla_decode_latent_gb300 as mla
+    batch = len(planned)
+    plan = mla.prefix_plan([1 + n for n in planned], 1, heads, 1, 16, BF16, False, 0)
+    assert plan.own_folded and plan.pairs > plan.row_blocks * 3  # the units of the shared keys alone
+    width = -(-(1 + max(planned)) // 16)
+    for lens in ([1] * batch, [0] * batch, [1 + b % 2 for b in range(batch)], [1 + min(n, 40) for n in planned],
+                 [1 + n for n in planned]):
+        p = PrefixProblem(batch, 1, heads, lens, 1, 16, seed=31)
+        t = p.to_device()
+        if t["bt"].shape[1] < width:  # entries past a sequence's last page are not read
+            t["bt"] = torch_pad(t["bt"], width)
+        out, lse, _, status = p.run(t=t, plan=plan)
+        assert status == 0
+        assert_close(out, lse, *p.reference(), f"{lens}")
+
+
+def torch_pad(bt, width):
+    import torch
+    return torch.nn.functional.pad(bt, (0, width - bt.shape[1]), value=-1).contiguous()

@@ -38,7 +38,10 @@ def test_plan(batch, heads, sq, prefix, own, sms):
         assert p.block_keys == 0 and p.own_splits * p.own_chunk >= most
         assert p.own_chunk % p.key_tile == 0 and (p.own_splits == 0) == (most == 0)
     if prefix:
-        assert 1 <= p.pairs <= min(max(1, sms // 2), p.row_blocks * p.prefix_tiles)
+        own_keys = [sum(lens[b] - prefix for b in range(128 * j // rows, min(batch - 1, (128 * j + 127) // rows) + 1))
+                    for j in range(p.row_blocks)]
+        tiles = p.row_blocks * p.prefix_tiles + p.own_folded * sum(-(-k // 256) for k in own_keys)
+        assert 1 <= p.pairs <= min(max(1, sms // 2), tiles)
     else:
         assert p.pairs == 0 and not p.own_folded
     segments = p.row_blocks + p.pairs if prefix else 0
@@ -46,13 +49,19 @@ def test_plan(batch, heads, sq, prefix, own, sms):
     offs = [p.ws_status_offset, p.ws_partition_offset, p.ws_keys_offset, p.ws_q_offset,
             p.ws_prefix_o_offset, p.ws_prefix_lse_offset, p.ws_own_o_offset, p.ws_own_lse_offset,
             p.workspace_bytes]
-    sizes = [16 + 4 * (batch + 1),
+    sizes = [16 + (keys + p.total_rows if prefix else 0),
              20 * p.row_blocks + 16 * (p.pairs + 1) + (4 * p.row_blocks * seqs if p.own_folded else 0),
              keys * 1152 if prefix else 0, p.total_rows * 1152 if prefix else 0,
              segments * 128 * 2048, segments * 128 * 4,
              p.own_splits * p.total_rows * 2048, p.own_splits * p.total_rows * 4]
     for a, b, n in zip(offs, offs[1:], sizes):
         assert a % 256 == 0 and b - a >= n
+
+
+def test_own_tiles_have_pairs_too():
+    """Two shared tiles and seven of own keys: more than the two pairs that the shared ones could use."""
+    p = mla.prefix_plan([512 + 200] * 8, 512, 16, 1, 16, 0, False, 152)
+    assert p.own_folded and p.prefix_tiles == 2 and p.pairs > 4
 
 
 def test_own_keys_fold_in_or_not():
