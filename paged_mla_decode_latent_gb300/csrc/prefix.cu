@@ -555,27 +555,35 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
     constexpr double kTile = 2.4, kSegment = 4.7, kMergeFixed = 1.5, kMergeRow = 4096.0 / 4.0e6;
     const int pairs = std::min(std::max(1, d.num_sms / 2), kMaxPairs);
     std::vector<int64_t> first(p.row_blocks + 1, 0);  // tiles before each row block, own folded in
+    double staged = 0.0;                              // own keys of all row blocks
     for (int j = 0; j < p.row_blocks; ++j) {
       const int b0 = (int)((int64_t)j * mla::kRowTile / p.rows);
       const int b1 = (int)((std::min<int64_t>((int64_t)(j + 1) * mla::kRowTile, total_rows) - 1) / p.rows);
       int64_t keys = 0;
       for (int b = b0; b <= b1; ++b) keys += own[b];
+      staged += (double)keys;
       first[j + 1] = first[j] + p.prefix_tiles + ceil_div(keys, mla::kPrefixTile);
     }
     if (p.prefix_tiles > 0) {
       // Own keys as further tiles, unless they need too much room or cost more
-      // than a launch of the decode kernels of their own (about 10 us and 2.2
-      // us a key tile for each unit, all pairs at work; batch 64 x 128 heads
-      // with up to 512 own keys: 24 us against 3).
+      // than a launch of the decode kernels of their own: 10 us and 2.2 or 2.9
+      // a key tile (of 64 or 128 keys) for each unit, all pairs at work, against
+      // the tiles and the staging of what the cache is read for once.  Whole
+      // calls, folded against apart (us, 1024 shared keys, bf16): 128 x 16 heads
+      // with 250 own keys 33 / 43, 500: 53 / 54, 1000: 91 / 78, 2000: 163 / 114;
+      // 128 x 128 heads, 1000: 117 / 124, 2000: 193 / 169; 32 x 16 heads, 2000:
+      // 49 / 59.
+      const double key_tile_us = p.key_tile == mla::kKeyTile ? 2.2 : 2.9;
+      const double stage_key_us = kv_dtype == MLA_KV_BF16 ? 0.45e-3 : 0.36e-3;
       double separate = 0.0, longest = 0.0;
       for (int b = 0; b < batch; ++b) {
-        const double unit = 10.0 + 2.2 * (double)ceil_div(own[b], p.key_tile);
+        const double unit = 10.0 + key_tile_us * (double)ceil_div(own[b], p.key_tile);
         separate += unit * d.row_blocks;
         longest = std::max(longest, unit);
       }
       separate = std::max(longest, separate / pairs) + kMergeFixed;
       const double folded =
-          kTile * (double)(first[p.row_blocks] - (int64_t)p.row_blocks * p.prefix_tiles) / pairs;
+          kTile * (double)(first[p.row_blocks] - (int64_t)p.row_blocks * p.prefix_tiles) / pairs + stage_key_us * staged;
       p.own_folded = max_ctx > prefix_len && folded <= separate &&
                      room_to_fold(batch, p.rows, max_ctx - prefix_len);
       if (p.own_folded) p.own_splits = 0;
