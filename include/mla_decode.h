@@ -484,7 +484,8 @@ int mla_decode_fwd_noalloc(const mla_decode_plan_t* plan, const void* q, const v
  * batch are one product, so each shared row is read once for 128 query rows
  * instead of once per sequence; every sequence's own keys follow, and the two
  * parts are merged into one softmax.  The result is that of mla_decode_fwd +
- * mla_decode_combine on the same arguments: for sequence b, token i, head h
+ * mla_decode_combine on the same arguments, up to rounding and to what is said
+ * below of values that f16 does not hold: for sequence b, token i, head h
  *
  *   n   = causal ? ctx_b - Sq + i + 1 : ctx_b        (clamped to [0, ctx_b])
  *   key j < prefix_len is row prefix_table[j / page_size][j % page_size],
@@ -497,11 +498,15 @@ int mla_decode_fwd_noalloc(const mla_decode_plan_t* plan, const void* q, const v
  * sequence's own copy of the page, of which only the slots from prefix_len %
  * page_size on are read.
  *
- * Keys and query rows are staged in f16 (exact for bf16 and e4m3 values of
- * magnitude 2^-14 to 65504, to 2^-25 below that).  A larger or non-finite key
- * sets MLA_DEVFLAG_KV_RANGE, and the rows that see it come out NaN; such a
- * query value sets MLA_DEVFLAG_Q_RANGE and spoils its row.  (Long own keys are
- * read as they are, by the kernels of mla_decode_fwd, and follow its rules.)
+ * Keys and query rows are staged in f16: exact where f16 holds a value, else off
+ * by at most 2^-17 of its row's largest latent value or 2^-36 of its largest
+ * value (rows of small values are scaled by a power of two on the way; below
+ * 2^-69 that stops).  A magnitude beyond 65504 and a non-finite value are not
+ * held: such a key sets MLA_DEVFLAG_KV_RANGE, and the rows that see it come out
+ * NaN; such a query value sets MLA_DEVFLAG_Q_RANGE and spoils its row.  Own keys
+ * that the plan keeps apart (own_folded = 0, which the other sequences' lengths
+ * have a part in) are read as they are by the kernels of mla_decode_fwd and
+ * follow its rules: there a bf16 value beyond 65504 is a value.
  */
 typedef struct mla_decode_prefix_plan_t {
   int32_t version;       /* MLA_DECODE_PREFIX_PLAN_VERSION */

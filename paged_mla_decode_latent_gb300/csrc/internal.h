@@ -75,6 +75,13 @@ constexpr int kPrefixTile = 256;  // keys per tile
 // time of two tiles, measured), so a row block of n tiles counts for n + 2.
 constexpr int kSegmentTiles = 2;
 
+// What the staging notes of a row, a byte each: the two marks, and in the bits
+// from kStagedLift on the power of two that its values were multiplied by, in
+// steps of kLiftStep binary orders.
+constexpr uint32_t kStagedBadPage = 1;  // through a page id out of range
+constexpr uint32_t kStagedRange = 2;    // holds a value that f16 cannot
+constexpr int kStagedLift = 3, kLiftStep = 4, kMaxLift = 80;
+
 // `total` such units dealt to pairs in contiguous shares that differ by at most
 // one: pair i takes [start(i), start(i + 1)).
 struct PrefixShares {
@@ -104,8 +111,8 @@ struct PrefixShape {
   int2* parts;              // [row blocks]: the first pair that holds a part of one, and their number
   int32_t* own_off;         // [row blocks, block_seqs]: a sequence's first own key in its block's
   int32_t* status;
-  // Status bits of each staged key and query row (a bad page, values that f16
-  // cannot hold), for the attention to act on and to report.
+  // The note of each staged key and query row, for the attention to act on and
+  // to report.
   uint8_t *key_flags, *row_flags;
   int rows, rows_per_seq, heads, sq, causal, batch;
   int prefix_len, max_ctx;

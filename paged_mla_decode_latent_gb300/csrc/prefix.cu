@@ -35,6 +35,9 @@ constexpr int kChunk = 32;  // rows a staging CTA copies
 constexpr int kStageThreads = 256;
 constexpr int kStageIters = kChunk * kPieces / kStageThreads;  // 9 pieces a thread
 static_assert(kStageThreads == 8 * kChunk, "eight threads a row");
+constexpr int kLatentIters = MLA_D_V / 64;  // of them latent values
+static_assert(kLatentIters == kStageIters - 1, "the last piece is the rope dims");
+constexpr float kLowLatent = 0x1p-8f;  // bf16 rows whose latent values are all below it are lifted
 constexpr int kPadChunks = mla::kPrefixTile / kChunk;
 constexpr int kManyParts = 8;  // partials a row from which the merge takes eight warps a row
 // Own keys are folded in while they are at most this many, and their row
@@ -77,12 +80,61 @@ __device__ __forceinline__ uint4 to_f16(uint4 v, bool fp8) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The power of two that a row of small values is multiplied by, so that f16
+// keeps its bits: the largest, in steps, that leaves its largest magnitude
+// (`top`, a float's bits) below 2^15.
+__device__ __forceinline__ int lift_of(uint32_t top) {
+  const int e = 14 - ((int)(top >> 23) - 127);
+  return top == 0 ? 0 : min(mla::kMaxLift, max(0, e)) / mla::kLiftStep * mla::kLiftStep;
+}
+
+__device__ __forceinline__ uint32_t lifted(uint32_t w, float by) {
+  const __half2 v = __floats2half2_rn(__uint_as_float(w << 16) * by, __uint_as_float(w & 0xFFFF0000u) * by);
+  return *reinterpret_cast<const uint32_t*>(&v);
+}
+
 __device__ __forceinline__ __half2 abs2(uint32_t w) { return __habs2(*reinterpret_cast<const __half2*>(&w)); }
 
 __device__ __forceinline__ uint32_t finite_or_zero(uint32_t w) {
   if ((w & 0x7C00u) == 0x7C00u) w &= 0xFFFF0000u;
   if ((w & 0x7C000000u) == 0x7C000000u) w &= 0xFFFFu;
   return w;
+}
+
+// Stages a row again that is not as it should be, and returns its note.  Called by
+// the row's eight lanes, pieces as in the staging; rare, so out of line.  `src`:
+// the row in bf16, looked at only where all lanes find it low.
+__device__ __noinline__ uint32_t stage_again(const uint16_t* src, uint16_t* dst, bool over, bool low, bool query) {
+  const uint32_t row_lanes = 0xFFu << (threadIdx.x & 24);
+  uint4* out = reinterpret_cast<uint4*>(dst) + (threadIdx.x & 7);
+  if (__any_sync(row_lanes, over)) {
+    // A query value spoils its own row only; a key goes without what f16 cannot
+    // hold (0 x NaN would spoil rows that do not see it).
+#pragma unroll 1
+    for (int i = 0; over && !query && i < kStageIters; ++i) {
+      const uint4 w = out[8 * i];
+      out[8 * i] = make_uint4(finite_or_zero(w.x), finite_or_zero(w.y), finite_or_zero(w.z), finite_or_zero(w.w));
+    }
+    return mla::kStagedRange;
+  }
+  if (!__all_sync(row_lanes, low)) return 0;
+  const uint4* from = reinterpret_cast<const uint4*>(src) + (threadIdx.x & 7);
+  uint32_t most = 0;  // the largest magnitude, as a float's bits
+#pragma unroll 1
+  for (int i = 0; i < kStageIters; ++i) {
+    const uint4 w = from[8 * i];
+    const uint32_t a = max(w.x & 0x7FFF0000u, w.x << 17 >> 1), b = max(w.y & 0x7FFF0000u, w.y << 17 >> 1);
+    const uint32_t c = max(w.z & 0x7FFF0000u, w.z << 17 >> 1), d = max(w.w & 0x7FFF0000u, w.w << 17 >> 1);
+    most = max(most, max(max(a, b), max(c, d)));
+  }
+  const int lift = lift_of(__reduce_max_sync(row_lanes, most));
+  const float by = __uint_as_float((uint32_t)(127 + lift) << 23);
+#pragma unroll 1
+  for (int i = 0; lift > 0 && i < kStageIters; ++i) {
+    const uint4 w = from[8 * i];
+    out[8 * i] = make_uint4(lifted(w.x, by), lifted(w.y, by), lifted(w.z, by), lifted(w.w, by));
+  }
+  return (uint32_t)(lift / mla::kLiftStep) << mla::kStagedLift;
 }
 
 // The tiles of each row block, where each pair starts and where each sequence's
@@ -170,6 +222,11 @@ __device__ void partition(const StageParams& p) {
 // 1152 or 576 B in and 1152 B out a row, 9 loads in flight a thread.  Flags go
 // out as a byte for every row, not into words that something would have to
 // clear first: a clearing kernel before this one cost 1 us, and 2 of host time.
+//
+// f16 loses bits below 2^-14 (an absolute 2^-25).  A bf16 row whose latent
+// values are all below kLowLatent is staged once more, times a power of two that
+// the attention undoes; any other row is off by at most 2^-17 of its largest
+// latent value.  Ordinary rows pay for one vote.
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   ptx::launch_dependents();
   ptx::grid_dependency_wait();
@@ -240,6 +297,7 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   if (row >= n) return;
   uint4 v[kStageIters];
   bool fp8 = false, bad_page = false;
+  uint32_t at_row = 0;  // below 2^31, as num_pages * page_size is
   if (row < n_src && src != nullptr) {
     const uint4* at = reinterpret_cast<const uint4*>(src + row * MLA_D_QK) + sub;
 #pragma unroll
@@ -249,17 +307,17 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
     int64_t page = table[page_i];
     bad_page = page < 0 || page >= p.num_pages;
     if (bad_page) page = 0;
-    const int64_t at_row = page * p.page_size + (key - page_i * (uint32_t)p.page_size);
+    at_row = (uint32_t)(page * p.page_size + (key - page_i * (uint32_t)p.page_size));
     fp8 = p.fp8;
     if (fp8) {
-      const uint2* at = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + at_row * MLA_D_QK) + sub;
+      const uint2* at = reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.cache) + (int64_t)at_row * MLA_D_QK) + sub;
 #pragma unroll
       for (int i = 0; i < kStageIters; ++i) {
         const uint2 c = at[8 * i];
         v[i] = make_uint4(c.x, c.y, 0, 0);
       }
     } else {
-      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + at_row * MLA_D_QK) + sub;
+      const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p.cache) + (int64_t)at_row * MLA_D_QK) + sub;
 #pragma unroll
       for (int i = 0; i < kStageIters; ++i) v[i] = at[8 * i];
     }
@@ -268,27 +326,26 @@ __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
     for (int i = 0; i < kStageIters; ++i) v[i] = make_uint4(0, 0, 0, 0);
   }
   uint4* out = reinterpret_cast<uint4*>(dst + (dst_row + row) * MLA_D_QK) + sub;
-  __half2 top = __floats2half2_rn(0.f, 0.f);  // largest magnitude; NaN if there is one
+  // Largest magnitudes of the latent values and of all; NaN if there is one.
+  __half2 latent_top = __floats2half2_rn(0.f, 0.f), top;
 #pragma unroll
   for (int i = 0; i < kStageIters; ++i) {
     const uint4 w = to_f16(v[i], fp8);
     out[8 * i] = w;
-    top = __hmax2_nan(top, __hmax2_nan(__hmax2_nan(abs2(w.x), abs2(w.y)), __hmax2_nan(abs2(w.z), abs2(w.w))));
+    const __half2 most = __hmax2_nan(__hmax2_nan(abs2(w.x), abs2(w.y)), __hmax2_nan(abs2(w.z), abs2(w.w)));
+    if (i < kLatentIters) latent_top = __hmax2_nan(latent_top, most);
+    else top = __hmax2_nan(latent_top, most);
   }
   const bool over = not_finite(*reinterpret_cast<const uint32_t*>(&top));
-  const bool any = __any_sync(0xFFu << (threadIdx.x & 24), over);  // in the row
+  const bool low = !fp8 && row < n_src && __hblt2(latent_top, __float2half2_rn(kLowLatent));
+  const uint32_t row_lanes = 0xFFu << (threadIdx.x & 24);
+  uint32_t note = 0;
+  if (__any_sync(row_lanes, over || low))
+    note = stage_again(src != nullptr ? src + row * MLA_D_QK
+                                      : static_cast<const uint16_t*>(p.cache) + (int64_t)at_row * MLA_D_QK,
+                       dst + (dst_row + row) * MLA_D_QK, over, low, src != nullptr);
   if (sub == 0)
-    (src != nullptr ? g.row_flags : g.key_flags)[dst_row + row] =
-        (uint8_t)((bad_page ? MLA_DEVFLAG_BAD_PAGE : 0) |
-                  (any ? src != nullptr ? MLA_DEVFLAG_Q_RANGE : MLA_DEVFLAG_KV_RANGE : 0));
-  // Rare: a query value spoils its own row only; a key is staged anew without
-  // what f16 cannot hold (0 x NaN would spoil rows that do not see it).
-  if (!over || src != nullptr) return;
-#pragma unroll 1
-  for (int i = 0; i < kStageIters; ++i) {
-    const uint4 w = out[8 * i];
-    out[8 * i] = make_uint4(finite_or_zero(w.x), finite_or_zero(w.y), finite_or_zero(w.z), finite_or_zero(w.w));
-  }
+    (src != nullptr ? g.row_flags : g.key_flags)[dst_row + row] = (uint8_t)(note | (bad_page ? mla::kStagedBadPage : 0));
 }
 
 struct MergeParams {

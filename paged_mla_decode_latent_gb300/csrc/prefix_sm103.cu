@@ -21,6 +21,14 @@
 // needed.  Keys that f16 cannot hold are staged as zeros and remembered; rows
 // that see one come out NaN.
 //
+// Rows of small values come multiplied by a power of two: a query row's is taken
+// back in its own c, a key's 2^e in its score and its weight,
+//
+//   z_j = c 2^-e_j <q_r, k'_j>,   p_j = 2^(z_j - e_j - m),   o = sum_j p_j k'_j / sum_j p_j 2^e_j
+//
+// with m the running maximum of z_j - e_j, so that the weights keep their bits
+// whatever the keys' magnitudes are.  Only tiles that hold such a key pay.
+//
 // Split over a CTA pair.  An fp32 accumulator of 128 rows x 512 value dims
 // fills the TMEM of one SM, so a pair shares the 128 rows: `cta_group::2` MMAs
 // with M = 128 give each CTA 64 rows and put the two halves of N on the two
@@ -216,19 +224,32 @@ struct Walk {
   }
 };
 
-// Reports the flags of a warp's 64 keys (four in each of 16 lanes, twice);
-// returns the row's sum of weights, NaN if it sees a key that f16 cannot hold,
-// [from, lim) being those that it sees.  Rare, so out of line.
-__device__ __noinline__ float flagged_keys(const mla::PrefixShape& g, uint32_t flags, int from, int lim, float l) {
+// The note of key i of a warp's 64 (four in each of 16 lanes, twice).
+__device__ __forceinline__ uint32_t note_of(uint32_t notes, int i) {
+  return __shfl_sync(0xffffffffu, notes, i / 4) >> (8 * (i % 4)) & 0xFFu;
+}
+
+// Reports the marks of a warp's 64 keys; returns the row's sum of weights, NaN
+// if it sees a key that f16 cannot hold, [from, lim) being those that it sees.
+// Rare, so out of line.
+__device__ __noinline__ float marked_keys(const mla::PrefixShape& g, uint32_t notes, int from, int lim, float l) {
   uint32_t all = 0;
   for (int i = 0; i < 64; ++i) {
-    const uint32_t f = __shfl_sync(0xffffffffu, flags, i / 4) >> (8 * (i % 4)) & 0xFFu;
+    const uint32_t f = note_of(notes, i);
     all |= f;
-    if ((f & MLA_DEVFLAG_KV_RANGE) && i >= from && i < lim) l = NAN;
+    if ((f & mla::kStagedRange) && i >= from && i < lim) l = NAN;
   }
-  if ((threadIdx.x & 31) == 0) atomicOr(g.status, (int)all);
+  if ((threadIdx.x & 31) == 0)
+    atomicOr(g.status, (all & mla::kStagedBadPage ? MLA_DEVFLAG_BAD_PAGE : 0) |
+                           (all & mla::kStagedRange ? MLA_DEVFLAG_KV_RANGE : 0));
   return l;
 }
+
+constexpr uint32_t kMarks = (mla::kStagedBadPage | mla::kStagedRange) * 0x01010101u;  // of four rows
+
+// The binary orders that a row was lifted by, and 2^e.
+__device__ __forceinline__ int lift_of(uint32_t note) { return (int)(note >> mla::kStagedLift) * mla::kLiftStep; }
+__device__ __forceinline__ float power2(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 
 template <bool kPoll>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
@@ -426,20 +447,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int dim0 = 256 * (q4 >> 1) + 128 * ch;
     const uint32_t lanes = (uint32_t)(32 * q4) << 16;
     const float s_kv = p.kv_scale != nullptr ? *p.kv_scale : 1.f;
-    // A scale of zero is taken as the smallest that keeps -inf * c2 = -inf.
-    const float c2 = fmaxf(p.softmax_scale * s_kv * 1.4426950408889634f, 1.0e-37f);
     const uint32_t p_full = ptx::mapa(ptx::smem_u32(&bars.p_full), 0);
     const uint32_t o_free = ptx::mapa(ptx::smem_u32(&bars.o_free), 0);
     volatile float* xch = reinterpret_cast<volatile float*>(smem + OFF_X);
     const uint32_t p_row = sbase + OFF_P + kg * PSLAB + r * 128;
-    const uint32_t* key_flags = reinterpret_cast<const uint32_t*>(p.g.key_flags + 64 * kg) + (lane & 15);
+    const uint32_t* key_notes = reinterpret_cast<const uint32_t*>(p.g.key_flags + 64 * kg) + (lane & 15);
     uint32_t it = 0;
     while (w.next()) {
       const int row = w.rb * mla::kRowTile + 64 * (int)rank + r;
       // The row sees the first `shared` keys of the prefix and, of its row
       // block's own keys, [own0, own1).
       int shared = 0, own0 = 0, own1 = 0;
+      uint32_t row_note = 0;
       if (row < p.g.rows) {
+        row_note = p.g.row_flags[row];
         const int b = row / p.g.rows_per_seq, n_vis = p.g.visible(row, b);
         shared = min(n_vis, p.g.prefix_len);
         if (p.g.fold) {
@@ -447,10 +468,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           own1 = own0 + max(0, n_vis - p.g.prefix_len);
         }
       }
-      if (kg == 0 && row < p.g.rows && p.g.row_flags[row] != 0) atomicOr(p.g.status, p.g.row_flags[row]);
+      if (kg == 0 && (row_note & mla::kStagedRange)) atomicOr(p.g.status, MLA_DEVFLAG_Q_RANGE);
+      // A scale of zero is taken as the smallest that keeps -inf * c2 = -inf.
+      const float c2 = fmaxf(p.softmax_scale * s_kv * 1.4426950408889634f * power2(-lift_of(row_note)), 1.0e-37f);
       float m = kMaxSentinel, l = 0.f;
       for (int t = w.t0; t < w.t1; ++t, ++it) {
-        const uint32_t flags = key_flags[w.key_row(t) / 4];  // of four of this warp's 64 keys
+        const uint32_t notes = key_notes[w.key_row(t) / 4];  // of four of this warp's 64 keys
         wait(c, ptx::smem_u32(&bars.s_full[it & 1]), (it >> 1) & 1);
         __syncwarp();
         ptx::tc_fence_after();
@@ -469,6 +492,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int i = 0; i < 32; ++i)
               if (32 * h + i < from || 32 * h + i >= lim) s[h][i] = 0xFF800000u;  // -inf: weight 0
         }
+        const bool noted = __any_sync(0xffffffffu, notes != 0);
+        float by = c2;  // s times this: z - e
+        if (noted) {
+          by = 1.f;
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int e = lift_of(note_of(notes, 32 * h + i));
+              s[h][i] = __float_as_uint(fmaf(__uint_as_float(s[h][i]) * power2(-e), c2, (float)-e));
+            }
+        }
         float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int h = 0; h < 2; ++h)
@@ -476,9 +511,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], __uint_as_float(s[h][i]));
         const float mine = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
         volatile float* x = xch + (it & 1) * 256;
-        x[kg * 64 + r] = mine;
+        x[kg * 64 + r] = mine * by;
         group_sync(q4 & 1);
-        const float mt = fmaxf(fmaxf(x[r], x[64 + r]), fmaxf(x[128 + r], x[192 + r])) * c2;
+        const float mt = fmaxf(fmaxf(x[r], x[64 + r]), fmaxf(x[128 + r], x[192 + r]));
         // The row's maximum moves only when it lags by more than kLag; a row
         // that has seen no key yet keeps the sentinel.
         const bool need = mt > m + kLag;
@@ -487,20 +522,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         m = mn;
         l *= alpha;
         const float base = kHead - m;
+        float lifted_sum = 0.f;  // of 2^e_j p_j
+        if (noted) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              lifted_sum = fmaf(fast_exp2(__uint_as_float(s[h][i]) + base),
+                                power2(lift_of(note_of(notes, 32 * h + i))), lifted_sum);
+        }
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pk[32];
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float a = fast_exp2(fmaf(__uint_as_float(s[h][i]), c2, base));
-            const float b2 = fast_exp2(fmaf(__uint_as_float(s[h][i + 1]), c2, base));
+            const float a = fast_exp2(fmaf(__uint_as_float(s[h][i]), by, base));
+            const float b2 = fast_exp2(fmaf(__uint_as_float(s[h][i + 1]), by, base));
             sum[i & 3] += a;
             sum[(i & 3) + 1] += b2;
             pk[16 * h + i / 2] = pack_f16(a, b2);
           }
-        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-        if (__any_sync(0xffffffffu, flags != 0)) l = flagged_keys(p.g, flags, from, lim, l);
+        l += noted ? lifted_sum : (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        if (__any_sync(0xffffffffu, (notes & kMarks) != 0)) l = marked_keys(p.g, notes, from, lim, l);
         // The weights' buffer and O are free once the values of the tile
         // before are accumulated (a segment's first tile waited for that at
         // the end of the segment before).
