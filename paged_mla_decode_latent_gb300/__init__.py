@@ -19,6 +19,7 @@ freshly allocated outputs and workspace, for convenience.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import math
 import os
@@ -231,6 +232,26 @@ def _raw_stream(stream, device: int) -> int:
     if stream is None:
         return _torch()._C._cuda_getCurrentRawStream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream):
+    """A context in which torch allocates and copies on `stream` (None: the current one)."""
+    if stream is None:
+        return contextlib.nullcontext()
+    torch = _torch()
+    if not hasattr(stream, "cuda_stream"):
+        # 0 and 1 (cudaStreamLegacy) name the default stream, which no ExternalStream wraps.
+        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) > 1 else torch.cuda.default_stream()
+    return torch.cuda.stream(stream)
+
+
+def _results(stream, *tensors):
+    """Results that `stream` owns, for use on the current stream: their memory is not handed out
+    again while that one may still read them."""
+    if stream is not None:
+        for t in tensors:
+            t.record_stream(_torch().cuda.current_stream(t.device))
+    return tensors
 
 
 def plan(seq_lens_host, num_heads: int, sq: int, page_size: int, kv_dtype: int = KV_BF16,
@@ -471,23 +492,26 @@ def prefix_check(p: PrefixPlan, workspace, stream=None) -> int:
 def decode_prefix(q, kv_cache, prefix_table, block_table, seq_lens, prefix_len: int,
                   seq_lens_host=None, kv_scale=None, softmax_scale: float | None = None,
                   causal: bool = False, p: PrefixPlan | None = None, workspace=None, stream=None):
-    """prefix_plan + prefix_fwd; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H])."""
+    """prefix_plan + prefix_fwd; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H]).  With `stream`
+    given, what is allocated belongs to it; the caller orders it behind whatever wrote the inputs
+    and keeps those until it is done."""
     import torch
     B, Sq, H, D = q.shape
     assert D == D_QK
     kv_dtype = KV_FP8_E4M3 if kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn) else KV_BF16
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(192.0)
-    if p is None:
-        host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
-        p = prefix_plan(host, prefix_len, H, Sq, int(kv_cache.shape[1]), kv_dtype, causal)
-    if workspace is None:
-        workspace = workspace_for(p, q.device)
-    out = torch.empty((B, Sq, H, D_V), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
-    prefix_fwd(p, q, kv_cache, kv_scale, prefix_table, block_table, seq_lens, softmax_scale, out,
-               lse, workspace, stream)
-    return out, lse
+    with _on(stream):
+        if p is None:
+            host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
+            p = prefix_plan(host, prefix_len, H, Sq, int(kv_cache.shape[1]), kv_dtype, causal)
+        if workspace is None:
+            workspace = workspace_for(p, q.device)
+        out = torch.empty((B, Sq, H, D_V), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
+        prefix_fwd(p, q, kv_cache, kv_scale, prefix_table, block_table, seq_lens, softmax_scale, out,
+                   lse, workspace, stream)
+    return _results(stream, out, lse)
 
 
 def workspace_for(p, device="cuda"):
@@ -499,20 +523,22 @@ def workspace_for(p, device="cuda"):
 def decode(q, kv_cache, block_table, seq_lens, seq_lens_host=None, kv_scale=None,
            softmax_scale: float | None = None, causal: bool = False, p: Plan | None = None,
            workspace=None, stream=None):
-    """plan + fwd + combine; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H])."""
+    """plan + fwd + combine; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H]).  `stream` as in
+    ``decode_prefix``."""
     import torch
     B, Sq, H, D = q.shape
     assert D == D_QK
     kv_dtype = KV_FP8_E4M3 if kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn) else KV_BF16
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(192.0)
-    if p is None:
-        host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
-        p = plan(host, H, Sq, int(kv_cache.shape[1]), kv_dtype, causal)
-    if workspace is None:
-        workspace = workspace_for(p, q.device)
-    out = torch.empty((B, Sq, H, D_V), dtype=torch.bfloat16, device=q.device)
-    lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
-    fwd(p, q, kv_cache, kv_scale, block_table, seq_lens, softmax_scale, out, lse, workspace, stream)
-    combine(p, seq_lens, out, lse, workspace, stream)
-    return out, lse
+    with _on(stream):
+        if p is None:
+            host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
+            p = plan(host, H, Sq, int(kv_cache.shape[1]), kv_dtype, causal)
+        if workspace is None:
+            workspace = workspace_for(p, q.device)
+        out = torch.empty((B, Sq, H, D_V), dtype=torch.bfloat16, device=q.device)
+        lse = torch.empty((B, Sq, H), dtype=torch.float32, device=q.device)
+        fwd(p, q, kv_cache, kv_scale, block_table, seq_lens, softmax_scale, out, lse, workspace, stream)
+        combine(p, seq_lens, out, lse, workspace, stream)
+    return _results(stream, out, lse)
