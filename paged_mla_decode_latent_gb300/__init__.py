@@ -491,10 +491,11 @@ def prefix_check(p: PrefixPlan, workspace, stream=None) -> int:
 
 def decode_prefix(q, kv_cache, prefix_table, block_table, seq_lens, prefix_len: int,
                   seq_lens_host=None, kv_scale=None, softmax_scale: float | None = None,
-                  causal: bool = False, p: PrefixPlan | None = None, workspace=None, stream=None):
-    """prefix_plan + prefix_fwd; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H]).  With `stream`
-    given, what is allocated belongs to it; the caller orders it behind whatever wrote the inputs
-    and keeps those until it is done."""
+                  causal: bool | None = None, p: PrefixPlan | None = None, workspace=None, stream=None):
+    """prefix_plan + prefix_fwd; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H]).  With `p`
+    given, prefix_len is the plan's, and causal too unless it is None (the default: no mask, or
+    the plan's).  With `stream` given, what is allocated belongs to it; the caller orders it behind
+    whatever wrote the inputs and keeps those until it is done."""
     import torch
     B, Sq, H, D = q.shape
     assert D == D_QK
@@ -504,7 +505,9 @@ def decode_prefix(q, kv_cache, prefix_table, block_table, seq_lens, prefix_len: 
     with _on(stream):
         if p is None:
             host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
-            p = prefix_plan(host, prefix_len, H, Sq, int(kv_cache.shape[1]), kv_dtype, causal)
+            p = prefix_plan(host, prefix_len, H, Sq, int(kv_cache.shape[1]), kv_dtype, bool(causal))
+        elif p.prefix_len != prefix_len or causal is not None and bool(p.causal) != bool(causal):
+            raise MLADecodeError(ERR_INVALID_ARG, "decode_prefix: the plan is for another prefix length or mask")
         if workspace is None:
             workspace = workspace_for(p, q.device)
         out = torch.empty((B, Sq, H, D_V), dtype=torch.bfloat16, device=q.device)

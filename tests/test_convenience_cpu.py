@@ -81,3 +81,19 @@ def test_without_a_stream_the_current_one_does(recorded, which):
     log, kept, note = recorded
     call(which, note)
     assert all(s is None for _, s in log) and kept == []
+
+
+@pytest.mark.parametrize("plan_causal", [False, True])
+def test_a_plan_for_something_else_is_refused(recorded, plan_causal):
+    """The plan's prefix length and mask are the call's: arguments that contradict it raise."""
+    log, _, note = recorded
+    p = mla.prefix_plan([300, 290], 256, 16, 1, 16, mla.KV_BF16, plan_causal)
+    call("decode_prefix", note, p=p)
+    call("decode_prefix", note, p=p, causal=plan_causal)
+    with pytest.raises(mla.MLADecodeError) as e:
+        call("decode_prefix", note, p=p, causal=not plan_causal)
+    assert e.value.status == mla.ERR_INVALID_ARG
+    with pytest.raises(mla.MLADecodeError) as e:
+        call("decode_prefix", note, p=mla.prefix_plan([300, 290], 255, 16, 1, 16, mla.KV_BF16, plan_causal))
+    assert e.value.status == mla.ERR_INVALID_ARG
+    assert [w for w, _ in log].count("prefix_fwd") == 2
