@@ -546,7 +546,8 @@ typedef struct mla_decode_prefix_plan_t {
  * count the prefix.  The plan stays valid for later calls whose contexts are
  * all <= plan->max_ctx, with the same prefix length.  Pure host code.
  * Returns MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (more than
- * MLA_PREFIX_MAX_ROWS rows) or MLA_ERR_CUDA. */
+ * MLA_PREFIX_MAX_ROWS rows, or own keys whose last chunk would end past 2^31)
+ * or MLA_ERR_CUDA. */
 int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batch, int32_t prefix_len,
                            int32_t num_heads, int32_t sq, int32_t page_size, int32_t kv_dtype,
                            int32_t causal, int32_t num_sms, mla_decode_prefix_plan_t* plan);

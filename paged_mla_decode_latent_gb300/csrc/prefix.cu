@@ -471,6 +471,12 @@ bool room_to_fold(int64_t batch, int rows, int64_t own) {
          blocks * ceil_div(keys, mla::kPrefixTile) * mla::kPrefixTile <= kMaxRegionRows;
 }
 
+// The decode kernels count keys in int32, up to the last chunk's end.
+bool chunks_fit(const mla_decode_prefix_plan_t& p) {
+  return p.own_splits == 0 ||
+         (p.own_chunk > 0 && p.prefix_len + (int64_t)p.own_splits * p.own_chunk <= INT32_MAX);
+}
+
 // Staged rows of keys: the shared ones and each row block's own, in whole tiles.
 int64_t staged_keys(const mla_decode_prefix_plan_t& p) {
   return (int64_t)p.prefix_tiles * mla::kPrefixTile + (int64_t)p.row_blocks * p.block_keys;
@@ -553,7 +559,7 @@ int check_plan(const mla_decode_prefix_plan_t* p) {
   const int64_t own = std::max(0, p->max_ctx - p->prefix_len);
   if (p->own_folded ? p->prefix_len == 0 || p->own_splits != 0 ||
                           !room_to_fold(p->batch, p->num_heads * p->sq, own)
-                    : (int64_t)p->own_splits * p->own_chunk < own)
+                    : (int64_t)p->own_splits * p->own_chunk < own || !chunks_fit(*p))
     return MLA_ERR_INVALID_ARG;
   // Everything else is what lay_out makes of these: a plan whose other fields
   // differ was edited.
@@ -605,6 +611,7 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
     p.num_sms = d.num_sms;
     p.own_chunk = d.chunk_len;
     p.own_splits = d.max_ctx > 0 ? d.num_splits : 0;
+    if (!chunks_fit(p)) return MLA_ERR_UNSUPPORTED;
     lay_out(&p);
 
     // Measured on GB300 (us): a 256-key tile on one pair, a segment's query
