@@ -378,6 +378,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto pass = [&](uint32_t bar, uint32_t parity) {
         return __all_sync(0xffffffffu, wait(c, bar, parity)) != 0;
       };
+      // A barrier that both CTAs' softmax warps arrive on: what they wrote (their
+      // halves of P, their rows of O) comes before the MMAs that follow.
+      auto pass_pair = [&](uint32_t bar, uint32_t parity) {
+        if (!pass(bar, parity)) return false;
+        ptx::mbar_acquire_cluster(bar, parity);
+        return true;
+      };
       auto take = [&] {
         if (!ready && !pass(full0 + 8 * slot, ph)) return false;
         ptx::tc_fence_after();
@@ -416,8 +423,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           if (t == 0) continue;
           // O is free once the segment before is read.
-          if (t == 1 && seg > 0 && !pass(ptx::smem_u32(&bars.o_free), (seg - 1) & 1)) goto mma_end;
-          if (!pass(ptx::smem_u32(&bars.p_full), (it - 1 - (t < n)) & 1)) goto mma_end;
+          if (t == 1 && seg > 0 && !pass_pair(ptx::smem_u32(&bars.o_free), (seg - 1) & 1)) goto mma_end;
+          if (!pass_pair(ptx::smem_u32(&bars.p_full), (it - 1 - (t < n)) & 1)) goto mma_end;
 #pragma unroll 8
           for (int v = 0; v < 8; ++v) {  // 64-key group v / 2, O columns 128 (v % 2)
             if (!take()) goto mma_end;

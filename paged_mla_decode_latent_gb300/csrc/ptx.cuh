@@ -386,13 +386,26 @@ __device__ __forceinline__ void prefetch_tensormap(const void* tmap) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
 }
 
-// Arrive on a barrier of another CTA of the cluster, releasing this CTA's
-// writes at CTA scope: for operands that the other CTA's thread only hands to
-// an MMA, which reads them in this CTA's own shared memory (the writer's proxy
-// fence has made them visible there).  A release at cluster scope took about
-// 1900 cycles here.
+// Arrive on a barrier of another CTA of the cluster, at cluster scope, after this
+// thread's writes to its own CTA's shared memory and those it has seen: the
+// fence is restricted to that memory, so it waits for nothing else.  (A plain
+// arrive.release.cluster took about 1900 cycles here, and 2 to 9% of the whole
+// prefix call; this one takes 0.2 us of its smallest.)  The other side acquires
+// at the same scope, mbar_acquire_cluster.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
+  asm volatile(
+      "fence.release.sync_restrict::shared::cta.cluster;\n\t"
+      "mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+      : "memory");
+}
+
+// For a phase that a wait of CTA scope has found complete: what the arrivals of
+// the cluster's other CTAs released is ordered before what follows.
+__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar), "r"(parity)
+      : "memory");
 }
 
 // ------------------------------------------------- programmatic launch ---
