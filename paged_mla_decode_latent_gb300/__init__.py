@@ -234,14 +234,15 @@ def _raw_stream(stream, device: int) -> int:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _on(stream):
-    """A context in which torch allocates and copies on `stream` (None: the current one)."""
+def _on(stream, device):
+    """A context in which torch allocates and copies on `stream` of `device` (None: the current one)."""
     if stream is None:
         return contextlib.nullcontext()
     torch = _torch()
     if not hasattr(stream, "cuda_stream"):
         # 0 and 1 (cudaStreamLegacy) name the default stream, which no ExternalStream wraps.
-        stream = torch.cuda.ExternalStream(int(stream)) if int(stream) > 1 else torch.cuda.default_stream()
+        stream = (torch.cuda.ExternalStream(int(stream), device=device) if int(stream) > 1
+                  else torch.cuda.default_stream(device))
     return torch.cuda.stream(stream)
 
 
@@ -502,7 +503,7 @@ def decode_prefix(q, kv_cache, prefix_table, block_table, seq_lens, prefix_len: 
     kv_dtype = KV_FP8_E4M3 if kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn) else KV_BF16
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(192.0)
-    with _on(stream):
+    with _on(stream, q.device):
         if p is None:
             host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
             p = prefix_plan(host, prefix_len, H, Sq, int(kv_cache.shape[1]), kv_dtype, bool(causal))
@@ -534,7 +535,7 @@ def decode(q, kv_cache, block_table, seq_lens, seq_lens_host=None, kv_scale=None
     kv_dtype = KV_FP8_E4M3 if kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn) else KV_BF16
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(192.0)
-    with _on(stream):
+    with _on(stream, q.device):
         if p is None:
             host = seq_lens_host if seq_lens_host is not None else seq_lens.cpu()
             p = plan(host, H, Sq, int(kv_cache.shape[1]), kv_dtype, causal)
