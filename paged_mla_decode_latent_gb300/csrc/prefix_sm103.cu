@@ -97,6 +97,11 @@ constexpr uint32_t TM_COLS = 512;
 // maximum is current at 2^kHead, so 21 binary orders below it keep all 11
 // bits; the running maximum may lag by kLag before O is rescaled, and 2^(kHead
 // + kLag) = 32768 stays below the largest f16.
+//
+// 11 bits put an output off by about 1e-4 in norm, against the 1.65e-3 of its
+// own rounding to bf16 (the sum keeps the weights unrounded).  The decode
+// kernels' two bf16 terms give heavy keys 16 bits and light ones 8; a second
+// f16 term would cost eight more value slabs beside a tile's seventeen.
 constexpr float kHead = 7.f, kLag = 8.f;
 constexpr float kMaxSentinel = -1.0e30f;
 constexpr uint64_t kDrainNs = 500000000ull;
@@ -127,8 +132,8 @@ struct Ctx {
 // (polling warps slow the MMA and load loops down) and reads the timer, which
 // costs hundreds of cycles, only once a whole sleep has passed in vain.  Out
 // of line, so that the loops around the waits stay short: with this inlined
-// and the slab loops unrolled they ran from the instruction cache's misses
-// (136 against 107 us at batch 64 x 8192).
+// and the slab loops unrolled batch 64 x 8192 took 136 us against 107 (the
+// instruction cache's misses, probably).
 // kPoll: a limit below a sleep; every try returns at once.
 template <bool kPoll>
 __device__ __noinline__ bool wait_slow(const Ctx& c, uint32_t bar, uint32_t parity) {
@@ -155,6 +160,7 @@ __device__ __forceinline__ bool wait_for(const Ctx& c, uint32_t bar, uint32_t pa
          wait_slow<kPoll>(c, bar, parity);
 }
 
+// 2^-22 relative, far inside the 11 bits that the weights keep.
 __device__ __forceinline__ float fast_exp2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -189,9 +195,10 @@ __device__ __forceinline__ void group_sync(int g) {
 // A loaded value that is the same in every lane, as a uniform one.
 __device__ __forceinline__ int uniform(int x) { return __shfl_sync(0xffffffffu, x, 0); }
 
-// A pair's walk over its segments (the whole warp's: loop bounds that are not
-// known to be uniform cost the MMA loop its uniform registers, 517 against
-// 459 us at batch 128 x 23333): tiles [t0, t1) of row block rb, which has n.
+// A pair's walk over its segments (the whole warp's, with loop bounds made
+// uniform by a shuffle: without it batch 128 x 23333 took 517 us against 459,
+// probably for the MMA loop's addresses, which then need vector registers):
+// tiles [t0, t1) of row block rb, which has n.
 struct Walk {
   const mla::PrefixShape& g;
   int next_rb, next_t, next_n, end_rb, end_t;
@@ -261,8 +268,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                                              ~static_cast<uintptr_t>(1023));
   Bars& bars = *reinterpret_cast<Bars*>(smem + OFF_BAR);
   const uint32_t sbase = ptx::smem_u32(smem);
-  // Through a shuffle, so that the compiler knows the warp index is uniform:
-  // the MMA and load loops then keep their addresses in uniform registers.
+  // Through a shuffle, so that the compiler can take the warp index as uniform,
+  // and the MMA and load loops' addresses with it.
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const uint32_t rank = blockIdx.x & 1;  // the CTA's rank in its cluster, as a uniform value
   const int pair = blockIdx.x >> 1;
