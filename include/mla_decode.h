@@ -499,14 +499,15 @@ int mla_decode_fwd_noalloc(const mla_decode_plan_t* plan, const void* q, const v
  * page_size on are read.
  *
  * Keys and query rows are staged in f16: exact where f16 holds a value, else off
- * by at most 2^-17 of its row's largest latent value or 2^-36 of its largest
- * value (rows of small values are scaled by a power of two on the way; below
- * 2^-69 that stops).  A magnitude beyond 65504 and a non-finite value are not
- * held: such a key sets MLA_DEVFLAG_KV_RANGE, and the rows that see it come out
- * NaN; such a query value sets MLA_DEVFLAG_Q_RANGE and spoils its row.  Own keys
- * that the plan keeps apart (own_folded = 0, which the other sequences' lengths
- * have a part in) are read as they are by the kernels of mla_decode_fwd and
- * follow its rules: there a bf16 value beyond 65504 is a value.
+ * by at most 2^-17 of a key's largest latent value or a query row's largest
+ * value, or 2^-36 of the row's largest value (rows of small values are scaled by
+ * a power of two on the way; where all are below 2^-88 that stops).  A magnitude
+ * beyond 65504 and a non-finite value are not held: such a key sets
+ * MLA_DEVFLAG_KV_RANGE, and the rows that see it come out NaN; such a query value
+ * sets MLA_DEVFLAG_Q_RANGE and spoils its row.  Own keys that the plan keeps apart
+ * (own_folded = 0, which the other sequences' lengths have a part in) are read as
+ * they are by the kernels of mla_decode_fwd and follow its rules: there a bf16
+ * value beyond 65504 is a value.
  */
 typedef struct mla_decode_prefix_plan_t {
   int32_t version;       /* MLA_DECODE_PREFIX_PLAN_VERSION */

@@ -37,7 +37,8 @@ constexpr int kStageIters = kChunk * kPieces / kStageThreads;  // 9 pieces a thr
 static_assert(kStageThreads == 8 * kChunk, "eight threads a row");
 constexpr int kLatentIters = MLA_D_V / 64;  // of them latent values
 static_assert(kLatentIters == kStageIters - 1, "the last piece is the rope dims");
-constexpr float kLowLatent = 0x1p-8f;  // bf16 rows whose latent values are all below it are lifted
+constexpr int kLowExponent = -8;  // bf16 rows whose latent values are all below 2^-8 are lifted
+constexpr float kLowLatent = 0x1p-8f;
 constexpr int kPadChunks = mla::kPrefixTile / kChunk;
 constexpr int kManyParts = 8;  // partials a row from which the merge takes eight warps a row
 // Own keys are folded in while they are at most this many, and their row
@@ -80,12 +81,18 @@ __device__ __forceinline__ uint4 to_f16(uint4 v, bool fp8) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// The power of two that a row of small values is multiplied by, so that f16
-// keeps its bits: the largest, in steps, that leaves its largest magnitude
-// (`top`, a float's bits) below 2^15.
-__device__ __forceinline__ int lift_of(uint32_t top) {
-  const int e = 14 - ((int)(top >> 23) - 127);
-  return top == 0 ? 0 : min(mla::kMaxLift, max(0, e)) / mla::kLiftStep * mla::kLiftStep;
+// The binary orders that a row of small values is lifted by: as few steps as bring
+// its largest latent value to kLowLatent, while its largest of all, `top`, stays
+// below 2^15 (both a float's bits; for a query, whose latent values are nothing by
+// themselves, and for a row without any, `latent` is `top`).  No more than that: a
+// key's weight shrinks by as much, and has to stand beside those of keys that are
+// just not lifted (with lifted rows brought to 2^15, light keys beside such a one
+// were lost, 6% of the output).
+__device__ __forceinline__ int lift_of(uint32_t latent, uint32_t top) {
+  const int want = kLowExponent - ((int)(latent >> 23) - 127);
+  const int room = 14 - ((int)(top >> 23) - 127);
+  const int e = (max(0, want) + mla::kLiftStep - 1) / mla::kLiftStep * mla::kLiftStep;
+  return min(min(e, mla::kMaxLift), max(0, room) / mla::kLiftStep * mla::kLiftStep);
 }
 
 __device__ __forceinline__ uint32_t lifted(uint32_t w, float by) {
@@ -119,15 +126,19 @@ __device__ __noinline__ uint32_t stage_again(const uint16_t* src, uint16_t* dst,
   }
   if (!__all_sync(row_lanes, low)) return 0;
   const uint4* from = reinterpret_cast<const uint4*>(src) + (threadIdx.x & 7);
-  uint32_t most = 0;  // the largest magnitude, as a float's bits
+  uint32_t latent = 0, most = 0;  // largest magnitudes, as a float's bits
 #pragma unroll 1
   for (int i = 0; i < kStageIters; ++i) {
     const uint4 w = from[8 * i];
     const uint32_t a = max(w.x & 0x7FFF0000u, w.x << 17 >> 1), b = max(w.y & 0x7FFF0000u, w.y << 17 >> 1);
     const uint32_t c = max(w.z & 0x7FFF0000u, w.z << 17 >> 1), d = max(w.w & 0x7FFF0000u, w.w << 17 >> 1);
     most = max(most, max(max(a, b), max(c, d)));
+    if (i < kLatentIters) latent = most;
   }
-  const int lift = lift_of(__reduce_max_sync(row_lanes, most));
+  latent = __reduce_max_sync(row_lanes, latent);
+  most = __reduce_max_sync(row_lanes, most);
+  if (query || latent == 0) latent = most;
+  const int lift = most == 0 ? 0 : lift_of(latent, most);
   const float by = __uint_as_float((uint32_t)(127 + lift) << 23);
 #pragma unroll 1
   for (int i = 0; lift > 0 && i < kStageIters; ++i) {
@@ -225,7 +236,7 @@ __device__ void partition(const StageParams& p) {
 //
 // f16 loses bits below 2^-14 (an absolute 2^-25).  A bf16 row whose latent
 // values are all below kLowLatent is staged once more, times a power of two that
-// the attention undoes; any other row is off by at most 2^-17 of its largest
+// the attention undoes; any row is then off by at most 2^-17 of its largest
 // latent value.  Ordinary rows pay for one vote.
 __global__ void __launch_bounds__(kStageThreads) stage_kernel(StageParams p) {
   ptx::launch_dependents();

@@ -130,3 +130,49 @@ def test_zero_rows_and_subnormals():
     out, lse, _, status = p.run()
     assert status == 0
     check_rows(p, out, lse, "zeros and subnormals")
+
+
+@pytest.mark.parametrize("k", [8, 9, 10, 11, 12])
+@pytest.mark.parametrize("flat", [False, True])
+def test_keys_about_the_border_of_what_is_scaled(k, flat):
+    """Thousands of keys of one magnitude, of which some are scaled when staged and some are not: their
+    weights keep the same bits.  flat: scores near zero, so that every key counts."""
+    p = PrefixProblem(6, 1, 64, [2203 - 30 * i for i in range(6)], 2158, 64, seed=k, q_mult=2.0 ** k,
+                      scale=syn.DEFAULT_SCALE * (2.0 ** -10 if flat else 1.0))
+    p.cache = scale_bits(p.cache, 2.0 ** -k)
+    out, lse, _, status = p.run()
+    assert status == 0
+    check_rows(p, out, lse, f"2^-{k}")
+
+
+def test_keys_of_two_magnitudes():
+    """Half of the keys at 2^-10, half of order one, in rows whose scores favour either."""
+    p = PrefixProblem(8, 1, 64, [2203 - i for i in range(8)], 2158, 64, seed=3)
+    flat = p.cache.reshape(-1, 576)
+    half = np.random.default_rng(4).random((flat.shape[0], 1)) < 0.5
+    p.cache = scale_bits(flat, np.where(half, 2.0 ** -10, 1.0)).reshape(p.cache.shape)
+    out, lse, _, status = p.run()
+    assert status == 0
+    check_rows(p, out, lse, "two magnitudes")
+
+
+@pytest.mark.parametrize("spike", [2.0 ** -8, 2.0 ** -6, 2.0 ** -4, 1.0, 2.0 ** 6])
+def test_many_light_small_keys_beside_a_heavy_one(spike):
+    """2100 equal keys of magnitude 2^-10 with e^-8 of the weight of one that a single large value keeps
+    from being scaled: together they hold a third of the output's other dims."""
+    p = PrefixProblem(2, 1, 16, [2110, 2120], 2100, 1, seed=5, scale=1.0)
+    rng = np.random.default_rng(6)
+    row = np.zeros((2, 576), np.float32)
+    row[:, :512] = rng.standard_normal((2, 512)).clip(-2, 2) * 2.0 ** -10
+    row[0, 7], row[0, 512] = spike, 2.0 ** -9
+    p.cache.reshape(-1, 576)[:] = syn.f32_to_bf16_bits(row[1])
+    p.cache[p.prefix_table[50], 0] = syn.f32_to_bf16_bits(row[0])
+    q = np.zeros(p.q_bits.shape, np.float32)
+    q[..., 512] = 2.0 ** 12
+    p.q_bits = syn.f32_to_bf16_bits(q)
+    out, lse, _, status = p.run()
+    assert status == 0
+    ref, ref_lse = p.reference()
+    rest = np.arange(512) != 7
+    err = np.linalg.norm((out - ref)[..., rest], axis=-1) / np.linalg.norm(ref[..., rest], axis=-1)
+    assert err.max() <= 4e-3 and np.abs(lse - ref_lse).max() <= 1e-3
