@@ -496,7 +496,9 @@ def decode_prefix(q, kv_cache, prefix_table, block_table, seq_lens, prefix_len: 
     """prefix_plan + prefix_fwd; returns (out bf16 [B,Sq,H,512], lse fp32 [B,Sq,H]).  With `p`
     given, prefix_len is the plan's, and causal too unless it is None (the default: no mask, or
     the plan's).  With `stream` given, what is allocated belongs to it; the caller orders it behind
-    whatever wrote the inputs and keeps those until it is done."""
+    whatever wrote the inputs and keeps those until it is done.  The result is ``decode``'s up to
+    rounding, but for magnitudes beyond 65504 and non-finite values: staged in f16, they make the
+    rows that see them NaN and set a status bit (include/mla_decode.h)."""
     import torch
     B, Sq, H, D = q.shape
     assert D == D_QK
