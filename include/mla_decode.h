@@ -11,6 +11,7 @@
  *
  *   n      = causal ? ctx_b - Sq + i + 1 : ctx_b        (clamped to [0, ctx_b])
  *   row_j  = kv_scale * cache[block_table[b][j / page_size]][j % page_size][:]
+ *            (a 4-bit cache: the values that the row stands for)
  *   z_j    = softmax_scale * <q[b,i,h,:], row_j>                  j < n
  *   lse    = ln sum_j exp(z_j)                                     (natural log)
  *   out[d] = sum_j exp(z_j - lse) * row_j[d]                       d < 512
@@ -75,15 +76,42 @@ typedef enum mla_status {
 /* Cache element types. */
 typedef enum mla_kv_dtype {
   MLA_KV_BF16 = 0,     /* bfloat16 latent rows, 1152 bytes each */
-  MLA_KV_FP8_E4M3 = 1  /* OCP fp8 E4M3FN codes, 576 bytes each, times kv_scale */
+  MLA_KV_FP8_E4M3 = 1, /* OCP fp8 E4M3FN codes, 576 bytes each, times kv_scale */
+  MLA_KV_FP4_E2M1 = 4  /* 4-bit latent, f16 rope: rows of MLA_FP4_ROW bytes (below), times kv_scale */
 } mla_kv_dtype;
+
+/*
+ * The row of a 4-bit cache (MLA_KV_FP4_E2M1), 416 bytes:
+ *   bytes 0..255    the 512 latent dims as OCP E2M1 codes, dim 2i in the low
+ *                   half of byte i and dim 2i + 1 in the high half
+ *   bytes 256..287  32 OCP E4M3FN scales, one for 16 dims
+ *   bytes 288..415  the 64 rope dims in f16 (their precision decides which
+ *                   position a key has, and they are an eighth of the row)
+ * Latent dim d is kv_scale * scale[d / 16] * code[d], rope dim r is kv_scale *
+ * rope[r].  A scale with its sign bit set counts with its sign; a NaN scale
+ * makes its 16 dims NaN.  A NaN or infinity in a row spoils every query row of
+ * the sequence, also those whose causal mask hides that key; rows past a
+ * sequence's length are never read.
+ *
+ * The inserts (mla_decode_epilogue, mla_decode_rope_epilogue, mla_decode_step)
+ * write, for a block of 16 values x and with every quotient rounded to fp32,
+ *   q = x / kv_scale,  scale = e4m3(min(max |q| / 6, 448)),  code = e2m1(q / scale)
+ * to nearest even, codes saturating at +-6; a block whose scale rounds to zero
+ * gets zero codes, one that holds a NaN a NaN scale.  A rope dim is f16(x /
+ * kv_scale), saturating at +-65504.
+ *
+ * Taken by mla_decode_plan and mla_decode_dplan_info and what follows them,
+ * mla_decode_fwd_noalloc, mla_decode_step and both epilogues.  The shared-prefix
+ * decode and mla_gather_kv_b_proj answer MLA_ERR_UNSUPPORTED.
+ */
+#define MLA_FP4_ROW 416
 
 /* Bits of the device status word (OR-ed together by the kernels). */
 #define MLA_DEVFLAG_BAD_PAGE 0x1   /* block-table entry outside [0, num_pages) */
 #define MLA_DEVFLAG_CTX_RANGE 0x2  /* seq_lens[b] < 0 or beyond the plan's max_ctx
                                       (clamped to [0, max_ctx] on the device) */
 #define MLA_DEVFLAG_TIMEOUT 0x4    /* a bounded barrier wait gave up         */
-#define MLA_DEVFLAG_Q_RANGE 0x8    /* fp8 or shared-prefix path: |q| beyond the fp16 range */
+#define MLA_DEVFLAG_Q_RANGE 0x8    /* fp8, 4-bit or shared-prefix path: |q| beyond the fp16 range */
 #define MLA_DEVFLAG_KV_RANGE 0x10  /* shared prefix: a cache value beyond the fp16
                                       range, infinite or NaN */
 #define MLA_DEVFLAG_POSITION 0x20  /* rotation: a position outside the table */
@@ -110,7 +138,7 @@ typedef struct mla_decode_plan_t {
   int32_t row_blocks;   /* ceil(rows / row_tile) */
   int32_t max_ctx;      /* longest context the plan covers */
   int32_t key_tile;     /* keys per pipeline tile: 128 when rows <= 64 (bf16) or <= 16
-                           (fp8), the few-row kernel; 64 otherwise */
+                           (fp8, 4 bits), the few-row kernel; 64 otherwise */
   int32_t chunk_len;    /* keys per split, a multiple of key_tile */
   int32_t num_splits;   /* splits per sequence = ceil(max_ctx / chunk_len) */
   int32_t num_sms;      /* SM count the partition was balanced for */
@@ -158,11 +186,12 @@ int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int32_t num_hea
  *
  * plan            host, from mla_decode_plan
  * q               device bf16 [B, Sq, H, 576], contiguous, 16-byte aligned
- * kv_cache        device [num_pages, page_size, 576] bf16 or e4m3 codes,
+ * kv_cache        device [num_pages, page_size, 576] bf16 or e4m3 codes, or
+ *                 [num_pages, page_size, MLA_FP4_ROW] bytes of 4-bit rows,
  *                 contiguous, 16-byte aligned
  * num_pages       pages in kv_cache (block-table entries are checked against it)
- * kv_scale        device fp32[1]: dequant multiplier of the fp8 cache; NULL
- *                 means 1.0; ignored for bf16
+ * kv_scale        device fp32[1]: dequant multiplier of the fp8 or 4-bit
+ *                 cache; NULL means 1.0; ignored for bf16
  * block_table     device int32 [B, bt_stride]; entries past ceil(ctx_b /
  *                 page_size) are never read
  * bt_stride       int32 elements between consecutive sequences' tables
@@ -339,6 +368,7 @@ int mla_gather_kv_b_proj(const void* kv_cache, int64_t num_pages, int32_t page_s
  *   row                  = kv_c[t, :] || k_pe[t, :]                     (576 wide)
  *   cache[slot / page_size][slot % page_size][:] = row                  bf16 cache
  *                                              = e4m3(row / kv_scale)   fp8 cache
+ *                                              = the 4-bit row (above)  4-bit cache
  * with slot = slot_mapping[t]; slot < 0 (a padding token) writes nothing.
  * The fp8 code is round-to-nearest-even of the fp32 quotient (correctly
  * rounded fp32 division), saturating to +-448.  q_pe and k_pe are taken as
@@ -352,8 +382,8 @@ int mla_gather_kv_b_proj(const void* kv_cache, int64_t num_pages, int32_t page_s
  * num_tokens   T >= 0 (0 queues nothing)
  * num_heads    H, 1 .. 128
  * q_out        device bf16 [T, H, 576]: the q of mla_decode_fwd
- * kv_cache     device [num_pages, page_size, 576] bf16 or e4m3 codes
- * kv_dtype     mla_kv_dtype of the cache; kv_scale device fp32[1] (fp8 only)
+ * kv_cache     device [num_pages, page_size, 576] bf16 or e4m3 codes, or 4-bit rows
+ * kv_dtype     mla_kv_dtype of the cache; kv_scale device fp32[1] (fp8 and 4 bits)
  * cache_inputs_early  1: kv_c and k_pe are older than the kernel this call
  *              is queued behind, so they are read before the dependency
  *              wait (as slot_mapping and kv_scale always are); 0: after it
@@ -384,6 +414,7 @@ int mla_decode_epilogue(const void* ql_nope, const void* q_pe, const void* kv_c,
  *   row                  = kv_c[t, :] || rot(k_pe[t, :])
  *   cache[slot / page_size][slot % page_size][:] = row                bf16 cache
  *                                              = e4m3(row / kv_scale) fp8 cache
+ *                                              = the 4-bit row        4-bit cache
  * The rotation is fp32, rounded once to the type it is stored in.  slot < 0 (a
  * padding token) inserts nothing; its query rows are still written.  The slots
  * of one call are distinct (of two tokens with one slot, each 16-byte piece

@@ -29,6 +29,8 @@ LIB_PATH = os.path.join(PKG, "libmla_decode.so")
 
 KV_BF16 = 0
 KV_FP8_E4M3 = 1
+KV_FP4_E2M1 = 4
+FP4_ROW = 416
 D_QK = 576
 D_V = 512
 
@@ -191,6 +193,21 @@ def _is_fp8(cache):
     return cache.dtype in (torch.uint8, torch.float8_e4m3fn)
 
 
+def _kv_dtype(cache) -> int:
+    """What a cache tensor holds: [pages, page, 576] bf16 or codes, or [pages, page, 416] bytes of 4-bit rows."""
+    torch = _torch()
+    if cache.dtype is torch.uint8 and cache.shape[-1] == FP4_ROW:
+        return KV_FP4_E2M1
+    return KV_FP8_E4M3 if _is_fp8(cache) else KV_BF16
+
+
+def _check_fp4(kv_dtype, page_size, cache, where):
+    """A plan for 4-bit rows goes with a cache of them, and no other plan does."""
+    if (kv_dtype == KV_FP4_E2M1) != (_kv_dtype(cache) == KV_FP4_E2M1) or kv_dtype == KV_FP4_E2M1 and not (
+            cache.dim() == 3 and cache.shape[1] == page_size and cache.is_contiguous()):
+        raise MLADecodeError(ERR_INVALID_ARG, where)
+
+
 def _row_stride(table):
     """Elements between the rows of a block table (one row: its length)."""
     if table is None:
@@ -271,6 +288,7 @@ def plan(seq_lens_host, num_heads: int, sq: int, page_size: int, kv_dtype: int =
 def fwd(p: Plan, q, kv_cache, kv_scale, block_table, seq_lens, softmax_scale: float, out, lse,
         workspace, stream=None) -> None:
     """``mla_decode_fwd``.  Tensors are CUDA tensors in the layouts of the C ABI."""
+    _check_fp4(p.kv_dtype, p.page_size, kv_cache, "mla_decode_fwd")
     st = lib().mla_decode_fwd(
         ctypes.byref(p), _ptr(q), _ptr(kv_cache), int(kv_cache.shape[0]), _ptr(kv_scale),
         _ptr(block_table), int(block_table.stride(0)), _ptr(seq_lens), float(softmax_scale),
@@ -312,6 +330,7 @@ def plan_device(d: DPlan, seq_lens, workspace, kv_indptr=None, stream=None) -> N
 def fwd_dplan(d: DPlan, q, kv_cache, kv_scale, block_table, softmax_scale: float, out, lse,
               workspace, kv_indptr=None, stream=None) -> None:
     """``mla_decode_fwd_dplan``; block_table is kv_indices when kv_indptr is given."""
+    _check_fp4(d.kv_dtype, d.page_size, kv_cache, "mla_decode_fwd_dplan")
     stride = int(block_table.stride(0)) if block_table.dim() == 2 else 1
     st = lib().mla_decode_fwd_dplan(
         ctypes.byref(d), _ptr(q), _ptr(kv_cache), int(kv_cache.shape[0]), _ptr(kv_scale),
@@ -353,14 +372,12 @@ def gather_kv_b_proj(kv_cache, kv_scale, block_table, seq_lens, cu_seqlens, max_
 def epilogue(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_cache, kv_scale=None,
              cache_inputs_early: bool = False, status=None, stream=None) -> None:
     """``mla_decode_epilogue``: q_out = ql_nope || q_pe; cache[slot] = kv_c || k_pe
-    (bf16, or e4m3 codes of x / kv_scale for a uint8 / float8 cache)."""
-    import torch
+    (bf16, e4m3 codes of x / kv_scale for a uint8 / float8 cache, or 4-bit rows)."""
     T, H, _ = ql_nope.shape
-    fp8 = kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
     st = lib().mla_decode_epilogue(
         _ptr(ql_nope), _ptr(q_pe), _ptr(kv_c), _ptr(k_pe), _ptr(slot_mapping), int(T), int(H),
         _ptr(q_out), _ptr(kv_cache), int(kv_cache.shape[0]), int(kv_cache.shape[1]),
-        KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale), int(bool(cache_inputs_early)),
+        _kv_dtype(kv_cache), _ptr(kv_scale), int(bool(cache_inputs_early)),
         _ptr(status), _stream(stream))
     _raise(st, "mla_decode_epilogue")
 
@@ -376,7 +393,8 @@ def rope_epilogue(ql_nope, q_pe, kv_c, k_pe, positions, cos_sin, slot_mapping, q
         raise MLADecodeError(ERR_INVALID_ARG, "mla_decode_rope_epilogue")
     T, H, _ = ql_nope.shape
     ql_s, qp_s, kc_s, kp_s = ql_nope.stride(), q_pe.stride(), kv_c.stride(), k_pe.stride()
-    fp8 = kv_cache.dtype is not bf
+    coded = kv_cache.dtype is not bf
+    dtype = _kv_dtype(kv_cache) if coded else KV_BF16
     # What the C ABI reads, and nothing else: types, shapes, rows or all of a tensor contiguous,
     # the current device.
     if not (ql_nope.dtype is q_pe.dtype is kv_c.dtype is k_pe.dtype is q_out.dtype is bf
@@ -384,14 +402,14 @@ def rope_epilogue(ql_nope, q_pe, kv_c, k_pe, positions, cos_sin, slot_mapping, q
             and ql_nope.shape[2] == D_V and q_pe.shape == (T, H, 64) and kv_c.shape == (T, D_V)
             and k_pe.shape == (T, 64) and positions.shape == slot_mapping.shape == (T,)
             and cos_sin.dim() == 2 and cos_sin.shape[1] == 64 and q_out.shape == (T, H, D_QK)
-            and kv_cache.dim() == 3 and kv_cache.shape[2] == D_QK
+            and kv_cache.dim() == 3 and kv_cache.shape[2] == (FP4_ROW if dtype == KV_FP4_E2M1 else D_QK)
             and ql_s[2] == qp_s[2] == kc_s[1] == kp_s[1] == 1
             and positions.is_contiguous() and slot_mapping.is_contiguous()
             and cos_sin.is_contiguous() and q_out.is_contiguous() and kv_cache.is_contiguous()
             and 0 <= dev == q_pe.get_device() == kv_c.get_device()
             == k_pe.get_device() == positions.get_device() == slot_mapping.get_device()
             == cos_sin.get_device() == q_out.get_device() == kv_cache.get_device()
-            and (not fp8 or _is_fp8(kv_cache) and kv_scale is not None
+            and (not coded or _is_fp8(kv_cache) and kv_scale is not None
                  and kv_scale.dtype is torch.float32 and kv_scale.numel() == 1
                  and kv_scale.get_device() == dev)
             and (status is None or status.dtype is torch.int32 and status.numel() == 1
@@ -402,7 +420,7 @@ def rope_epilogue(ql_nope, q_pe, kv_c, k_pe, positions, cos_sin, slot_mapping, q
         kv_c.data_ptr(), kc_s[0], k_pe.data_ptr(), kp_s[0],
         positions.data_ptr(), cos_sin.data_ptr(), cos_sin.shape[0], 1 if interleaved else 0,
         slot_mapping.data_ptr(), T, H, q_out.data_ptr(), kv_cache.data_ptr(), kv_cache.shape[0],
-        kv_cache.shape[1], KV_FP8_E4M3 if fp8 else KV_BF16, kv_scale.data_ptr() if fp8 else None,
+        kv_cache.shape[1], dtype, kv_scale.data_ptr() if coded else None,
         1 if inputs_early else 0, None if status is None else status.data_ptr(),
         _raw_stream(stream, dev))
     _raise(st, "mla_decode_rope_epilogue")
@@ -412,6 +430,7 @@ def step(p: Plan, ql_nope, q_pe, kv_c, k_pe, slot_mapping, q, kv_cache, kv_scale
          seq_lens, softmax_scale: float, out, lse, workspace, cache_inputs_early: bool = False,
          stream=None) -> None:
     """``mla_decode_step``: epilogue, fwd and combine chained by programmatic launches."""
+    _check_fp4(p.kv_dtype, p.page_size, kv_cache, "mla_decode_step")
     st = lib().mla_decode_step(
         ctypes.byref(p), _ptr(ql_nope), _ptr(q_pe), _ptr(kv_c), _ptr(k_pe), _ptr(slot_mapping),
         int(bool(cache_inputs_early)), _ptr(q), _ptr(kv_cache), int(kv_cache.shape[0]),
@@ -534,7 +553,7 @@ def decode(q, kv_cache, block_table, seq_lens, seq_lens_host=None, kv_scale=None
     import torch
     B, Sq, H, D = q.shape
     assert D == D_QK
-    kv_dtype = KV_FP8_E4M3 if kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn) else KV_BF16
+    kv_dtype = _kv_dtype(kv_cache)
     if softmax_scale is None:
         softmax_scale = 1.0 / math.sqrt(192.0)
     with _on(stream, q.device):

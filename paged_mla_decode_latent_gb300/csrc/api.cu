@@ -9,6 +9,7 @@
 
 #include "../../include/mla_decode.h"
 #include "internal.h"
+#include "kv.h"
 
 int mla_launch_fwd_sm103(const mla::FwdParams& p, void* stream);
 int mla_launch_fwd_pipe_sm103(const mla::FwdParams& p, void* stream);
@@ -25,8 +26,7 @@ int check_plan(const mla_decode_plan_t* plan) {
     return MLA_ERR_INVALID_ARG;
   if (plan->num_splits < 1 || plan->chunk_len < 1 || plan->num_splits > mla::kMaxSplits)
     return MLA_ERR_INVALID_ARG;
-  if (plan->kv_dtype != MLA_KV_BF16 && plan->kv_dtype != MLA_KV_FP8_E4M3)
-    return MLA_ERR_INVALID_ARG;
+  if (!mla::kv_dtype_known(plan->kv_dtype)) return MLA_ERR_INVALID_ARG;
   if (plan->wait_limit_us < 0) return MLA_ERR_INVALID_ARG;
   if (plan->key_tile != mla::kKeyTile && plan->key_tile != mla::kKeyTileSmall)
     return MLA_ERR_INVALID_ARG;
@@ -69,7 +69,7 @@ int fwd_impl(const mla_decode_plan_t* plan, const void* q, const void* kv_cache,
   p.q = static_cast<const uint16_t*>(q);
   p.cache = kv_cache;
   p.num_pages = num_pages;
-  p.kv_scale = plan->kv_dtype == MLA_KV_FP8_E4M3 ? kv_scale : nullptr;
+  p.kv_scale = plan->kv_dtype != MLA_KV_BF16 ? kv_scale : nullptr;
   p.bt = block_table;
   p.bt_stride = bt_stride;
   p.seq_lens = seq_lens;
@@ -131,7 +131,7 @@ extern "C" int mla_decode_step(const mla_decode_plan_t* plan, const void* ql_nop
   if (st != MLA_OK) return st;
   st = check_workspace(plan, workspace, workspace_bytes);
   if (st != MLA_OK) return st;
-  if (plan->kv_dtype == MLA_KV_FP8_E4M3 && kv_scale == nullptr) return MLA_ERR_INVALID_ARG;
+  if (plan->kv_dtype != MLA_KV_BF16 && kv_scale == nullptr) return MLA_ERR_INVALID_ARG;
   int32_t* status =
       reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + plan->ws_status_offset);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -205,7 +205,7 @@ cudaError_t opt_in_smem(const void* kernel, int bytes, int dev, int slot) {
 }  // namespace mla
 
 // Few-row blocks go to the 128-key-tile kernel; 128-row blocks with a bf16
-// cache to the four-stage kernel (fp8 needs room for raw stages it lacks).
+// cache to the four-stage kernel (fp8 and 4 bits need room for raw stages it lacks).
 int mla_launch_fwd(const mla::FwdParams& p, void* stream) {
   if (p.key_tile == mla::kKeyTileSmall) return mla_launch_fwd_small_sm103(p, stream);
   if (p.kv_dtype == MLA_KV_BF16) return mla_launch_fwd_pipe_sm103(p, stream);

@@ -62,8 +62,9 @@ __global__ void __launch_bounds__(128) combine_kernel(mla::CombineParams p) {
   __syncthreads();
   if (threadIdx.x == 0) {
     float tot = red[0] + red[1] + red[2] + red[3];
-    L_s = (m == -INFINITY) ? -INFINITY : m + logf(tot);
-    red[0] = (m == -INFINITY) ? 0.f : 1.f / tot;
+    // tot == 0 only where every split is empty (m == -inf); a NaN stays one
+    L_s = (tot == 0.f) ? -INFINITY : m + logf(tot);
+    red[0] = (tot == 0.f) ? 0.f : 1.f / tot;
   }
   __syncthreads();
   const float inv = red[0];

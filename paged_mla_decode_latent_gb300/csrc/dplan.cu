@@ -38,6 +38,7 @@
 
 #include "../../include/mla_decode.h"
 #include "internal.h"
+#include "kv.h"
 
 namespace {
 
@@ -197,7 +198,7 @@ extern "C" int mla_decode_dplan_info(int32_t batch, int32_t num_heads, int32_t s
   if (num_heads < 1 || num_heads > 128 || sq < 1 || sq > 16 || num_heads * sq > mla::kMaxRows)
     return MLA_ERR_INVALID_ARG;
   if (page_size < 1 || page_size > 4096 || ctx_capacity < 0) return MLA_ERR_INVALID_ARG;
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (!mla::kv_dtype_known(kv_dtype)) return MLA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return MLA_ERR_INVALID_ARG;
   if (num_sms <= 0) {
     int dev = 0;
@@ -310,7 +311,7 @@ extern "C" int mla_decode_fwd_dplan(const mla_decode_dplan_t* dplan, const void*
   p.q = static_cast<const uint16_t*>(q);
   p.cache = kv_cache;
   p.num_pages = num_pages;
-  p.kv_scale = dplan->kv_dtype == MLA_KV_FP8_E4M3 ? kv_scale : nullptr;
+  p.kv_scale = dplan->kv_dtype != MLA_KV_BF16 ? kv_scale : nullptr;
   p.bt = block_table;
   p.bt_stride = bt_stride;
   p.bt_indptr = kv_indptr;

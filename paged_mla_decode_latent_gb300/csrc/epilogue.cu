@@ -26,7 +26,9 @@
 #include <cstdint>
 
 #include "../../include/mla_decode.h"
+#include "fp4.cuh"
 #include "internal.h"
+#include "kv.h"
 
 namespace {
 
@@ -40,11 +42,11 @@ struct EpiParams {
   const uint16_t* k_pe;     // bf16 [T, 64]
   const int64_t* slot_mapping;  // [T]; < 0 = no insert
   uint16_t* q_out;          // bf16 [T, H, 576]
-  void* cache;              // [num_pages, page_size, 576] bf16 or e4m3
-  const float* kv_scale;    // fp8 only
+  void* cache;              // [num_pages, page_size, 576] bf16 or e4m3, or 4-bit rows
+  const float* kv_scale;    // fp8 and 4 bits
   int32_t* status;          // optional
   int64_t num_slots;        // num_pages * page_size
-  int tokens, heads, fp8, cache_early;
+  int tokens, heads, dtype, cache_early;
 };
 
 // Two fp32 -> two e4m3 codes (round to nearest even, saturating to +-448;
@@ -96,12 +98,22 @@ __global__ void __launch_bounds__(kThreads) epilogue_kernel(EpiParams p) {
     if (piece == 0 && p.status) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
     return;
   }
-  if (!p.fp8) {
+  if (p.dtype == MLA_KV_BF16) {
     reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.cache) + slot * MLA_D_QK)[piece] = v;
     return;
   }
   const float s = *p.kv_scale;
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if (p.dtype == MLA_KV_FP4_E2M1) {  // the row's pieces 2k and 2k + 1 are with neighbouring lanes
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      x[2 * k] = __uint_as_float(w[k] << 16);
+      x[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+    }
+    fp4::store_piece(static_cast<uint8_t*>(p.cache) + slot * fp4::kRow, piece, x, s);
+    return;
+  }
   uint32_t codes[2];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
@@ -131,16 +143,16 @@ extern "C" int mla_decode_epilogue(const void* ql_nope, const void* q_pe, const 
                                    int32_t cache_inputs_early, int32_t* status, void* stream) {
   if (num_tokens < 0 || num_heads < 1 || num_heads > 128 || page_size < 1 || num_pages < 1)
     return MLA_ERR_INVALID_ARG;
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (!mla::kv_dtype_known(kv_dtype)) return MLA_ERR_INVALID_ARG;
   if (cache_inputs_early != 0 && cache_inputs_early != 1) return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (!ql_nope || !q_pe || !kv_c || !k_pe || !slot_mapping || !q_out || !kv_cache)
     return MLA_ERR_INVALID_ARG;
-  if (kv_dtype == MLA_KV_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
+  if (kv_dtype != MLA_KV_BF16 && !kv_scale) return MLA_ERR_INVALID_ARG;
   if (!aligned16(ql_nope) || !aligned16(q_pe) || !aligned16(kv_c) || !aligned16(k_pe) ||
       !aligned16(q_out) || !aligned16(kv_cache) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7))
     return MLA_ERR_INVALID_ARG;
-  if (kv_dtype == MLA_KV_FP8_E4M3 && (reinterpret_cast<uintptr_t>(kv_scale) & 3))
+  if (kv_dtype != MLA_KV_BF16 && (reinterpret_cast<uintptr_t>(kv_scale) & 3))
     return MLA_ERR_INVALID_ARG;
   EpiParams p;
   p.ql_nope = static_cast<const uint16_t*>(ql_nope);
@@ -155,7 +167,7 @@ extern "C" int mla_decode_epilogue(const void* ql_nope, const void* q_pe, const 
   p.num_slots = num_pages * (int64_t)page_size;
   p.tokens = num_tokens;
   p.heads = num_heads;
-  p.fp8 = kv_dtype == MLA_KV_FP8_E4M3;
+  p.dtype = kv_dtype;
   p.cache_early = cache_inputs_early;
   const int64_t threads = (int64_t)num_tokens * (num_heads + 1) * kPieces;
   cudaLaunchConfig_t cfg = {};

@@ -58,6 +58,7 @@
 #include <cstdint>
 
 #include "../../include/mla_decode.h"
+#include "fp4.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -68,7 +69,7 @@ constexpr int ATOM = T * 128;          // one 64-dim slab of a 16-bit stage: 64 
 constexpr int ATOM8 = T * 64;          // the same slab of raw fp8 codes: 64 keys x 64 B
 constexpr int SLOTS = 5;               // slabs per stage: 4 value + 1 rope (half of it used)
 constexpr int STAGE = SLOTS * ATOM;    // 40 KB of 16-bit operands (36 KB of it filled)
-constexpr int RAW_STAGE = SLOTS * ATOM8;  // 20 KB of fp8 codes
+constexpr int RAW_STAGE8 = SLOTS * ATOM8;  // 20 KB of fp8 codes
 constexpr int QROPE = 128 * 128;       // rope dims of Q, 128 rows x 128 B
 // Exchange with the partner CTA: each softmax warp sends and receives the
 // partial scores of its 16 rows x 64 keys per tile (1024 scores), each
@@ -90,10 +91,11 @@ constexpr int kThreads = 32 * 12;
 // raw stage of codes its loader warp copies into and converts from.  (A
 // fourth bf16 stage needs a 13th warp, which cuts the registers to 128 a
 // thread; measured, the 12-warp kernel with 3 stages is faster.)
-template <bool kFp8>
+template <int kDtype>
 struct Layout {
   static constexpr int NS = 3;              // operand stages = loader warps
-  static constexpr int NR = kFp8 ? 3 : 0;   // raw fp8 stages (one per loader warp)
+  static constexpr int NR = kDtype != MLA_KV_BF16 ? 3 : 0;  // raw stages of codes (one per loader warp)
+  static constexpr int RAW_STAGE = kDtype == MLA_KV_FP4_E2M1 ? T * fp4::kRawRow : RAW_STAGE8;
   static constexpr int OFF_STAGE = 0;
   static constexpr int OFF_RAW = OFF_STAGE + NS * STAGE;
   static constexpr int OFF_QROPE = OFF_RAW + NR * RAW_STAGE;
@@ -101,8 +103,9 @@ struct Layout {
   static constexpr int OFF_BAR = OFF_RECV + XCHG;
   static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;  // + barriers + alignment slack
 };
-static_assert(Layout<false>::SMEM_BYTES <= 232448, "bf16 smem");
-static_assert(Layout<true>::SMEM_BYTES <= 232448, "fp8 smem");
+static_assert(Layout<MLA_KV_BF16>::SMEM_BYTES <= 232448, "bf16 smem");
+static_assert(Layout<MLA_KV_FP8_E4M3>::SMEM_BYTES <= 232448, "fp8 smem");
+static_assert(Layout<MLA_KV_FP4_E2M1>::SMEM_BYTES <= 232448, "4-bit smem");
 
 // TMEM columns
 constexpr uint32_t TM_O = 0;     // 256 fp32 columns: this CTA's value half
@@ -206,7 +209,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
 
 // fp32 bits + half a unit of the 24-bit value: the top three bytes are the
 // value rounded to 16 significant bits (half away from zero on the magnitude).
-__device__ __forceinline__ uint32_t round_up_bits(float x) { return __float_as_uint(x) + 0x80u; }
+template <bool kNaN = false>
+__device__ __forceinline__ uint32_t round_up_bits(float x) {
+  // The MMA's NaN, 0x7FFFFFFF, would carry into the sign and leave a zero.
+  if (kNaN) return (uint32_t)min((int)__float_as_uint(x), 0x7FFFFF7F) + 0x80u;
+  return __float_as_uint(x) + 0x80u;
+}
 
 // Four values -> three words (the upper three bytes of each).
 __device__ __forceinline__ void pack24(uint32_t A, uint32_t B, uint32_t C, uint32_t D, uint32_t* w) {
@@ -260,14 +268,17 @@ __device__ __forceinline__ uint64_t vmajor_desc(uint32_t addr) {
   return ptx::smem_desc(addr, ATOM, 1024, 2);
 }
 
-template <bool kFp8>
+template <int kDtype>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fwd_sm103_kernel(mla::FwdParams p) {
-  using L = Layout<kFp8>;
+  using L = Layout<kDtype>;
+  constexpr bool kFp8 = kDtype == MLA_KV_FP8_E4M3, kFp4 = kDtype == MLA_KV_FP4_E2M1;
+  constexpr bool kF16 = kFp8 || kFp4;  // codes that the loaders convert to f16 operands
+  constexpr int RAW_STAGE = L::RAW_STAGE;
   constexpr int NS = L::NS;
   constexpr int OFF_STAGE = L::OFF_STAGE, OFF_RAW = L::OFF_RAW, OFF_QROPE = L::OFF_QROPE;
   constexpr int OFF_RECV = L::OFF_RECV, OFF_BAR = L::OFF_BAR;
-  constexpr uint32_t kAB = kFp8 ? 0u : 1u;  // operand type: f16 (fp8 cache) or bf16
+  constexpr uint32_t kAB = kF16 ? 0u : 1u;  // operand type: f16 (fp8 and 4-bit caches) or bf16
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -320,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   const int n_tiles = k1 > k0 ? (k1 - k0 + T - 1) / T : 0;
   const int vdim0 = (int)rank * 256;  // this CTA's value dims
-  const float s_kv = (p.kv_dtype == MLA_KV_FP8_E4M3 && p.kv_scale) ? *p.kv_scale : 1.f;
+  const float s_kv = (kF16 && p.kv_scale) ? *p.kv_scale : 1.f;
 
   if (n_tiles == 0) {
     // No key of this split: the row results are out = 0, lse = -inf.  Both
@@ -407,7 +418,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint64_t v0 = dv + s * kStageU;
         for (int kk = 0; kk < T / 16; ++kk)
           ptx::mma_ts(tmem + TM_O, pa + kk * 8, v0 + kk * (2048 >> 4), id_pv, (t | kk) != 0);
-        if (!kFp8 && second) {  // second-order weights (see the softmax)
+        if (!kF16 && second) {  // second-order weights (see the softmax)
           for (int kk = 0; kk < T / 16; ++kk)
             ptx::mma_ts(tmem + TM_O, pa + 32 + kk * 8, v0 + kk * (2048 >> 4), id_pv, 1);
         }
@@ -485,9 +496,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // and arrives on the stage's full barrier, while the other loader warps
     // have their tiles in flight.  Block-table entries for the warp's next
     // tile are read before it waits.
-    constexpr int LPI = kFp8 ? 4 : 8;        // lanes per piece
+    // 4 bits: a lane looks up and converts keys lane and lane + 32 of the tile;
+    // the copies go 128 bytes of codes (8 lanes), 64 of rope (4) and 16 of
+    // scales (1) a key.
+    constexpr int LPI = kFp4 ? 1 : kFp8 ? 4 : 8;  // lanes per piece
     constexpr int IPI = 32 / LPI;            // pieces per warp instruction
-    constexpr int NK = T / IPI;              // keys per lane: 16 (bf16) or 8 (fp8)
+    constexpr int NK = T / IPI;              // keys per lane: 16 (bf16), 8 (fp8) or 2 (4 bits)
     const int lw = warp;  // the operand stage this warp owns
     const int g = lane / LPI, sub = lane % LPI;
     constexpr int n_slots = SLOTS;
@@ -525,6 +539,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int t = lw; t < n_tiles; t += NS) {
       const int s = lw;
       const char* row[NK];
+      uint32_t rix[NK];  // 4 bits: the cache row's index (num_pages * page_size < 2^31)
       bool bad = false;
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
@@ -535,15 +550,36 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const uint32_t key = (uint32_t)key_of(t, i);
         const int64_t r = page * p.page_size + (int64_t)(key - page_of(key) * pdiv);
-        row[i] = cache + r * (kFp8 ? mla::kDQK : mla::kDQK * 2);
+        row[i] = cache + r * (kFp4 ? fp4::kRow : kFp8 ? mla::kDQK : mla::kDQK * 2);
+        rix[i] = (uint32_t)r;
       }
       if (bad) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
       load_pages(t + NS);
-      if constexpr (!kFp8) {
+      if constexpr (!kF16) {
         if (t >= NS && !wait_all(c, ptx::smem_u32(&bars.kv_empty[s]), ((t / NS) - 1) & 1))
           break;
       }
-      const uint32_t dst = sbase + (kFp8 ? OFF_RAW + lw * RAW_STAGE : OFF_STAGE + s * STAGE);
+      const uint32_t dst = sbase + (kF16 ? OFF_RAW + lw * RAW_STAGE : OFF_STAGE + s * STAGE);
+      if constexpr (kFp4) {
+        __syncwarp();  // every lane has converted the codes that these replace
+#pragma unroll
+        for (int i = 0; i < T / 4; ++i) {
+          const int kk = 4 * i + (lane >> 3), ch = lane & 7;
+          const char* src = cache + (size_t)__shfl_sync(0xffffffffu, rix[i / 8], kk & 31) * fp4::kRow;
+          ptx::cp_async_16(dst + kk * fp4::kRawRow + ch * 16, src + 128 * (int)rank + ch * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < T / 8; ++i) {
+          const int kk = 8 * i + (lane >> 2), ch = lane & 3;
+          const char* src = cache + (size_t)__shfl_sync(0xffffffffu, rix[i / 4], kk & 31) * fp4::kRow;
+          ptx::cp_async_16(dst + kk * fp4::kRawRow + fp4::kRawRope + ch * 16,
+                           src + fp4::kRope + 64 * (int)rank + ch * 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+          ptx::cp_async_16(dst + (32 * i + lane) * fp4::kRawRow + fp4::kRawScales,
+                           row[i] + fp4::kScales + 16 * (int)rank);
+      } else
       for (int sl = 0; sl < n_slots; ++sl) {
         if (sl == 4 && !rope_lane) continue;
         const int dim = sl < 4 ? vdim0 + sl * 64 : 512;
@@ -585,6 +621,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             st_shared_u4(rowp + (((2 * sub) ^ (kk & 7)) * 16), lo);
             st_shared_u4(rowp + (((2 * sub + 1) ^ (kk & 7)) * 16), hi);
           }
+        }
+      }
+      if constexpr (kFp4) {
+        __syncwarp();  // the other lanes' copies
+        if (t >= NS && !wait_all(c, ptx::smem_u32(&bars.kv_empty[s]), ((t / NS) - 1) & 1))
+          break;
+        const uint32_t out = sbase + OFF_STAGE + s * STAGE;
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+          const int kk = 32 * i + lane;
+          const uint32_t raw = dst + kk * fp4::kRawRow, rowp = out + kk * 128;
+          const uint4 scales = ld_shared_u4(raw + fp4::kRawScales);
+          const uint32_t sc[4] = {scales.x, scales.y, scales.z, scales.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            uint4 v[4];
+            fp4::convert(ld_shared_u4(raw + j * 16), sc[j >> 1] >> (16 * (j & 1)), v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              st_shared_u4(rowp + (j >> 1) * ATOM + (((4 * (j & 1) + e) ^ (kk & 7)) * 16), v[e]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            st_shared_u4(rowp + 4 * ATOM + (((4 * (int)rank + e) ^ (kk & 7)) * 16),
+                         ld_shared_u4(raw + fp4::kRawRope + e * 16));
         }
       }
       ptx::fence_proxy_async_smem();
@@ -633,7 +694,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           uint4 x = valid_row ? qv[(vdim0 + chunk * 64) / 8 + v] : make_uint4(0, 0, 0, 0);
-          if (kFp8) x = bf16x8_to_f16x8(x, q_range);
+          if (kF16) x = bf16x8_to_f16x8(x, q_range);
           buf[v * 4 + 0] = x.x;
           buf[v * 4 + 1] = x.y;
           buf[v * 4 + 2] = x.z;
@@ -646,12 +707,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           uint4 x = valid_row ? qv[512 / 8 + v] : make_uint4(0, 0, 0, 0);
-          if (kFp8) x = bf16x8_to_f16x8(x, q_range);
+          if (kF16) x = bf16x8_to_f16x8(x, q_range);
           *reinterpret_cast<uint4*>(qr + ((v ^ (r & 7)) * 16)) = x;
         }
         ptx::fence_proxy_async_smem();
       }
-      if (kFp8 && q_range) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
+      if (kF16 && q_range) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       ptx::mbar_arrive(ptx::smem_u32(&bars.q_ready));
@@ -675,7 +736,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int buf = t & 1;
       if (!wait_all(c, ptx::smem_u32(&bars.s_full[buf]), (t >> 1) & 1)) { ok = false; break; }
       if (!live) {
-        if (!kFp8 && lane == 0) reinterpret_cast<volatile uint8_t*>(&bars.heavy[buf])[sw] = 0;
+        if (!kF16 && lane == 0) reinterpret_cast<volatile uint8_t*>(&bars.heavy[buf])[sw] = 0;
         ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
         continue;
       }
@@ -704,8 +765,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t w[12];
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // rounded to 24 bits: the top 3 bytes of x + 0x80
-            pack24(round_up_bits(s[16 * qd + 4 * k]), round_up_bits(s[16 * qd + 4 * k + 1]),
-                   round_up_bits(s[16 * qd + 4 * k + 2]), round_up_bits(s[16 * qd + 4 * k + 3]),
+            pack24(round_up_bits<kFp4>(s[16 * qd + 4 * k]), round_up_bits<kFp4>(s[16 * qd + 4 * k + 1]),
+                   round_up_bits<kFp4>(s[16 * qd + 4 * k + 2]), round_up_bits<kFp4>(s[16 * qd + 4 * k + 3]),
                    w + 3 * k);
 #pragma unroll
           for (int v = 0; v < 3; ++v)
@@ -839,9 +900,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          pk[2 * j] = kFp8 ? pack_f16(s[4 * j], s[4 * j + 1]) : pack_bf16(s[4 * j], s[4 * j + 1]);
+          pk[2 * j] = kF16 ? pack_f16(s[4 * j], s[4 * j + 1]) : pack_bf16(s[4 * j], s[4 * j + 1]);
           pk[2 * j + 1] =
-              kFp8 ? pack_f16(s[4 * j + 2], s[4 * j + 3]) : pack_bf16(s[4 * j + 2], s[4 * j + 3]);
+              kF16 ? pack_f16(s[4 * j + 2], s[4 * j + 3]) : pack_bf16(s[4 * j + 2], s[4 * j + 3]);
         }
         lA += sA;
         lB += sB;
@@ -850,7 +911,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // holds pairs 4j + i%4, which is where the 16x128b shape writes.
       const uint32_t pcol = tmem + lanes16 + TM_S + buf * T;
       ptx::tmem_st16x128b_x8(pcol, pk);
-      if constexpr (!kFp8) {
+      if constexpr (!kF16) {
         // bf16 keeps 8 significant bits.  Where one key carries a sizeable
         // share of a row's weight (more than 1/16 of the row sum so far), the
         // rounding would show in O, so the warp's rows also get a second bf16
@@ -898,7 +959,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // parity wait on o_done only tells the current phase from the one
       // before it, and o_done may be one phase short or already complete).
       ptx::tc_fence_after();
-      const float invA = lA > 0.f ? s_kv / lA : 0.f, invB = lB > 0.f ? s_kv / lB : 0.f;
+      // 4 bits: a sum that is NaN is no empty row
+      const bool someA = kFp4 ? !(lA <= 0.f) : lA > 0.f, someB = kFp4 ? !(lB <= 0.f) : lB > 0.f;
+      const float invA = someA ? s_kv / lA : 0.f, invB = someB ? s_kv / lB : 0.f;
       const int rowA = rb * mla::kRowTile + rA, rowB = rb * mla::kRowTile + rB;
       const bool okA = rowA < p.rows, okB = rowB < p.rows;
       const size_t pA = part * p.rows + rowA;
@@ -923,8 +986,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (rank == 0 && cq == 0) {
-        const float lseA = lA > 0.f ? (mA + log2f(lA)) * 0.6931471805599453f : -INFINITY;
-        const float lseB = lB > 0.f ? (mB + log2f(lB)) * 0.6931471805599453f : -INFINITY;
+        const float lseA = someA ? (mA + log2f(lA)) * 0.6931471805599453f : -INFINITY;
+        const float lseB = someB ? (mB + log2f(lB)) * 0.6931471805599453f : -INFINITY;
         if (single) {
           if (okA) p.lse[(size_t)b * p.rows + rowA] = lseA;
           if (okB) p.lse[(size_t)b * p.rows + rowB] = lseB;
@@ -957,13 +1020,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }  // namespace
 
 int mla_launch_fwd_sm103(const mla::FwdParams& p, void* stream) {
-  const bool fp8 = p.kv_dtype == MLA_KV_FP8_E4M3;
-  auto kernel = fp8 ? fwd_sm103_kernel<true> : fwd_sm103_kernel<false>;
-  const int smem = fp8 ? Layout<true>::SMEM_BYTES : Layout<false>::SMEM_BYTES;
+  auto kernel = fwd_sm103_kernel<MLA_KV_BF16>;
+  int smem = Layout<MLA_KV_BF16>::SMEM_BYTES, slot = 0;
+  if (p.kv_dtype == MLA_KV_FP8_E4M3) {
+    kernel = fwd_sm103_kernel<MLA_KV_FP8_E4M3>;
+    smem = Layout<MLA_KV_FP8_E4M3>::SMEM_BYTES;
+    slot = 1;
+  } else if (p.kv_dtype == MLA_KV_FP4_E2M1) {
+    kernel = fwd_sm103_kernel<MLA_KV_FP4_E2M1>;
+    smem = Layout<MLA_KV_FP4_E2M1>::SMEM_BYTES;
+    slot = 11;
+  }
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
-  e = mla::opt_in_smem(reinterpret_cast<const void*>(kernel), smem, dev, fp8 ? 1 : 0);
+  e = mla::opt_in_smem(reinterpret_cast<const void*>(kernel), smem, dev, slot);
   if (e != cudaSuccess) return (int)e;
   // Splits vary slowest, so every sequence's first chunk is dispatched
   // before any second chunk (the planner simulates this order).  Launched as

@@ -464,6 +464,7 @@ extern "C" int mla_gather_kv_b_proj(const void* kv_cache, int64_t num_pages, int
   if (batch < 1 || batch > 65535 || num_heads < 1 || num_heads > 128 || page_size < 1 ||
       page_size > 4096 || num_pages < 1 || bt_stride < 1 || max_ctx < 0)
     return MLA_ERR_INVALID_ARG;
+  if (kv_dtype == MLA_KV_FP4_E2M1) return MLA_ERR_UNSUPPORTED;
   if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
   if (kv_dtype == MLA_KV_FP8_E4M3 && !kv_scale) return MLA_ERR_INVALID_ARG;
   if (bt_stride * (int64_t)page_size < (int64_t)max_ctx) return MLA_ERR_INVALID_ARG;

@@ -26,6 +26,7 @@
 
 #include "../../include/mla_decode.h"
 #include "internal.h"
+#include "kv.h"
 
 namespace {
 
@@ -72,7 +73,7 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
   if (num_heads < 1 || num_heads > 128 || sq < 1 || sq > 16) return MLA_ERR_INVALID_ARG;
   if (num_heads * sq > mla::kMaxRows) return MLA_ERR_INVALID_ARG;
   if (page_size < 1 || page_size > 4096) return MLA_ERR_INVALID_ARG;
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (!mla::kv_dtype_known(kv_dtype)) return MLA_ERR_INVALID_ARG;
   if (causal != 0 && causal != 1) return MLA_ERR_INVALID_ARG;
   int32_t max_ctx = 0;
   for (int b = 0; b < batch; ++b) {

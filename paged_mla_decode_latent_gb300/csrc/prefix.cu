@@ -591,6 +591,7 @@ extern "C" int mla_decode_prefix_plan(const int32_t* seq_lens_host, int32_t batc
   if (plan == nullptr || seq_lens_host == nullptr) return MLA_ERR_INVALID_ARG;
   if (batch < 1 || batch > 65535 || prefix_len < 0 || prefix_len > MLA_PREFIX_MAX_LEN)
     return MLA_ERR_INVALID_ARG;
+  if (kv_dtype == MLA_KV_FP4_E2M1) return MLA_ERR_UNSUPPORTED;
   try {
     std::vector<int32_t> own(batch);
     int32_t max_ctx = 0;

@@ -20,7 +20,9 @@
 #include <cstdint>
 
 #include "../../include/mla_decode.h"
+#include "fp4.cuh"
 #include "internal.h"
+#include "kv.h"
 #include "ptx.cuh"
 
 namespace {
@@ -120,6 +122,9 @@ __device__ __forceinline__ uint2 codes(const float (&x)[8], float s, float inv, 
   return make_uint2(lo[0] | lo[1] << 16, lo[2] | lo[3] << 16);
 }
 
+// The 4-bit insert has a form of its own, so that its registers are not the
+// others'.
+template <bool kFp4>
 __global__ void __launch_bounds__(kThreads, 4) rope_epilogue_kernel(RopeParams p) {
   const int sub = (int)(threadIdx.x & 7);
   const uint32_t row = blockIdx.x * kRows + (threadIdx.x >> 3);
@@ -161,7 +166,24 @@ __global__ void __launch_bounds__(kThreads, 4) rope_epilogue_kernel(RopeParams p
       if (sub == 0 && p.status) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
       return;
     }
-    if (p.fp8) {
+    if constexpr (kFp4) {  // pieces 2k and 2k + 1 are with neighbouring lanes
+      const float s = *p.kv_scale;
+      uint8_t* dst = static_cast<uint8_t*>(p.cache) + slot * fp4::kRow;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          x[2 * k] = lo_f(w[k]);
+          x[2 * k + 1] = hi_f(w[k]);
+        }
+        fp4::store_piece(dst, sub + 8 * i, x, s);
+      }
+      fp4::store_piece(dst, 64 + sub, o, s);
+      return;
+    }
+    if (!kFp4 && p.fp8) {
       const float s = *p.kv_scale;
       const bool near = fabsf(s) >= 0x1p-100f && fabsf(s) <= 0x1p100f;
       const float inv = near ? __frcp_rn(s) : NAN;
@@ -216,12 +238,12 @@ extern "C" int mla_decode_rope_epilogue(
   if (num_tokens < 0 || num_heads < 1 || num_heads > 128 || page_size < 1 || num_pages < 1 ||
       max_positions < 1)
     return MLA_ERR_INVALID_ARG;
-  if (kv_dtype != MLA_KV_BF16 && kv_dtype != MLA_KV_FP8_E4M3) return MLA_ERR_INVALID_ARG;
+  if (!mla::kv_dtype_known(kv_dtype)) return MLA_ERR_INVALID_ARG;
   if (interleaved < 0 || interleaved > 1 || inputs_early < 0 || inputs_early > 1)
     return MLA_ERR_INVALID_ARG;
   if (num_tokens == 0) return MLA_OK;
   if (!ql_nope || !q_pe || !kv_c || !k_pe || !positions || !cos_sin || !slot_mapping || !q_out ||
-      !kv_cache || (kv_dtype == MLA_KV_FP8_E4M3 && !kv_scale))
+      !kv_cache || (kv_dtype != MLA_KV_BF16 && !kv_scale))
     return MLA_ERR_INVALID_ARG;
   if (misaligned(ql_nope, 16) || misaligned(q_pe, 16) || misaligned(kv_c, 16) ||
       misaligned(k_pe, 16) || misaligned(cos_sin, 16) || misaligned(q_out, 16) ||
@@ -262,6 +284,7 @@ extern "C" int mla_decode_rope_epilogue(
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, rope_epilogue_kernel, p) != cudaSuccess) return MLA_ERR_CUDA;
+  auto kernel = kv_dtype == MLA_KV_FP4_E2M1 ? rope_epilogue_kernel<true> : rope_epilogue_kernel<false>;
+  if (cudaLaunchKernelEx(&cfg, kernel, p) != cudaSuccess) return MLA_ERR_CUDA;
   return MLA_OK;
 }
