@@ -115,6 +115,10 @@ typedef enum mla_kv_dtype {
 #define MLA_DEVFLAG_KV_RANGE 0x10  /* shared prefix: a cache value beyond the fp16
                                       range, infinite or NaN */
 #define MLA_DEVFLAG_POSITION 0x20  /* rotation: a position outside the table */
+#define MLA_DEVFLAG_NO_PAGES 0x40  /* pages: fewer are free than were asked for */
+#define MLA_DEVFLAG_BAD_ROW 0x80   /* pages: a parent outside the table */
+#define MLA_DEVFLAG_REFS 0x100     /* pages: a count below zero, or a free page in a table */
+#define MLA_DEVFLAG_SHARED 0x200   /* pages: a row grows in a page that others hold too */
 
 #define MLA_DECODE_PLAN_VERSION 1
 #define MLA_D_QK 576 /* query/key row width: 512 latent + 64 rope */
@@ -608,6 +612,101 @@ int mla_decode_prefix_fwd(const mla_decode_prefix_plan_t* plan, const void* q,
 /* mla_decode_check for the last prefix call that used `workspace`. */
 int mla_decode_prefix_check(const mla_decode_prefix_plan_t* plan, const void* workspace,
                             void* stream, int32_t* host_status);
+
+/*
+ * The pages of a cache, kept on the GPU.  A book of pages is
+ *
+ *   refs         device int32 [num_pages], 16-byte aligned: how many rows hold
+ *                page p; 0: it is free.  A caller that keeps a page beyond any row
+ *                (a prompt's) counts itself in.
+ *   block_table  device int32 [rows, bt_stride]: the first ceil(len / page_size)
+ *                entries of a row are its pages, the others are not read;
+ *                `width` <= bt_stride entries are there to be used
+ *   seq_lens     device int32 [rows], tokens
+ *
+ * and what mla_decode_fwd reads.  The calls below change it without the host
+ * knowing a length, so that they can be captured together with the decode.  Free
+ * pages are handed out lowest first: the result is a matter of the arguments
+ * alone.  rows <= 65535, num_pages < 2^31 - 1, page_size 1 .. 4096.
+ *
+ * status  optional device int32 word (NULL = none), cleared by the caller.  Nothing
+ *         faults: a page id outside [0, num_pages) counts nothing and is not
+ *         copied (MLA_DEVFLAG_BAD_PAGE), a length outside [0, width * page_size] is
+ *         clamped (MLA_DEVFLAG_CTX_RANGE), a book that does not add up sets
+ *         MLA_DEVFLAG_REFS.
+ * workspace  device, 256-byte aligned, >= mla_pages_workspace_bytes(num_pages,
+ *         rows) (fork: the larger of both row counts); it holds nothing between
+ *         calls; calls that may overlap need one each.
+ *
+ * Return MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (a cache past 2^62
+ * bytes), MLA_ERR_WORKSPACE or MLA_ERR_CUDA.
+ */
+
+/* Bytes of workspace, or -1 for sizes out of range. */
+int64_t mla_pages_workspace_bytes(int64_t num_pages, int32_t rows);
+
+/*
+ * mla_pages_resize -- every row gets the length new_lens[b] (0 frees it): first
+ * all rows give back the pages past their new length, then rows in order are
+ * given the free pages that they need.  A row that cannot have all of them, and
+ * every later row that needs any, keeps its old length (MLA_DEVFLAG_NO_PAGES).
+ * seq_lens holds the lengths that came of it.  A row that grows in its last,
+ * partly filled page must be the only one that holds it (MLA_DEVFLAG_SHARED tells;
+ * mla_pages_fork sees to it, and a row cut back into a shared page does not grow
+ * again without one).
+ *
+ * new_lens  device int32 [rows], not seq_lens itself
+ * slots     optional device int64 [rows, tokens] (tokens >= 0, 0: none): the cache
+ *           slots of each row's last `tokens` tokens, as slot_mapping of
+ *           mla_decode_epilogue; -1 for a token that this call did not add
+ */
+int mla_pages_resize(int32_t* refs, int64_t num_pages, int32_t* block_table, int64_t bt_stride,
+                     int32_t width, int32_t* seq_lens, const int32_t* new_lens, int32_t rows,
+                     int32_t page_size, int64_t* slots, int32_t tokens, int32_t* status,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * mla_pages_fork -- a new table whose row i goes on from row parents[i] of the
+ * old one (-1: an empty row; other values outside [0, rows) count as -1 and set
+ * MLA_DEVFLAG_BAD_ROW).  Beams, samples from one prompt, a batch put in another
+ * order; rows that nobody goes on from are freed.  Children share their parent's
+ * whole pages.  A partly filled last page stays with the lowest-numbered child;
+ * each further child, in order, gets the lowest free page and a copy of its filled
+ * slots in every layer (the other slots are left as they were).  A child that
+ * finds no free page keeps the whole pages only, and its length is cut to them
+ * (MLA_DEVFLAG_NO_PAGES).  The old table and lengths are left as they were; they
+ * no longer count.
+ *
+ * parents    device int32 [out_rows]
+ * table_out  device int32 [out_rows, out_stride], out_stride >= width; lens_out
+ *            device int32 [out_rows]; neither overlaps what it is made from.
+ *            Entries past a row's pages may be written too.
+ * kv_cache   device, 16-byte aligned: `layers` caches, layer_stride bytes apart, of
+ *            num_pages * page_size rows of row_bytes bytes (1152 bf16, 576 fp8,
+ *            MLA_FP4_ROW; any multiple of 16 up to 2^20)
+ */
+int mla_pages_fork(int32_t* refs, int64_t num_pages, const int32_t* block_table, int64_t bt_stride,
+                   int32_t width, const int32_t* seq_lens, int32_t rows, const int32_t* parents,
+                   int32_t* table_out, int64_t out_stride, int32_t* lens_out, int32_t out_rows,
+                   int32_t page_size, void* kv_cache, int32_t layers, int64_t layer_stride,
+                   int64_t row_bytes, int32_t* status, void* workspace, size_t workspace_bytes,
+                   void* stream);
+
+/*
+ * mla_pages_compact -- with n pages held, moves the k-th held page from n on into
+ * the k-th free page below n, in every layer: then pages [0, n) are held and the
+ * rest is free.  refs and the table (rows may be 0) follow.
+ *
+ * page_map  device int32 [num_pages]: a page's new number, -1 for one that was
+ *           free; for tables other than this one
+ * n_live    device int32 [1]: n
+ * kv_cache, layers, layer_stride, row_bytes  as mla_pages_fork
+ */
+int mla_pages_compact(int32_t* refs, int64_t num_pages, int32_t* block_table, int64_t bt_stride,
+                      int32_t width, const int32_t* seq_lens, int32_t rows, int32_t page_size,
+                      void* kv_cache, int32_t layers, int64_t layer_stride, int64_t row_bytes,
+                      int32_t* page_map, int32_t* n_live, int32_t* status, void* workspace,
+                      size_t workspace_bytes, void* stream);
 
 /* Static text for a status code. */
 const char* mla_status_string(int status);

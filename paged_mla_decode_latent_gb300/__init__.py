@@ -13,7 +13,8 @@ Names follow the C ABI: ``plan`` -> ``mla_decode_plan``, ``fwd`` ->
 ``mla_decode_step``; the device-planned path: ``dplan_info``, ``plan_device``,
 ``fwd_dplan`` and ``combine_dplan``; ``gather_kv_b_proj`` ->
 ``mla_gather_kv_b_proj``; for a batch that shares a prefix: ``prefix_plan``,
-``prefix_fwd`` and ``prefix_check`` -> ``mla_decode_prefix_*``.  ``decode`` is
+``prefix_fwd`` and ``prefix_check`` -> ``mla_decode_prefix_*``; for the pages of a
+cache: ``pages_resize``, ``pages_fork`` and ``pages_compact`` -> ``mla_pages_*``.  ``decode`` is
 plan + fwd + combine, and ``decode_prefix`` prefix_plan + prefix_fwd, with
 freshly allocated outputs and workspace, for convenience.
 """
@@ -48,6 +49,10 @@ DEVFLAG_TIMEOUT = 0x4
 DEVFLAG_Q_RANGE = 0x8
 DEVFLAG_KV_RANGE = 0x10
 DEVFLAG_POSITION = 0x20
+DEVFLAG_NO_PAGES = 0x40
+DEVFLAG_BAD_ROW = 0x80
+DEVFLAG_REFS = 0x100
+DEVFLAG_SHARED = 0x200
 
 # Every symbol include/mla_decode.h declares.
 EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_fwd", "mla_decode_combine",
@@ -55,6 +60,7 @@ EXPORTED_SYMBOLS = ("mla_decode_plan", "mla_decode_fwd", "mla_decode_combine",
                     "mla_decode_fwd_dplan", "mla_decode_combine_dplan", "mla_decode_epilogue",
                     "mla_decode_rope_epilogue", "mla_decode_step", "mla_gather_kv_b_proj", "mla_decode_fwd_noalloc",
                     "mla_decode_prefix_plan", "mla_decode_prefix_fwd", "mla_decode_prefix_check",
+                    "mla_pages_workspace_bytes", "mla_pages_resize", "mla_pages_fork", "mla_pages_compact",
                     "mla_status_string", "mla_decode_version")
 
 
@@ -165,6 +171,16 @@ def lib():
     L.mla_decode_prefix_fwd.restype = ctypes.c_int
     L.mla_decode_prefix_check.argtypes = [X, vp, vp, ctypes.POINTER(i32)]
     L.mla_decode_prefix_check.restype = ctypes.c_int
+    L.mla_pages_workspace_bytes.argtypes = [i64, i32]
+    L.mla_pages_workspace_bytes.restype = i64
+    L.mla_pages_resize.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, i32, vp, i32, vp, vp, ctypes.c_size_t, vp]
+    L.mla_pages_resize.restype = ctypes.c_int
+    L.mla_pages_fork.argtypes = [vp, i64, vp, i64, i32, vp, i32, vp, vp, i64, vp, i32, i32, vp, i32, i64, i64, vp, vp,
+                                 ctypes.c_size_t, vp]
+    L.mla_pages_fork.restype = ctypes.c_int
+    L.mla_pages_compact.argtypes = [vp, i64, vp, i64, i32, vp, i32, i32, vp, i32, i64, i64, vp, vp, vp, vp,
+                                    ctypes.c_size_t, vp]
+    L.mla_pages_compact.restype = ctypes.c_int
     L.mla_decode_check.argtypes = [P, vp, vp, ctypes.POINTER(i32)]
     L.mla_decode_check.restype = ctypes.c_int
     L.mla_status_string.argtypes = [ctypes.c_int]
@@ -537,6 +553,106 @@ def decode_prefix(q, kv_cache, prefix_table, block_table, seq_lens, prefix_len: 
         prefix_fwd(p, q, kv_cache, kv_scale, prefix_table, block_table, seq_lens, softmax_scale, out,
                    lse, workspace, stream)
     return _results(stream, out, lse)
+
+
+def pages_workspace(num_pages: int, rows: int, device="cuda"):
+    """A workspace for the ``pages_*`` calls on that many pages and table rows."""
+    import torch
+    n = lib().mla_pages_workspace_bytes(int(num_pages), int(rows))
+    if n < 0:
+        raise MLADecodeError(ERR_INVALID_ARG, "mla_pages_workspace_bytes")
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _int32_on(dev, *tensors) -> bool:
+    """Whether these are contiguous int32 tensors of device `dev`."""
+    i32 = _torch().int32
+    return all(t.dtype is i32 and t.get_device() == dev and t.is_contiguous() for t in tensors)
+
+
+def _table_on(dev, table) -> bool:
+    return (table.dtype is _torch().int32 and table.dim() == 2 and table.get_device() == dev
+            and table.shape[1] > 0 and table.stride(1) == 1
+            and (table.shape[0] < 2 or table.stride(0) >= table.shape[1]))
+
+
+def _layers(kv_cache, pages: int, dev):
+    """(page size, layers, bytes between layers, bytes of a row) of a cache [pages, page, row] or [layers, pages,
+    page, row]; None if it is neither."""
+    shape, stride, size = kv_cache.shape, kv_cache.stride(), kv_cache.element_size()
+    if (kv_cache.dim() not in (3, 4) or shape[-3] != pages or min(shape) < 1 or kv_cache.get_device() != dev
+            or stride[-1] != 1 or stride[-2] != shape[-1] or stride[-3] != shape[-1] * shape[-2]):
+        return None
+    layers = shape[0] if kv_cache.dim() == 4 else 1
+    return shape[-2], layers, stride[0] * size if layers > 1 else 0, shape[-1] * size
+
+
+def _status_on(dev, status) -> bool:
+    return status is None or (status.dtype is _torch().int32 and status.numel() == 1 and status.get_device() == dev)
+
+
+def pages_resize(refs, block_table, seq_lens, new_lens, page_size: int, workspace, slots=None, status=None,
+                 stream=None) -> None:
+    """``mla_pages_resize``: rows of the table get the lengths new_lens (0: freed); refs, block_table and seq_lens
+    are changed in place.  slots int64 [rows, tokens]: where each row's last tokens go, -1 for those not added."""
+    torch = _torch()
+    dev, rows = _device(refs), block_table.shape[0]
+    if not (dev >= 0 and refs.dim() == 1 and _int32_on(dev, refs, seq_lens, new_lens) and _table_on(dev, block_table)
+            and seq_lens.shape == new_lens.shape == (rows,) and workspace.is_contiguous()
+            and workspace.get_device() == dev and _status_on(dev, status)
+            and (slots is None or slots.dtype is torch.int64 and slots.dim() == 2 and slots.shape[0] == rows
+                 and slots.is_contiguous() and slots.get_device() == dev)):
+        raise MLADecodeError(ERR_INVALID_ARG, "mla_pages_resize")
+    tokens = 0 if slots is None else slots.shape[1]
+    st = lib().mla_pages_resize(
+        refs.data_ptr(), refs.shape[0], block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
+        seq_lens.data_ptr(), new_lens.data_ptr(), rows, int(page_size), slots.data_ptr() if tokens else None, tokens,
+        None if status is None else status.data_ptr(), workspace.data_ptr(), _ws_bytes(workspace),
+        _raw_stream(stream, dev))
+    _raise(st, "mla_pages_resize")
+
+
+def pages_fork(refs, block_table, seq_lens, parents, table_out, lens_out, kv_cache, workspace, status=None,
+               stream=None) -> None:
+    """``mla_pages_fork``: row i of table_out and lens_out goes on from row parents[i] (-1: empty) of block_table and
+    seq_lens; refs is changed in place.  kv_cache: [pages, page, row], or [layers, pages, page, row]."""
+    dev, rows, out_rows = _device(refs), block_table.shape[0], table_out.shape[0]
+    cache = _layers(kv_cache, refs.shape[0], dev) if dev >= 0 and refs.dim() == 1 else None
+    if not (cache is not None and _int32_on(dev, refs, seq_lens, parents, lens_out) and _table_on(dev, block_table)
+            and _table_on(dev, table_out) and seq_lens.shape == (rows,)
+            and parents.shape == lens_out.shape == (out_rows,) and table_out.shape[1] >= block_table.shape[1]
+            and workspace.is_contiguous() and workspace.get_device() == dev and _status_on(dev, status)):
+        raise MLADecodeError(ERR_INVALID_ARG, "mla_pages_fork")
+    page_size, layers, layer_stride, row_bytes = cache
+    st = lib().mla_pages_fork(
+        refs.data_ptr(), refs.shape[0], block_table.data_ptr(), _row_stride(block_table), block_table.shape[1],
+        seq_lens.data_ptr(), rows, parents.data_ptr(), table_out.data_ptr(), _row_stride(table_out),
+        lens_out.data_ptr(), out_rows, page_size, kv_cache.data_ptr(), layers, layer_stride, row_bytes,
+        None if status is None else status.data_ptr(), workspace.data_ptr(), _ws_bytes(workspace),
+        _raw_stream(stream, dev))
+    _raise(st, "mla_pages_fork")
+
+
+def pages_compact(refs, block_table, seq_lens, kv_cache, page_map, n_live, workspace, status=None, stream=None) -> None:
+    """``mla_pages_compact``: held pages move to the front of the cache (as ``pages_fork`` takes it); refs and
+    block_table (None: no table) follow, page_map int32 [pages] and n_live int32 [1] say where they went."""
+    dev = _device(refs)
+    cache = _layers(kv_cache, refs.shape[0], dev) if dev >= 0 and refs.dim() == 1 else None
+    rows = 0 if block_table is None else block_table.shape[0]
+    if not (cache is not None and _int32_on(dev, refs, page_map, n_live) and page_map.shape == refs.shape
+            and n_live.numel() == 1 and workspace.is_contiguous() and workspace.get_device() == dev
+            and _status_on(dev, status)
+            and (rows == 0 or _table_on(dev, block_table) and seq_lens is not None and _int32_on(dev, seq_lens)
+                 and seq_lens.shape == (rows,))):
+        raise MLADecodeError(ERR_INVALID_ARG, "mla_pages_compact")
+    page_size, layers, layer_stride, row_bytes = cache
+    st = lib().mla_pages_compact(
+        refs.data_ptr(), refs.shape[0], block_table.data_ptr() if rows else None,
+        _row_stride(block_table) if rows else 0, block_table.shape[1] if rows else 0,
+        seq_lens.data_ptr() if rows else None, rows, page_size, kv_cache.data_ptr(), layers, layer_stride, row_bytes,
+        page_map.data_ptr(), n_live.data_ptr(), None if status is None else status.data_ptr(), workspace.data_ptr(),
+        _ws_bytes(workspace), _raw_stream(stream, dev))
+    _raise(st, "mla_pages_compact")
 
 
 def workspace_for(p, device="cuda"):
