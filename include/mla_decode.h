@@ -141,8 +141,8 @@ typedef struct mla_decode_plan_t {
   int32_t row_tile;     /* rows one CTA pair handles (128) */
   int32_t row_blocks;   /* ceil(rows / row_tile) */
   int32_t max_ctx;      /* longest context the plan covers */
-  int32_t key_tile;     /* keys per pipeline tile: 128 when rows <= 64 (bf16) or <= 16
-                           (fp8, 4 bits), the few-row kernel; 64 otherwise */
+  int32_t key_tile;     /* keys per pipeline tile: 128 when rows <= 64 (bf16), <= 16 (fp8)
+                           or <= 32 (4 bits), the few-row kernels; 64 otherwise */
   int32_t chunk_len;    /* keys per split, a multiple of key_tile */
   int32_t num_splits;   /* splits per sequence = ceil(max_ctx / chunk_len) */
   int32_t num_sms;      /* SM count the partition was balanced for */

@@ -389,10 +389,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMA ---
-    if (lane == 0) {
+    // 4 bits: the whole warp walks the loop and one lane of it issues.  (In a branch
+    // that one lane takes alone an MMA costs about 64 cycles to issue, here what
+    // the tensor cores need: N = 64 from TMEM 32, N = 256 128.  Batch 64 x 128
+    // heads x 8192: 230 -> 215 us.)
+    const bool leader = kFp4 ? ptx::elect_one() : true;
+    auto all = [](bool x) { return kFp4 ? __all_sync(0xffffffffu, x) != 0 : x; };
+    if (kFp4 || lane == 0) {
       const uint32_t id_qk = ptx::idesc_f16(128, T, kAB, false, false);
       const uint32_t id_pv = ptx::idesc_f16(128, 256, kAB, false, true);
-      bool ok = wait(c, ptx::smem_u32(&bars.q_ready), 0);
+      bool ok = all(wait(c, ptx::smem_u32(&bars.q_ready), 0));
       ptx::tc_fence_after();
       // Operand descriptors from bases: the start address is the low field in
       // 16-byte units, so a stage, a slab or a 16-key step of V is an add (no
@@ -404,18 +410,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto issue_qk = [&](int u, int s) {  // tile u from stage s (u % NS)
         const uint32_t d = tmem + TM_S + (u & 1) * T;
         const uint64_t k0 = dk + s * kStageU;
+        if (!leader) return;
+#pragma unroll
         for (int a = 0; a < 4; ++a)
+#pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::mma_ts(d, tmem + TM_Q + a * 32 + kk * 8, k0 + a * kAtomU + 2 * kk, id_qk,
                         (a | kk) != 0);
         // this CTA's 32 rope dims: 16-dim steps 2 rank, 2 rank + 1 of the rope slab
-        for (int kk = 2 * (int)rank; kk < 2 * (int)rank + 2; ++kk)
-          ptx::mma_ss(d, dqr + 2 * kk, k0 + 4 * kAtomU + 2 * kk, id_qk, 1);
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+          ptx::mma_ss(d, dqr + 4 * rank + 2 * kk, k0 + 4 * kAtomU + 4 * rank + 2 * kk, id_qk, 1);
         ptx::mma_commit(ptx::smem_u32(&bars.s_full[u & 1]));
       };
       auto issue_pv = [&](int t, int s, bool second) {  // tile t from stage s (t % NS)
         const uint32_t pa = tmem + TM_S + (t & 1) * T;
         const uint64_t v0 = dv + s * kStageU;
+        if (!leader) return;
+#pragma unroll
         for (int kk = 0; kk < T / 16; ++kk)
           ptx::mma_ts(tmem + TM_O, pa + kk * 8, v0 + kk * (2048 >> 4), id_pv, (t | kk) != 0);
         if (!kF16 && second) {  // second-order weights (see the softmax)
@@ -439,7 +451,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       while (ok && np < n_tiles) {
         bool progress = false;
         if (nq < n_tiles && nq <= np + 1 &&
-            ptx::mbar_test_wait(ptx::smem_u32(&bars.kv_full[sq]), phq)) {
+            all(ptx::mbar_test_wait(ptx::smem_u32(&bars.kv_full[sq]), phq))) {
           ptx::tc_fence_after();
           issue_qk(nq++, sq);
           if (sq == NS - 1) {
@@ -450,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           progress = true;
         }
-        if (np < nq && ptx::mbar_test_wait(ptx::smem_u32(&bars.p_full[np & 1]), (np >> 1) & 1)) {
+        if (np < nq && all(ptx::mbar_test_wait(ptx::smem_u32(&bars.p_full[np & 1]), (np >> 1) & 1))) {
           ptx::tc_fence_after();
           const bool second = *reinterpret_cast<volatile uint64_t*>(&bars.heavy[np & 1]) != 0;
           issue_pv(np++, sp, second);
@@ -477,6 +489,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             *c.abort = 1;
             ok = false;
           }
+          ok = all(ok);
         }
       }
       (void)ok;
@@ -1005,7 +1018,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     if (bars.abort) {
       // wait for every tcgen05 op this CTA issued before giving TMEM back
-      if (lane == 0) {
+      if (kFp4 ? ptx::elect_one() : lane == 0) {
         ptx::mma_commit(ptx::smem_u32(&bars.drain));
         wait_drain(ptx::smem_u32(&bars.drain), 0);
       }
@@ -1029,7 +1042,7 @@ int mla_launch_fwd_sm103(const mla::FwdParams& p, void* stream) {
   } else if (p.kv_dtype == MLA_KV_FP4_E2M1) {
     kernel = fwd_sm103_kernel<MLA_KV_FP4_E2M1>;
     smem = Layout<MLA_KV_FP4_E2M1>::SMEM_BYTES;
-    slot = 11;
+    slot = 12;
   }
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -57,8 +57,8 @@
 #include <cstdint>
 
 #include "../../include/mla_decode.h"
-#include "fp4.cuh"
 #include "internal.h"
+#include "kv.h"
 #include "ptx.cuh"
 
 namespace {
@@ -68,14 +68,13 @@ constexpr int ATOM = T * 128;           // one 64-dim latent slab of a stage: 16
 constexpr int RATOM = T * 64;           // the CTA's rope half, 64-byte rows: 8 KB
 constexpr int STAGE = 4 * ATOM + RATOM; // 72 KB
 constexpr int NS = 2;                   // operand stages (one tile each)
-template <int kDtype>
+template <bool kFp8>
 struct LoadPart {
-  static constexpr int keys = kDtype == MLA_KV_BF16 ? 64 : 32;  // keys of one loader part
-  // codes of a 32-key part: 9 KB of fp8, 6.5 KB of 4 bits
-  static constexpr int raw = kDtype == MLA_KV_FP4_E2M1 ? 32 * fp4::kRawRow : 32 * (256 + 32);
+  static constexpr int keys = kFp8 ? 32 : 64;  // keys of one loader part
 };
+constexpr int RAW_PART = 32 * (256 + 32);      // fp8 codes of a 32-key part: 9 KB
 // Raw slots: two for each loader warp but the first, which owns a tile's
-// first part (the first the value MMAs release) and has one (4 bits: two).
+// first part (the first the value MMAs release) and has one.
 constexpr int NR = 7;
 // Rows and warps: a warp reaches only the TMEM lane quarter warp % 4, and
 // each quarter belongs to one SM sub-partition.  So that all four
@@ -111,10 +110,8 @@ __device__ __forceinline__ int loader_index(int w) { return kWide ? w - 8 : (w =
 __device__ __forceinline__ int mma_row(int r) { return 32 * (r >> 4) + (r & 15); }
 constexpr int RECV_W = 32 * 16 * 6;     // one warp's partial scores: 16 rows x 64 keys x 3 B (3 KB)
 
-template <int kDtype>
+template <bool kFp8>
 struct Layout {
-  static constexpr bool kF16 = kDtype != MLA_KV_BF16;  // codes that the loaders convert to f16 operands
-  static constexpr int slots = kDtype == MLA_KV_FP4_E2M1 ? 8 : NR;
   // Q as the A operand (128 MMA rows, K-major; the MMA reads all 128 rows of
   // a slab, 16 KB, and the unused ones may hold anything).  bf16 (up to 64
   // rows, at MMA rows 32 q + i): the real rows of a latent slab are its
@@ -124,15 +121,15 @@ struct Layout {
   // to 16 rows, MMA rows 0..15): slabs of 16 rows packed 2 KB apart, their
   // unused rows reading into the stages, then the rope rows (1 KB).
   __host__ __device__ static constexpr int qslab_off(int a) {
-    return kF16 ? a * 2048 : (a >> 1) * 16384 + (a & 1) * 2048;
+    return kFp8 ? a * 2048 : (a >> 1) * 16384 + (a & 1) * 2048;
   }
-  __host__ __device__ static constexpr int qrope_off() { return kF16 ? 4 * 2048 : 2 * 16384; }
-  __host__ __device__ static constexpr int qbytes() { return kF16 ? 4 * 2048 + 1024 : 2 * 16384 + 8192; }
-  static constexpr int max_rows = kF16 ? 16 : 64;
+  __host__ __device__ static constexpr int qrope_off() { return kFp8 ? 4 * 2048 : 2 * 16384; }
+  __host__ __device__ static constexpr int qbytes() { return kFp8 ? 4 * 2048 + 1024 : 2 * 16384 + 8192; }
+  static constexpr int max_rows = kFp8 ? 16 : 64;
   static constexpr int OFF_Q = 0;
   static constexpr int OFF_STAGE = (qbytes() + 1023) / 1024 * 1024;  // 40 KB bf16, 9 KB fp8
   static constexpr int OFF_RAW = OFF_STAGE + NS * STAGE;
-  static constexpr int OFF_RECV = OFF_RAW + (kF16 ? slots * LoadPart<kDtype>::raw : 0);
+  static constexpr int OFF_RECV = OFF_RAW + (kFp8 ? NR * RAW_PART : 0);
   static constexpr int RECV = (max_rows / 16) * 2 * RECV_W;  // two softmax warps a quarter
   static constexpr int OFF_XFREE = OFF_RECV + RECV;
   // the key-split exchange: [quarter][3 slots][2 warps][32 lanes] x 16 B
@@ -140,10 +137,9 @@ struct Layout {
   static constexpr int OFF_BAR = OFF_XMAX + (max_rows / 16) * 3 * 2 * 32 * 16;
   static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;
 };
-static_assert(Layout<MLA_KV_BF16>::SMEM_BYTES <= 232448, "bf16 smem");
-static_assert(Layout<MLA_KV_FP8_E4M3>::SMEM_BYTES <= 232448, "fp8 smem");
-static_assert(Layout<MLA_KV_FP4_E2M1>::SMEM_BYTES <= 232448, "4-bit smem");
-static_assert(Layout<MLA_KV_BF16>::OFF_STAGE % 1024 == 0 && Layout<MLA_KV_FP8_E4M3>::OFF_STAGE % 1024 == 0 &&
+static_assert(Layout<false>::SMEM_BYTES <= 232448, "bf16 smem");
+static_assert(Layout<true>::SMEM_BYTES <= 232448, "fp8 smem");
+static_assert(Layout<false>::OFF_STAGE % 1024 == 0 && Layout<true>::OFF_STAGE % 1024 == 0 &&
                   STAGE % 1024 == 0 && RATOM % 512 == 0,
               "swizzle atoms stay aligned");
 
@@ -230,12 +226,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
   return r;
 }
 
-template <bool kNaN = false>
-__device__ __forceinline__ uint32_t round_up_bits(float x) {
-  // The MMA's NaN, 0x7FFFFFFF, would carry into the sign and leave a zero.
-  if (kNaN) return (uint32_t)min((int)__float_as_uint(x), 0x7FFFFF7F) + 0x80u;
-  return __float_as_uint(x) + 0x80u;
-}
+__device__ __forceinline__ uint32_t round_up_bits(float x) { return __float_as_uint(x) + 0x80u; }
 
 __device__ __forceinline__ void pack24(uint32_t A, uint32_t B, uint32_t C, uint32_t D, uint32_t* w) {
   w[0] = __byte_perm(A, B, 0x5321);
@@ -289,15 +280,12 @@ __device__ __forceinline__ uint64_t vdesc(uint32_t addr) { return ptx::smem_desc
 __device__ __forceinline__ uint32_t sw128(int r, int c) { return r * 128 + ((c ^ (r & 7)) * 16); }
 __device__ __forceinline__ uint32_t sw64(int r, int c) { return r * 64 + ((c ^ ((r >> 1) & 3)) * 16); }
 
-template <int kDtype, bool kWide>
+template <bool kFp8, bool kWide>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count * 32, 1)
     fwd_small_kernel(mla::FwdParams p) {
-  using L = Layout<kDtype>;
-  constexpr bool kFp8 = kDtype == MLA_KV_FP8_E4M3, kFp4 = kDtype == MLA_KV_FP4_E2M1;
-  constexpr bool kF16 = L::kF16;
-  constexpr int RAW_PART = LoadPart<kDtype>::raw;
-  constexpr uint32_t kAB = kF16 ? 0u : 1u;
-  constexpr int PART = LoadPart<kDtype>::keys;
+  using L = Layout<kFp8>;
+  constexpr uint32_t kAB = kFp8 ? 0u : 1u;
+  constexpr int PART = LoadPart<kFp8>::keys;
   constexpr int UPT = T / PART;  // loader parts per tile
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -339,7 +327,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
   }
   const int n_tiles = k1 > k0 ? (k1 - k0 + T - 1) / T : 0;
   const int vdim0 = (int)rank * 256;
-  const float s_kv = (kF16 && p.kv_scale) ? *p.kv_scale : 1.f;
+  const float s_kv = (p.kv_dtype == MLA_KV_FP8_E4M3 && p.kv_scale) ? *p.kv_scale : 1.f;
 
   if (n_tiles == 0) {
     ptx::grid_dependency_wait();
@@ -415,7 +403,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
         const int s = t % NS;
         const uint32_t pa = tmem + TM_S + (t & 1) * T;
         const uint32_t st = sbase + L::OFF_STAGE + s * STAGE;
-        const bool two = !kF16 && heavy != 0;
+        const bool two = !kFp8 && heavy != 0;
         constexpr int MPP = PART / 16;  // value MMAs (16 keys each) per loader part
         for (int kk = 0; kk < T / 16; ++kk) {
           ptx::mma_ts(tmem + TM_O, pa + kk * 8, vdesc(st + kk * 2048), id_pv, (t | kk) != 0);
@@ -485,11 +473,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
     // f16 by the same lanes; the copy of the warp's next part is issued before
     // the current one waits for its stage and converts, so a part is always in
     // flight.
-    // 4 bits: a lane looks up and converts one key of the part; the copies go
-    // 128 bytes of codes (8 lanes), 64 of rope (4) and 16 of scales (1) a key.
-    constexpr int LPI = kFp4 ? 1 : kFp8 ? 4 : 8;  // lanes per 128-byte latent piece
+    constexpr int LPI = kFp8 ? 4 : 8;  // lanes per 128-byte latent piece
     constexpr int IPI = 32 / LPI;      // keys per warp instruction
-    constexpr int NK = PART / IPI;     // keys per lane and part: 16 (bf16), 4 (fp8) or 1 (4 bits)
+    constexpr int NK = PART / IPI;     // keys per lane and part: 16 (bf16) or 4 (fp8)
     const int g = lane / LPI, sub = lane % LPI;
     const int32_t* bt =
         p.bt + (p.bt_indptr ? (size_t)p.bt_indptr[b] : (size_t)b * p.bt_stride);
@@ -532,9 +518,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
       }
       if (bad) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
     };
-    auto row = [&](int i) { return cache + (size_t)rix[i] * (kFp4 ? fp4::kRow : kFp8 ? mla::kDQK : mla::kDQK * 2); };
+    auto row = [&](int i) { return cache + (size_t)rix[i] * (kFp8 ? mla::kDQK : mla::kDQK * 2); };
     load_pages(lw);
-    if constexpr (!kF16) {
+    if constexpr (!kFp8) {
       for (int u = lw; u < n_units; u += kLoaders) {
         const int t = u / UPT, h = u % UPT, s = t % NS;
         rows_of(u);
@@ -556,34 +542,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
         ptx::mbar_arrive(ptx::smem_u32(&bars.kv_full[s]));
       }
     } else {
-      // raw slot j of this warp: [PART keys][288 codes], or [PART keys][208
-      // bytes] of 4 bits; loader 0 has one of the former
-      const int nslot = !kFp4 && lw == 0 ? 1 : 2;
-      auto raw_slot = [&](int j) {
-        return sbase + L::OFF_RAW + (kFp4 ? 2 * lw + j : lw == 0 ? 0 : 2 * lw - 1 + j) * RAW_PART;
-      };
+      // raw slot j of this warp: [PART keys][288 codes]; loader 0 has one
+      const int nslot = lw == 0 ? 1 : 2;
+      auto raw_slot = [&](int j) { return sbase + L::OFF_RAW + (lw == 0 ? 0 : 2 * lw - 1 + j) * RAW_PART; };
       auto issue_raw = [&](int u, int j) {
         rows_of(u);
         const uint32_t raw = raw_slot(j);
-        if constexpr (kFp4) {
-          __syncwarp();  // every lane has converted the codes that these replace
-#pragma unroll
-          for (int i = 0; i < PART / 4; ++i) {
-            const int kr = 4 * i + (lane >> 3), ch = lane & 7;
-            const char* src = cache + (size_t)__shfl_sync(0xffffffffu, rix[0], kr) * fp4::kRow;
-            ptx::cp_async_16(raw + kr * fp4::kRawRow + ch * 16, src + 128 * (int)rank + ch * 16);
-          }
-#pragma unroll
-          for (int i = 0; i < PART / 8; ++i) {
-            const int kr = 8 * i + (lane >> 2), ch = lane & 3;
-            const char* src = cache + (size_t)__shfl_sync(0xffffffffu, rix[0], kr) * fp4::kRow;
-            ptx::cp_async_16(raw + kr * fp4::kRawRow + fp4::kRawRope + ch * 16,
-                             src + fp4::kRope + 64 * (int)rank + ch * 16);
-          }
-          ptx::cp_async_16(raw + lane * fp4::kRawRow + fp4::kRawScales,
-                           row(0) + fp4::kScales + 16 * (int)rank);
-          return;
-        }
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
           const int kr = i * IPI + g;  // key within the part
@@ -613,24 +577,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
         // copied.
         const uint32_t stage = sbase + L::OFF_STAGE + s * STAGE;
         const uint32_t raw = raw_slot(j);
-        if constexpr (kFp4) {
-          __syncwarp();  // the other lanes' copies
-          const int kk = h * PART + lane;
-          const uint32_t rawk = raw + lane * fp4::kRawRow;
-          const uint4 scales = ld_shared_u4(rawk + fp4::kRawScales);
-          const uint32_t sc[4] = {scales.x, scales.y, scales.z, scales.w};
-#pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            uint4 v[4];
-            fp4::convert(ld_shared_u4(rawk + q * 16), sc[q >> 1] >> (16 * (q & 1)), v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              st_shared_u4(stage + (q >> 1) * ATOM + sw128(kk, 4 * (q & 1) + e), v[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            st_shared_u4(stage + 4 * ATOM + sw64(kk, e), ld_shared_u4(rawk + fp4::kRawRope + e * 16));
-        } else
 #pragma unroll
         for (int i = 0; i < NK; ++i) {
           const int kr = i * IPI + g, kk = h * PART + kr;
@@ -735,17 +681,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
 #pragma unroll
       for (int k = 0; k < kQPieces; ++k)
         if (i0 + k * step < n_pieces) {
-          if (kF16) xs[k] = bf16x8_to_f16x8(xs[k], q_range);
+          if (kFp8) xs[k] = bf16x8_to_f16x8(xs[k], q_range);
           st_shared_u4(dsts[k], xs[k]);
         }
       for (int i = i0 + kQPieces * step; i < n_pieces; i += step) {  // beyond the forms' limits
         uint4 x;
         uint32_t dst;
         piece(i, x, dst);
-        if (kF16) x = bf16x8_to_f16x8(x, q_range);
+        if (kFp8) x = bf16x8_to_f16x8(x, q_range);
         st_shared_u4(dst, x);
       }
-      if (kF16 && q_range) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
+      if (kFp8 && q_range) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
       ptx::fence_proxy_async_smem();
       ptx::mbar_arrive(ptx::smem_u32(&bars.q_ready));
     }
@@ -769,7 +715,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
       const int buf = t & 1;
       if (!wait_all(c, ptx::smem_u32(&bars.s_full[buf]), (t >> 1) & 1)) { ok = false; break; }
       if (!live) {
-        if (!kF16 && lane == 0) reinterpret_cast<volatile uint8_t*>(&bars.heavy[buf])[sw] = 0;
+        if (!kFp8 && lane == 0) reinterpret_cast<volatile uint8_t*>(&bars.heavy[buf])[sw] = 0;
         ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
         continue;
       }
@@ -799,8 +745,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
           uint32_t w[12];
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            pack24(round_up_bits<kFp4>(s[16 * qd + 4 * k]), round_up_bits<kFp4>(s[16 * qd + 4 * k + 1]),
-                   round_up_bits<kFp4>(s[16 * qd + 4 * k + 2]), round_up_bits<kFp4>(s[16 * qd + 4 * k + 3]),
+            pack24(round_up_bits(s[16 * qd + 4 * k]), round_up_bits(s[16 * qd + 4 * k + 1]),
+                   round_up_bits(s[16 * qd + 4 * k + 2]), round_up_bits(s[16 * qd + 4 * k + 3]),
                    w + 3 * k);
 #pragma unroll
           for (int v = 0; v < 3; ++v)
@@ -933,13 +879,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
           }
           sA += a0 + a1;
           sB += b0 + b1;
-          if (!kF16) {
+          if (!kFp8) {
             gA[j >> 1] = fmaxf(gA[j >> 1], fmaxf(a0, a1));
             gB[j >> 1] = fmaxf(gB[j >> 1], fmaxf(b0, b1));
           }
-          hi[2 * j] = kF16 ? pack_f16(a0, a1) : pack_bf16(a0, a1);
-          hi[2 * j + 1] = kF16 ? pack_f16(b0, b1) : pack_bf16(b0, b1);
-          if (!kF16) {
+          hi[2 * j] = kFp8 ? pack_f16(a0, a1) : pack_bf16(a0, a1);
+          hi[2 * j + 1] = kFp8 ? pack_f16(b0, b1) : pack_bf16(b0, b1);
+          if (!kFp8) {
             lo[2 * j] = pack_bf16(a0 - __uint_as_float(hi[2 * j] << 16),
                                    a1 - __uint_as_float(hi[2 * j] & 0xFFFF0000u));
             lo[2 * j + 1] = pack_bf16(b0 - __uint_as_float(hi[2 * j + 1] << 16),
@@ -947,11 +893,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
           }
         }
         ptx::tmem_st16x128b_x8(pcol + kh * 32, hi);
-        if (!kF16) ptx::tmem_st16x128b_x8(pcol + T / 2 + kh * 32, lo);
+        if (!kFp8) ptx::tmem_st16x128b_x8(pcol + T / 2 + kh * 32, lo);
       }
       lA += sA;
       lB += sB;
-      if constexpr (!kF16) {
+      if constexpr (!kFp8) {
         // The low-order terms are written for every tile; the second PV runs
         // only over the 16-key groups where one key carries more than 1/16
         // of a row's weight.  The row's sum counts the other warp's keys up
@@ -992,9 +938,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
     lB += __shfl_xor_sync(0xffffffffu, lB, 2);
     if (ok && live && wait_all(c, ptx::smem_u32(&bars.o_final), 0)) {
       ptx::tc_fence_after();
-      // 4 bits: a sum that is NaN is no empty row
-      const bool someA = kFp4 ? !(lA <= 0.f) : lA > 0.f, someB = kFp4 ? !(lB <= 0.f) : lB > 0.f;
-      const float invA = someA ? s_kv / lA : 0.f, invB = someB ? s_kv / lB : 0.f;
+      const float invA = lA > 0.f ? s_kv / lA : 0.f, invB = lB > 0.f ? s_kv / lB : 0.f;
       const bool okA = rA < p.rows, okB = rB < p.rows;
       const size_t pA = part * p.rows + rA;  // problem rows (TMEM lanes are spread)
       const size_t pB = part * p.rows + rB;
@@ -1018,8 +962,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
         }
       }
       if (rank == 0 && cq == 0 && kh == 0) {
-        const float lseA = someA ? (mA + log2f(lA)) * 0.6931471805599453f : -INFINITY;
-        const float lseB = someB ? (mB + log2f(lB)) * 0.6931471805599453f : -INFINITY;
+        const float lseA = lA > 0.f ? (mA + log2f(lA)) * 0.6931471805599453f : -INFINITY;
+        const float lseB = lB > 0.f ? (mB + log2f(lB)) * 0.6931471805599453f : -INFINITY;
         if (single) {
           if (okA) p.lse[(size_t)b * p.rows + rA] = lseA;
           if (okB) p.lse[(size_t)b * p.rows + rB] = lseB;
@@ -1051,26 +995,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(Warps<kWide>::count 
 }  // namespace
 
 bool mla_small_rows_fit(int rows, int kv_dtype) {
-  return rows <= (kv_dtype == MLA_KV_BF16 ? Layout<MLA_KV_BF16>::max_rows : Layout<MLA_KV_FP8_E4M3>::max_rows);
+  if (kv_dtype == MLA_KV_FP4_E2M1) return rows <= mla::kFewRowsFp4;  // a kernel of their own
+  return rows <= (kv_dtype == MLA_KV_FP8_E4M3 ? Layout<true>::max_rows : Layout<false>::max_rows);
 }
 
 int mla_launch_fwd_small_sm103(const mla::FwdParams& p, void* stream) {
+  const bool fp8 = p.kv_dtype == MLA_KV_FP8_E4M3;
   const bool wide = p.rows > 16;  // more than lane quarter 0 holds rows (bf16 only)
-  auto kernel = wide ? fwd_small_kernel<MLA_KV_BF16, true> : fwd_small_kernel<MLA_KV_BF16, false>;
-  int smem = Layout<MLA_KV_BF16>::SMEM_BYTES, slot = wide ? 5 : 3;
-  if (p.kv_dtype == MLA_KV_FP8_E4M3) {
-    kernel = fwd_small_kernel<MLA_KV_FP8_E4M3, false>;
-    smem = Layout<MLA_KV_FP8_E4M3>::SMEM_BYTES;
-    slot = 4;
-  } else if (p.kv_dtype == MLA_KV_FP4_E2M1) {
-    kernel = fwd_small_kernel<MLA_KV_FP4_E2M1, false>;
-    smem = Layout<MLA_KV_FP4_E2M1>::SMEM_BYTES;
-    slot = 10;
-  }
+  auto kernel = fp8 ? fwd_small_kernel<true, false>
+                    : (wide ? fwd_small_kernel<false, true> : fwd_small_kernel<false, false>);
+  const int smem = fp8 ? Layout<true>::SMEM_BYTES : Layout<false>::SMEM_BYTES;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
-  e = mla::opt_in_smem(reinterpret_cast<const void*>(kernel), smem, dev, slot);
+  e = mla::opt_in_smem(reinterpret_cast<const void*>(kernel), smem, dev, fp8 ? 4 : (wide ? 5 : 3));
   if (e != cudaSuccess) return (int)e;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = p.units != nullptr ? dim3(2 * p.unit_capacity, 1, 1)

@@ -104,7 +104,8 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
   // multiples of 128 keys); everything else on the 128-row, 64-key one.
   p.key_tile = mla_small_rows_fit(p.rows, kv_dtype) ? mla::kKeyTileSmall : mla::kKeyTile;
   p.num_sms = num_sms;
-  p.cluster_size = mla::kClusterSize;
+  const bool fp4 = kv_dtype == MLA_KV_FP4_E2M1 && p.key_tile == mla::kKeyTileSmall;
+  p.cluster_size = fp4 ? 1 : mla::kClusterSize;
 
   // Per-pair cost model of the decode kernel on GB300.  Its pipeline is bound
   // by the latency of its per-tile chain (score contraction, score swap between
@@ -115,8 +116,10 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
   // split result its partial write, and a split launch the combine pass over
   // all partials.
   const int pairs = std::max(1, num_sms / p.cluster_size);
-  const double ns_per_key = 2200.0 / p.key_tile;
-  const double ns_fixed = 10000.0, ns_empty = 400.0, ns_partial = 1000.0;
+  // The few-row kernel of 4-bit caches: single CTAs, 2.2 us per 128-key tile up
+  // to 16 rows and 2.8 up to 32.
+  const double ns_per_key = (fp4 && p.rows > 16 ? 2800.0 : 2200.0) / p.key_tile;
+  const double ns_fixed = fp4 ? 8000.0 : 10000.0, ns_empty = 400.0, ns_partial = 1000.0;
   // The combine reads every non-empty unit's partials once (about 5000
   // bytes/ns) after a launch gap.
   const double ns_combine_fixed = 12000.0;  // measured: launch, dependency wait and the LSE pass

@@ -36,9 +36,12 @@ def test_rows_keep_what_they_can():
 
 def test_plans_take_4_bit_caches():
     p = mla.plan([300, 20], 16, 1, 64, mla.KV_FP4_E2M1, num_sms=152)
-    assert p.kv_dtype == mla.KV_FP4_E2M1 and p.key_tile == 128
-    assert mla.plan([300, 20], 17, 1, 64, mla.KV_FP4_E2M1, num_sms=152).key_tile == 64
-    assert mla.dplan_info(2, 16, 1, 64, mla.KV_FP4_E2M1, False, 300, 152).key_tile == 128
+    assert p.kv_dtype == mla.KV_FP4_E2M1 and p.key_tile == 128 and (p.grid_x, p.grid_y) == (1, 2)
+    assert mla.plan([300, 20], 32, 1, 64, mla.KV_FP4_E2M1, num_sms=152).key_tile == 128
+    p = mla.plan([300, 20], 33, 1, 64, mla.KV_FP4_E2M1, num_sms=152)
+    assert p.key_tile == 64 and (p.grid_x, p.grid_y) == (2, 2)
+    d = mla.dplan_info(2, 16, 2, 64, mla.KV_FP4_E2M1, False, 300, 152)
+    assert d.key_tile == 128 and d.row_blocks == 1 and mla.dplan_info(2, 33, 1, 64, mla.KV_FP4_E2M1, False, 300, 152).key_tile == 64
 
 
 @pytest.mark.parametrize("dtype", [2, 3, 5, -1])

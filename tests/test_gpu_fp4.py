@@ -17,7 +17,9 @@ pytestmark = pytest.mark.gpu
     (3, 1, 16, [300, 0, 77], 16, False), (2, 2, 8, [31, 33], 16, True), (1, 16, 1, [5], 3, True),
     (2, 1, 17, [65, 64], 1, False), (2, 1, 128, [63, 1], 16, False), (1, 3, 12, [500], 7, True),
     (2, 4, 16, [2, 4], 64, True), (1, 2, 128, [190], 16, True), (1, 16, 64, [97], 4096, True),
-    (4, 1, 20, [1, 2, 3, 4], 1, False), (1, 1, 16, [4097], 64, False), (1, 1, 128, [2049], 1, False)])
+    (4, 1, 20, [1, 2, 3, 4], 1, False), (1, 1, 16, [4097], 64, False), (1, 1, 128, [2049], 1, False),
+    (2, 1, 32, [1000, 127], 16, False), (2, 2, 16, [385, 2], 16, True), (2, 1, 33, [200, 64], 16, False),
+    (3, 8, 4, [7, 9, 257], 1, True), (1, 4, 8, [3], 16, True), (1, 1, 25, [129], 5, False)])
 @pytest.mark.parametrize("num_sms", [0, 8])
 def test_decode(batch, sq, heads, lens, page, causal, num_sms):
     p = f4.Fp4Problem(batch, sq, heads, lens, page, causal, seed=len(lens) + heads)
@@ -120,6 +122,31 @@ def test_a_nan_scale_spoils_the_sequence_that_holds_it(heads, at, n):
     p.cache[p.table[1, 2], 3, 256 + at] = 0x7F
     out, lse, _, status = p.run()
     assert status == 0 and np.isnan(out[1]).all() and np.isnan(lse[1]).all() and np.array_equal(out[0], good[0])
+
+
+@pytest.mark.parametrize("heads", [16, 32])
+def test_waits_run_out_without_a_fault(heads):
+    """With a bound of 1 us the pipeline's waits give up, the call says so, and the next one is right."""
+    import ctypes
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = f4.Fp4Problem(4, 1, heads, [4096] * 4, 16, seed=12)
+    t = p.to_device()
+    plan = mla.plan(p.lens, heads, 1, 16, mla.KV_FP4_E2M1)
+    ws = mla.workspace_for(plan)
+    short = mla.Plan.from_buffer_copy(plan)
+    short.wait_limit_us = 1
+    out, lse = torch.zeros(4, 1, heads, 512, dtype=torch.bfloat16, device="cuda"), torch.zeros(4, 1, heads, device="cuda")
+    for pl in (short, plan):
+        mla.fwd(pl, t["q"], t["cache"], t["scale"], t["bt"], t["lens"], p.scale, out, lse, ws)
+        mla.combine(pl, t["lens"], out, lse, ws)
+        v = ctypes.c_int32(0)
+        st = mla.lib().mla_decode_check(ctypes.byref(pl), ctypes.c_void_p(ws.data_ptr()), mla._stream(None), ctypes.byref(v))
+        if pl is short:
+            assert st == mla.ERR_TIMEOUT and v.value & mla.DEVFLAG_TIMEOUT
+        else:
+            assert st == 0
+    assert_close(out.double().cpu().numpy(), lse.double().cpu().numpy(), *p.reference(), "after a call that gave up")
 
 
 def inputs(tokens, heads, seed, values=None):
