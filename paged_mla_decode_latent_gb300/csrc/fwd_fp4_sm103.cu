@@ -430,22 +430,32 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
     int* vis = reinterpret_cast<int*>(xmax + 4 * N);          // [N]
     float* inv = reinterpret_cast<float*>(vis + N);           // [N]
     // Q to f16, K-major: 72 pieces of 8 dims a row; rows past the problem's are zero.
+    static_assert(N % 16 == 0, "9 x 128 pieces are 16 rows");
     {
+      // Nine loads in flight a thread, then their stores: 16 rows a round.
       bool range = false;
-      for (int i = tid; i < N * 72; i += 128) {
-        const int r = i / 72, ch = i - 72 * r;
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < n_rows)
-          x = reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.rows + r) * mla::kDQK)[ch];
-        uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll 1
+      for (int i0 = tid; i0 < N * 72; i0 += 9 * 128) {
+        uint4 x[9];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xFFFF0000u);
-          range |= fabsf(lo) > 65504.f || fabsf(hi) > 65504.f;
-          w[e] = pack_f16(lo, hi);
+        for (int j = 0; j < 9; ++j) {
+          const int i = i0 + 128 * j, r = i / 72, ch = i - 72 * r;
+          x[j] = make_uint4(0, 0, 0, 0);
+          if (r < n_rows) x[j] = reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.rows + r) * mla::kDQK)[ch];
         }
-        st_shared_u4(sbase + L::OFF_Q + (ch >> 3) * L::kQSlab + r * 128 + (((ch & 7) ^ (r & 7)) * 16),
-                     make_uint4(w[0], w[1], w[2], w[3]));
+#pragma unroll
+        for (int j = 0; j < 9; ++j) {
+          const int i = i0 + 128 * j, r = i / 72, ch = i - 72 * r;
+          uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float lo = __uint_as_float(w[e] << 16), hi = __uint_as_float(w[e] & 0xFFFF0000u);
+            range |= fabsf(lo) > 65504.f || fabsf(hi) > 65504.f;
+            w[e] = pack_f16(lo, hi);
+          }
+          st_shared_u4(sbase + L::OFF_Q + (ch >> 3) * L::kQSlab + r * 128 + (((ch & 7) ^ (r & 7)) * 16),
+                       make_uint4(w[0], w[1], w[2], w[3]));
+        }
       }
       if (range) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
       if (tid < N) {  // keys that a row sees
