@@ -440,7 +440,7 @@ int mla_decode_epilogue(const void* ql_nope, const void* q_pe, const void* kv_c,
  *              call is queued behind and are read before the dependency wait;
  *              0: nothing is
  * Returns MLA_OK, MLA_ERR_INVALID_ARG, MLA_ERR_UNSUPPORTED (T * (H + 1) past
- * 2^31 - 1) or MLA_ERR_CUDA.
+ * 2^31 - 1; 4-bit cache: T * (H + 8)) or MLA_ERR_CUDA.
  */
 int mla_decode_rope_epilogue(const void* ql_nope, int64_t ql_stride_t, int64_t ql_stride_h,
                              const void* q_pe, int64_t q_pe_stride_t, int64_t q_pe_stride_h,

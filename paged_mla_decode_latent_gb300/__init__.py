@@ -564,16 +564,18 @@ def pages_workspace(num_pages: int, rows: int, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
-def _int32_on(dev, *tensors) -> bool:
-    """Whether these are contiguous int32 tensors of device `dev`."""
-    i32 = _torch().int32
-    return all(t.dtype is i32 and t.get_device() == dev and t.is_contiguous() for t in tensors)
-
-
 def _table_on(dev, table) -> bool:
-    return (table.dtype is _torch().int32 and table.dim() == 2 and table.get_device() == dev
-            and table.shape[1] > 0 and table.stride(1) == 1
-            and (table.shape[0] < 2 or table.stride(0) >= table.shape[1]))
+    """Whether this is an int32 table [rows, width] of device `dev`, its rows contiguous."""
+    if table.dtype is not _torch().int32 or table.dim() != 2 or table.get_device() != dev:
+        return False
+    rows, width = table.shape
+    step, one = table.stride()
+    return one == 1 and width > 0 and (rows < 2 or step >= width)
+
+
+def _ints_on(dev, t, n) -> bool:
+    """Whether this is a contiguous int32 tensor of n elements on device `dev`."""
+    return t.dtype is _torch_module.int32 and t.shape == (n,) and t.get_device() == dev and t.is_contiguous()
 
 
 def _layers(kv_cache, pages: int, dev):
@@ -597,9 +599,9 @@ def pages_resize(refs, block_table, seq_lens, new_lens, page_size: int, workspac
     are changed in place.  slots int64 [rows, tokens]: where each row's last tokens go, -1 for those not added."""
     torch = _torch()
     dev, rows = _device(refs), block_table.shape[0]
-    if not (dev >= 0 and refs.dim() == 1 and _int32_on(dev, refs, seq_lens, new_lens) and _table_on(dev, block_table)
-            and seq_lens.shape == new_lens.shape == (rows,) and workspace.is_contiguous()
-            and workspace.get_device() == dev and _status_on(dev, status)
+    if not (dev >= 0 and _table_on(dev, block_table) and _ints_on(dev, refs, refs.shape[0])
+            and _ints_on(dev, seq_lens, rows) and _ints_on(dev, new_lens, rows)
+            and workspace.is_contiguous() and workspace.get_device() == dev and _status_on(dev, status)
             and (slots is None or slots.dtype is torch.int64 and slots.dim() == 2 and slots.shape[0] == rows
                  and slots.is_contiguous() and slots.get_device() == dev)):
         raise MLADecodeError(ERR_INVALID_ARG, "mla_pages_resize")
@@ -617,10 +619,11 @@ def pages_fork(refs, block_table, seq_lens, parents, table_out, lens_out, kv_cac
     """``mla_pages_fork``: row i of table_out and lens_out goes on from row parents[i] (-1: empty) of block_table and
     seq_lens; refs is changed in place.  kv_cache: [pages, page, row], or [layers, pages, page, row]."""
     dev, rows, out_rows = _device(refs), block_table.shape[0], table_out.shape[0]
-    cache = _layers(kv_cache, refs.shape[0], dev) if dev >= 0 and refs.dim() == 1 else None
-    if not (cache is not None and _int32_on(dev, refs, seq_lens, parents, lens_out) and _table_on(dev, block_table)
-            and _table_on(dev, table_out) and seq_lens.shape == (rows,)
-            and parents.shape == lens_out.shape == (out_rows,) and table_out.shape[1] >= block_table.shape[1]
+    cache = _layers(kv_cache, refs.shape[0], dev) if dev >= 0 else None
+    if not (cache is not None and _table_on(dev, block_table) and _table_on(dev, table_out)
+            and _ints_on(dev, refs, refs.shape[0]) and _ints_on(dev, seq_lens, rows)
+            and _ints_on(dev, parents, out_rows) and _ints_on(dev, lens_out, out_rows)
+            and table_out.shape[1] >= block_table.shape[1]
             and workspace.is_contiguous() and workspace.get_device() == dev and _status_on(dev, status)):
         raise MLADecodeError(ERR_INVALID_ARG, "mla_pages_fork")
     page_size, layers, layer_stride, row_bytes = cache
@@ -637,13 +640,13 @@ def pages_compact(refs, block_table, seq_lens, kv_cache, page_map, n_live, works
     """``mla_pages_compact``: held pages move to the front of the cache (as ``pages_fork`` takes it); refs and
     block_table (None: no table) follow, page_map int32 [pages] and n_live int32 [1] say where they went."""
     dev = _device(refs)
-    cache = _layers(kv_cache, refs.shape[0], dev) if dev >= 0 and refs.dim() == 1 else None
+    pages = refs.shape[0]
+    cache = _layers(kv_cache, pages, dev) if dev >= 0 else None
     rows = 0 if block_table is None else block_table.shape[0]
-    if not (cache is not None and _int32_on(dev, refs, page_map, n_live) and page_map.shape == refs.shape
-            and n_live.numel() == 1 and workspace.is_contiguous() and workspace.get_device() == dev
+    if not (cache is not None and _ints_on(dev, refs, pages) and _ints_on(dev, page_map, pages)
+            and _ints_on(dev, n_live, 1) and workspace.is_contiguous() and workspace.get_device() == dev
             and _status_on(dev, status)
-            and (rows == 0 or _table_on(dev, block_table) and seq_lens is not None and _int32_on(dev, seq_lens)
-                 and seq_lens.shape == (rows,))):
+            and (rows == 0 or _table_on(dev, block_table) and seq_lens is not None and _ints_on(dev, seq_lens, rows))):
         raise MLADecodeError(ERR_INVALID_ARG, "mla_pages_compact")
     page_size, layers, layer_stride, row_bytes = cache
     st = lib().mla_pages_compact(

@@ -10,8 +10,11 @@
 // added up by its CTA, the ranks inside it.  Counts change by integer atomics,
 // whose order does not show.
 //
-// Each call is a short chain of kernels, every one launched while the one
-// before it still runs and waiting for it (programmatic dependent launch).
+// A call is a chain of steps, each of which needs all of the one before.  Where
+// the book is small a cluster of eight CTAs takes the steps in one launch, with the
+// cluster's barrier between them; else each step is a kernel, launched while the
+// one before it still runs and waiting for it (programmatic dependent launch).
+// Moving rows is always a kernel of its own, over the whole GPU.
 //
 // refs and the tables are small (4 bytes a page or entry), so resize is bound by
 // the latency of its three kernels, fork and compact by those and by the rows
@@ -31,9 +34,13 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kPer = 8;                   // pages a thread looks at in a chunk
 constexpr int kChunk = kThreads * kPer;   // 4096
-constexpr int kSlice = 2048;              // table entries a CTA takes at a time
+constexpr int kWarps = kThreads / 32;
+constexpr int kSlice = 256;               // table entries a warp takes at a time
 constexpr int kSegment = 4 * 16 * kThreads;  // bytes that a CTA moves at a time
 constexpr int kMaxRows = 65535;
+constexpr int kCluster = 8;
+// What a cluster takes alone: more pages or entries than these it reads too slowly.
+constexpr int64_t kClusterPages = 1 << 16, kClusterEntries = 1 << 18;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t a) { return ceil_div(a, 256) * 256; }
@@ -84,7 +91,7 @@ __device__ __forceinline__ int length(const Book& k, const Table& t, int len) {
 }
 
 __device__ __forceinline__ int pages_of(int len, int page_size) {
-  return (int)(((int64_t)len + page_size - 1) / page_size);
+  return (int)(((uint32_t)len + (uint32_t)page_size - 1u) / (uint32_t)page_size);  // len >= 0: below 2^32
 }
 
 __device__ __forceinline__ bool known(const Book& k, int page) {
@@ -126,6 +133,11 @@ __device__ T block_scan(T v, T* before) {
 // The counts of all chunks, and of those before `chunk`.
 __device__ int chunk_sums(const Book& k, int chunk, int* before) {
   int all = 0, mine = 0, unused;
+  if (k.chunks <= 32) {  // each warp for itself
+    const int lane = threadIdx.x & 31, v = lane < k.chunks ? k.count[lane] : 0;
+    *before = __reduce_add_sync(0xffffffffu, lane < chunk ? v : 0);
+    return __reduce_add_sync(0xffffffffu, v);
+  }
   for (int c = threadIdx.x; c < k.chunks; c += kThreads) {
     const int v = k.count[c];
     all += v;
@@ -164,46 +176,46 @@ __device__ void count_chunk(const Book& k, int chunk) {
 
 // --------------------------------------------------------------- resize ---
 
-// CTA 0: the pages that each row needs and those needed before it.  The others:
-// pages that rows give back.
-__global__ void __launch_bounds__(kThreads) resize_ask_kernel(Book k, Table t, const int32_t* new_lens,
-                                                              int slices) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
-  if (blockIdx.x == 0) {
-    int64_t sum = 0;
-    for (int b0 = 0; b0 < t.rows; b0 += kThreads) {
-      const int b = b0 + threadIdx.x;
-      int need = 0;
-      if (b < t.rows) {
-        const int old = length(k, t, t.lens[b]);
-        need = max(0, pages_of(length(k, t, new_lens[b]), k.page_size) - pages_of(old, k.page_size));
-        k.row_b[b] = old;
-      }
-      // A row that 2^31 - 1 pages or more are asked for before gets none: there are fewer.
-      int64_t before;
-      const int64_t all = block_scan((int64_t)need, &before);
-      if (b < t.rows) k.row_a[b] = (int)min(sum + before, (int64_t)INT32_MAX);
-      sum += all;
+// The pages that each row needs, and those needed before it.
+__device__ void resize_needs(const Book& k, const Table& t, const int32_t* new_lens) {
+  int64_t sum = 0;
+  for (int b0 = 0; b0 < t.rows; b0 += kThreads) {
+    const int b = b0 + threadIdx.x;
+    int need = 0;
+    if (b < t.rows) {
+      const int old = length(k, t, t.lens[b]);
+      need = max(0, pages_of(length(k, t, new_lens[b]), k.page_size) - pages_of(old, k.page_size));
+      k.row_b[b] = old;
     }
-    if (threadIdx.x == 0) k.totals->wanted = (int)min(sum, (int64_t)INT32_MAX);
-    return;
+    // A row that 2^31 - 1 pages or more are asked for before gets none: there are fewer.
+    int64_t before;
+    const int64_t all = block_scan((int64_t)need, &before);
+    if (b < t.rows) k.row_a[b] = (int)min(sum + before, (int64_t)INT32_MAX);
+    sum += all;
   }
-  for (int64_t u = blockIdx.x - 1; u < (int64_t)t.rows * slices; u += gridDim.x - 1) {
+  if (threadIdx.x == 0) k.totals->wanted = (int)min(sum, (int64_t)INT32_MAX);
+}
+
+// A warp's slices of the rows: CTA `id` of `n`.
+struct Slices {
+  int64_t u, end, step;
+  int lane;
+  __device__ Slices(int64_t count, int id, int n)
+      : u((int64_t)id * kWarps + (threadIdx.x >> 5)), end(count), step((int64_t)n * kWarps), lane(threadIdx.x & 31) {}
+};
+
+// Pages that rows give back: CTA `id` of `n`.
+__device__ void resize_release(const Book& k, const Table& t, const int32_t* new_lens, int slices, int id, int n) {
+  const Slices w((int64_t)t.rows * slices, id, n);
+  for (int64_t u = w.u; u < w.end; u += w.step) {
     const int b = (int)(u / slices), j0 = (int)(u % slices) * kSlice;
     const int first = max(j0, pages_of(length(k, t, new_lens[b]), k.page_size));
     const int end = min(j0 + kSlice, pages_of(length(k, t, t.lens[b]), k.page_size));
-    for (int j = first + threadIdx.x; j < end; j += kThreads) {
+    for (int j = first + w.lane; j < end; j += 32) {
       const int page = t.at[b * t.stride + j];
       if (known(k, page)) atomicSub(&k.refs[page], 1);
     }
   }
-}
-
-__global__ void __launch_bounds__(kThreads) count_free_kernel(Book k) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
-  count_chunk<false>(k, blockIdx.x);
 }
 
 // What row b gets.
@@ -224,70 +236,114 @@ __device__ __forceinline__ Grant granted(const Book& k, const Table& t, const in
   return g;
 }
 
-// CTAs below k.chunks: the free pages of a chunk go to the rows that asked.  The
-// others: the rows' lengths, and the slots of tokens in pages that they had.
+// The rows' lengths, and the slots of tokens in pages that they had: CTA `id` of `n`.
+__device__ void resize_rows(const Book& k, const Table& t, const int32_t* new_lens, int64_t* slots, int tokens,
+                            int free_pages, int id, int n) {
+  const int per = max(tokens, 1);
+  for (int64_t i = (int64_t)id * kThreads + threadIdx.x; i < (int64_t)t.rows * per; i += (int64_t)n * kThreads) {
+    const int b = (int)(i / per), c = (int)(i % per);
+    const Grant g = granted(k, t, new_lens, b, free_pages);
+    if (c == 0) {
+      if (!g.given) flag(k, MLA_DEVFLAG_NO_PAGES);
+      t.lens[b] = g.len;
+      if (g.len > g.old_len && g.old_len % k.page_size != 0) {  // it grows in a page that it had
+        const int page = t.at[b * t.stride + g.held - 1];
+        if (known(k, page) && k.refs[page] > 1) flag(k, MLA_DEVFLAG_SHARED);
+      }
+    }
+    if (tokens == 0) continue;
+    const int pos = g.len - tokens + c;
+    if (pos < g.old_len) {
+      slots[i] = -1;
+    } else if (pos / k.page_size < g.held) {
+      slots[i] = (int64_t)t.at[b * t.stride + pos / k.page_size] * k.page_size + pos % k.page_size;
+    }
+  }
+}
+
+// The free pages of a chunk go to the rows that asked.  `before`: those of earlier chunks.
+__device__ void resize_give(const Book& k, const Table& t, const int32_t* new_lens, int64_t* slots, int tokens, int chunk,
+                            int free_pages, int before) {
+  // The chunk's free pages in a row first, then a page a thread: they are few, and
+  // eight times the work below in every warp that holds one of them took 20 us at
+  // 1.5 million pages and 256 rows, against 8.
+  __shared__ uint16_t list[kChunk];
+  const int wanted = k.totals->wanted;
+  if (before >= wanted) return;
+  int v[kPer], n = 0, at;
+  const int64_t p0 = (int64_t)chunk * kChunk;
+  load_refs(k, p0 + threadIdx.x * kPer, v);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) n += v[i] == 0;
+  __syncthreads();  // list's readers of the chunk before
+  const int all = min(block_scan(n, &at), wanted - before);
+#pragma unroll
+  for (int i = 0; i < kPer; ++i)
+    if (v[i] == 0) list[at++] = (uint16_t)(threadIdx.x * kPer + i);
+  __syncthreads();
+  for (int i = threadIdx.x; i < all; i += kThreads) {
+    const int r = before + i;
+    int b = 0, hi = t.rows;  // the last row that has asked for r or fewer pages before it
+    while (hi - b > 1) {
+      const int mid = (b + hi) / 2;
+      if (k.row_a[mid] <= r) b = mid;
+      else hi = mid;
+    }
+    const Grant g = granted(k, t, new_lens, b, free_pages);
+    if (!g.given) continue;
+    const int j = g.held + (r - k.row_a[b]);
+    const int64_t page = p0 + list[i];
+    t.at[b * t.stride + j] = (int32_t)page;
+    k.refs[page] = 1;
+    // the tokens asked about that this page holds
+    const int64_t start = (int64_t)j * k.page_size, from = (int64_t)g.len - tokens;
+    if (tokens > 0)
+      for (int64_t pos = max(start, max(from, (int64_t)g.old_len)); pos < min(start + k.page_size, (int64_t)g.len); ++pos)
+        slots[(int64_t)b * tokens + (pos - from)] = page * k.page_size + (pos - start);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) resize_ask_kernel(Book k, Table t, const int32_t* new_lens,
+                                                              int slices) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  if (blockIdx.x == 0) resize_needs(k, t, new_lens);
+  else resize_release(k, t, new_lens, slices, blockIdx.x - 1, gridDim.x - 1);
+}
+
+__global__ void __launch_bounds__(kThreads) count_free_kernel(Book k) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  count_chunk<false>(k, blockIdx.x);
+}
+
 __global__ void __launch_bounds__(kThreads) resize_give_kernel(Book k, Table t, const int32_t* new_lens,
                                                                int64_t* slots, int tokens) {
   ptx::grid_dependency_wait();
   ptx::launch_dependents();
-  const int wanted = k.totals->wanted;
   int before;
-  const int free_pages = chunk_sums(k, min((int)blockIdx.x, k.chunks), &before);
-  if ((int)blockIdx.x >= k.chunks) {
-    const int per = max(tokens, 1);
-    for (int64_t i = (int64_t)(blockIdx.x - k.chunks) * kThreads + threadIdx.x; i < (int64_t)t.rows * per;
-         i += (int64_t)(gridDim.x - k.chunks) * kThreads) {
-      const int b = (int)(i / per), c = (int)(i % per);
-      const Grant g = granted(k, t, new_lens, b, free_pages);
-      if (c == 0) {
-        if (!g.given) flag(k, MLA_DEVFLAG_NO_PAGES);
-        t.lens[b] = g.len;
-        if (g.len > g.old_len && g.old_len % k.page_size != 0) {  // it grows in a page that it had
-          const int page = t.at[b * t.stride + g.held - 1];
-          if (known(k, page) && k.refs[page] > 1) flag(k, MLA_DEVFLAG_SHARED);
-        }
-      }
-      if (tokens == 0) continue;
-      const int pos = g.len - tokens + c;
-      const int64_t slot = i;
-      if (pos < g.old_len) {
-        slots[slot] = -1;
-      } else if (pos / k.page_size < g.held) {
-        slots[slot] = (int64_t)t.at[b * t.stride + pos / k.page_size] * k.page_size + pos % k.page_size;
-      }
-    }
-    return;
+  const int chunk = min((int)blockIdx.x, k.chunks), free_pages = chunk_sums(k, chunk, &before);
+  if (chunk < k.chunks) resize_give(k, t, new_lens, slots, tokens, chunk, free_pages, before);
+  else resize_rows(k, t, new_lens, slots, tokens, free_pages, blockIdx.x - k.chunks, gridDim.x - k.chunks);
+}
+
+// All of it by one cluster.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    resize_kernel(Book k, Table t, const int32_t* new_lens, int slices, int64_t* slots, int tokens) {
+  const int id = blockIdx.x;
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  if (id == 0) resize_needs(k, t, new_lens);
+  resize_release(k, t, new_lens, slices, kCluster - 1 - id, kCluster);
+  ptx::cluster_sync_all();
+  for (int c = id; c < k.chunks; c += kCluster) count_chunk<false>(k, c);
+  ptx::cluster_sync_all();
+  int before, free_pages = chunk_sums(k, id, &before);
+  for (int c = id; c < k.chunks; c += kCluster) {
+    if (c != id) free_pages = chunk_sums(k, c, &before);
+    resize_give(k, t, new_lens, slots, tokens, c, free_pages, before);
   }
-  if (before >= wanted) return;
-  int v[kPer], n = 0, r;
-  const int64_t p0 = (int64_t)blockIdx.x * kChunk + threadIdx.x * kPer;
-  load_refs(k, p0, v);
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) n += v[i] == 0;
-  block_scan(n, &r);
-  r += before;
-  for (int i = 0; i < kPer; ++i) {
-    if (v[i] != 0) continue;
-    if (r >= wanted) break;
-    int lo = 0, hi = t.rows;  // the last row that has asked for r or fewer pages before it
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) / 2;
-      if (k.row_a[mid] <= r) lo = mid;
-      else hi = mid;
-    }
-    const Grant g = granted(k, t, new_lens, lo, free_pages);
-    if (g.given) {
-      const int j = g.held + (r - k.row_a[lo]);
-      const int64_t page = p0 + i;
-      t.at[lo * t.stride + j] = (int32_t)page;
-      k.refs[page] = 1;
-      // the tokens asked about that this page holds
-      const int64_t first = (int64_t)j * k.page_size, from = (int64_t)g.len - tokens;
-      for (int64_t pos = max(first, max(from, (int64_t)g.old_len)); pos < min(first + k.page_size, (int64_t)g.len); ++pos)
-        if (tokens > 0) slots[(int64_t)lo * tokens + (pos - from)] = page * k.page_size + (pos - first);
-    }
-    ++r;
-  }
+  resize_rows(k, t, new_lens, slots, tokens, free_pages, kCluster - 1 - id, kCluster);
 }
 
 // ----------------------------------------------------------------- fork ---
@@ -300,48 +356,43 @@ struct Children {
   int rows;
 };
 
-// CTA 0: which children need a copy of their parent's last page.  The others: the
-// parents' counts, by children - 1 for whole pages, and for a partly filled last
-// page by the one child that keeps it.
-__global__ void __launch_bounds__(kThreads) fork_ask_kernel(Book k, Table t, Children c, int slices) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
-  if (blockIdx.x == 0) {
-    int32_t* first = k.row_a;  // a parent's first child
-    for (int r = threadIdx.x; r < t.rows; r += kThreads) first[r] = INT32_MAX;
-    __syncthreads();
-    for (int i = threadIdx.x; i < c.rows; i += kThreads) {
-      const int r = c.parents[i];
-      if (r >= 0 && r < t.rows) atomicMin(&first[r], i);
-      else if (r != -1) flag(k, MLA_DEVFLAG_BAD_ROW);
-    }
-    __syncthreads();
-    int sum = 0;
-    for (int i0 = 0; i0 < c.rows; i0 += kThreads) {
-      const int i = i0 + threadIdx.x, r = i < c.rows ? c.parents[i] : -1;
-      const int copies = r >= 0 && r < t.rows && length(k, t, t.lens[r]) % k.page_size != 0 && __ldcg(&first[r]) != i;
-      int before;
-      const int all = block_scan(copies, &before);
-      if (copies) k.row_b[sum + before] = i;
-      sum += all;
-    }
-    if (threadIdx.x == 0) k.totals->wanted = sum;
-    return;
+// Which children need a copy of their parent's last page.
+__device__ void fork_needs(const Book& k, const Table& t, const Children& c) {
+  int32_t* first = k.row_a;  // a parent's first child
+  for (int r = threadIdx.x; r < t.rows; r += kThreads) first[r] = INT32_MAX;
+  __syncthreads();
+  for (int i = threadIdx.x; i < c.rows; i += kThreads) {
+    const int r = c.parents[i];
+    if (r >= 0 && r < t.rows) atomicMin(&first[r], i);
+    else if (r != -1) flag(k, MLA_DEVFLAG_BAD_ROW);
   }
-  int counted = -1, children = 0;
-  for (int64_t u = blockIdx.x - 1; u < (int64_t)t.rows * slices; u += gridDim.x - 1) {
+  __syncthreads();
+  int sum = 0;
+  for (int i0 = 0; i0 < c.rows; i0 += kThreads) {
+    const int i = i0 + threadIdx.x, r = i < c.rows ? c.parents[i] : -1;
+    const int copies = r >= 0 && r < t.rows && length(k, t, t.lens[r]) % k.page_size != 0 && __ldcg(&first[r]) != i;
+    int before;
+    const int all = block_scan(copies, &before);
+    if (copies) k.row_b[sum + before] = i;
+    sum += all;
+  }
+  if (threadIdx.x == 0) k.totals->wanted = sum;
+}
+
+// The parents' counts, by children - 1 for whole pages, and for a partly filled
+// last page by the one child that keeps it: CTA `id` of `n`.
+__device__ void fork_release(const Book& k, const Table& t, const Children& c, int slices, int id, int n) {
+  const Slices w((int64_t)t.rows * slices, id, n);
+  for (int64_t u = w.u; u < w.end; u += w.step) {
     const int r = (int)(u / slices), j0 = (int)(u % slices) * kSlice;
     const int len = length(k, t, t.lens[r]), whole = len / k.page_size;
     const int end = min(j0 + kSlice, pages_of(len, k.page_size));
     if (j0 >= end) continue;
-    if (r != counted) {
-      int n = 0, unused;
-      for (int i = threadIdx.x; i < c.rows; i += kThreads) n += c.parents[i] == r;
-      children = block_scan(n, &unused);
-      counted = r;
-    }
+    int children = 0;
+    for (int i = w.lane; i < c.rows; i += 32) children += c.parents[i] == r;
+    children = __reduce_add_sync(0xffffffffu, children);
     if (children == 1) continue;
-    for (int j = j0 + threadIdx.x; j < end; j += kThreads) {
+    for (int j = j0 + w.lane; j < end; j += 32) {
       const int page = t.at[r * t.stride + j];
       const int change = (j < whole ? children : min(children, 1)) - 1;
       if (known(k, page) && change != 0) atomicAdd(&k.refs[page], change);
@@ -349,31 +400,24 @@ __global__ void __launch_bounds__(kThreads) fork_ask_kernel(Book k, Table t, Chi
   }
 }
 
-// CTAs below k.chunks count; the others write the children's rows.
-__global__ void __launch_bounds__(kThreads) fork_rows_kernel(Book k, Table t, Children c, int slices) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
-  if ((int)blockIdx.x < k.chunks) {
-    count_chunk<false>(k, blockIdx.x);
-    return;
-  }
-  for (int64_t u = blockIdx.x - k.chunks; u < (int64_t)c.rows * slices; u += gridDim.x - k.chunks) {
+// The children's rows: CTA `id` of `n`.
+__device__ void fork_rows(const Book& k, const Table& t, const Children& c, int slices, int id, int n) {
+  const Slices w((int64_t)c.rows * slices, id, n);
+  for (int64_t u = w.u; u < w.end; u += w.step) {
     const int i = (int)(u / slices), j0 = (int)(u % slices) * kSlice, r = c.parents[i];
     const int len = r >= 0 && r < t.rows ? length(k, t, t.lens[r]) : 0;
-    if (j0 == 0 && threadIdx.x == 0) c.lens[i] = len;
+    if (j0 == 0 && w.lane == 0) c.lens[i] = len;
     const int end = min(j0 + kSlice, pages_of(len, k.page_size));
-    for (int j = j0 + threadIdx.x; j < end; j += kThreads) c.table[i * c.stride + j] = t.at[r * t.stride + j];
+    for (int j = j0 + w.lane; j < end; j += 32) c.table[i * c.stride + j] = t.at[r * t.stride + j];
   }
 }
 
-// The k-th free page goes to the k-th child that needs one.
-__global__ void __launch_bounds__(kThreads) fork_give_kernel(Book k, Table t, Children c) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
+// The k-th free page goes to the k-th child that needs one: those of a chunk.
+__device__ void fork_give(const Book& k, const Children& c, int chunk) {
   const int wanted = k.totals->wanted;
   int before;
-  const int free_pages = chunk_sums(k, blockIdx.x, &before);
-  if (blockIdx.x == 0) {
+  const int free_pages = chunk_sums(k, chunk, &before);
+  if (chunk == 0) {
     if (threadIdx.x == 0) k.totals->given = min(wanted, free_pages);
     // Children that find none keep their parent's whole pages.
     for (int r = free_pages + threadIdx.x; r < wanted; r += kThreads) {
@@ -384,7 +428,7 @@ __global__ void __launch_bounds__(kThreads) fork_give_kernel(Book k, Table t, Ch
   }
   if (before >= wanted) return;
   int v[kPer], n = 0, r;
-  const int64_t p0 = (int64_t)blockIdx.x * kChunk + threadIdx.x * kPer;
+  const int64_t p0 = (int64_t)chunk * kChunk + threadIdx.x * kPer;
   load_refs(k, p0, v);
 #pragma unroll
   for (int i = 0; i < kPer; ++i) n += v[i] == 0;
@@ -399,6 +443,41 @@ __global__ void __launch_bounds__(kThreads) fork_give_kernel(Book k, Table t, Ch
     k.row_c[r] = (int32_t)(p0 + i);
     ++r;
   }
+}
+
+__global__ void __launch_bounds__(kThreads) fork_ask_kernel(Book k, Table t, Children c, int slices) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  if (blockIdx.x == 0) fork_needs(k, t, c);
+  else fork_release(k, t, c, slices, blockIdx.x - 1, gridDim.x - 1);
+}
+
+__global__ void __launch_bounds__(kThreads) fork_rows_kernel(Book k, Table t, Children c, int slices) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  if ((int)blockIdx.x < k.chunks) count_chunk<false>(k, blockIdx.x);
+  else fork_rows(k, t, c, slices, blockIdx.x - k.chunks, gridDim.x - k.chunks);
+}
+
+__global__ void __launch_bounds__(kThreads) fork_give_kernel(Book k, Children c) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  fork_give(k, c, blockIdx.x);
+}
+
+// The three steps by one cluster.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    fork_kernel(Book k, Table t, Children c, int slices) {
+  const int id = blockIdx.x;
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  if (id == 0) fork_needs(k, t, c);
+  fork_release(k, t, c, slices, kCluster - 1 - id, kCluster);
+  fork_rows(k, t, c, slices, kCluster - 1 - id, kCluster);
+  ptx::cluster_sync_all();
+  for (int x = id; x < k.chunks; x += kCluster) count_chunk<false>(k, x);
+  ptx::cluster_sync_all();
+  for (int x = id; x < k.chunks; x += kCluster) fork_give(k, c, x);
 }
 
 // The first `bytes` bytes at `from` to `to`, by the CTA: segment `s` of them.
@@ -441,14 +520,12 @@ __global__ void __launch_bounds__(kThreads) count_live_kernel(Book k) {
 
 // With n live pages: holes below n (page_b) and live pages from n on (page_a),
 // both in order, and each of the latter's place in that order (page_c).
-__global__ void __launch_bounds__(kThreads) compact_match_kernel(Book k, int32_t* map, int32_t* n_live) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
+__device__ void compact_match(const Book& k, int32_t* map, int32_t* n_live, int chunk) {
   int before;
-  const int n = chunk_sums(k, blockIdx.x, &before);
-  const int64_t p0 = (int64_t)blockIdx.x * kChunk + threadIdx.x * kPer;
+  const int n = chunk_sums(k, chunk, &before);
+  const int64_t p0 = (int64_t)chunk * kChunk + threadIdx.x * kPer;
   int low = 0, unused;  // live pages below n
-  if ((int)blockIdx.x >= n / kChunk) {
+  if (chunk >= n / kChunk) {
     int at_n;
     chunk_sums(k, n / kChunk, &at_n);
     int u[kPer], c = 0;
@@ -478,7 +555,7 @@ __global__ void __launch_bounds__(kThreads) compact_match_kernel(Book k, int32_t
     }
     r += live;
   }
-  if (blockIdx.x == n / kChunk || (n / kChunk == k.chunks && blockIdx.x == 0)) {
+  if (chunk == n / kChunk || (n / kChunk == k.chunks && chunk == 0)) {
     // (n == pages at a chunk's end: every page is live, and none moves)
     if (threadIdx.x == 0) {
       k.totals->live = n;
@@ -486,6 +563,23 @@ __global__ void __launch_bounds__(kThreads) compact_match_kernel(Book k, int32_t
       *n_live = n;
     }
   }
+}
+
+__global__ void __launch_bounds__(kThreads) compact_match_kernel(Book k, int32_t* map, int32_t* n_live) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  compact_match(k, map, n_live, blockIdx.x);
+}
+
+// Both steps by one cluster.
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    compact_kernel(Book k, int32_t* map, int32_t* n_live) {
+  const int id = blockIdx.x;
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  for (int x = id; x < k.chunks; x += kCluster) count_chunk<true>(k, x);
+  ptx::cluster_sync_all();
+  for (int x = id; x < k.chunks; x += kCluster) compact_match(k, map, n_live, x);
 }
 
 __global__ void __launch_bounds__(kThreads) compact_move_kernel(Book k, Table t, Cache cache, int32_t* map, int slices) {
@@ -498,10 +592,11 @@ __global__ void __launch_bounds__(kThreads) compact_move_kernel(Book k, Table t,
     k.refs[to] = k.refs[from];
     k.refs[from] = 0;
   }
-  for (int64_t u = blockIdx.x; u < (int64_t)t.rows * slices; u += gridDim.x) {
+  const Slices w((int64_t)t.rows * slices, blockIdx.x, gridDim.x);
+  for (int64_t u = w.u; u < w.end; u += w.step) {
     const int b = (int)(u / slices), j0 = (int)(u % slices) * kSlice;
     const int end = min(j0 + kSlice, pages_of(length(k, t, t.lens[b]), k.page_size));
-    for (int j = j0 + threadIdx.x; j < end; j += kThreads) {
+    for (int j = j0 + w.lane; j < end; j += 32) {
       const int page = t.at[b * t.stride + j];
       if (!known(k, page)) continue;
       if (page < n) {
@@ -597,6 +692,10 @@ cudaError_t launch(void (*kernel)(A...), int64_t grid, void* stream, A... args) 
 // CTAs for work in pieces: all of them, up to what the GPU runs in a few rounds.
 int64_t some(int64_t pieces) { return std::max<int64_t>(1, std::min<int64_t>(pieces, 152 * 8)); }
 
+bool by_cluster(int64_t pages, int64_t rows, int64_t width) {
+  return pages <= kClusterPages && rows * width <= kClusterEntries;
+}
+
 bool overlap(const void* a, int64_t a_bytes, const void* b, int64_t b_bytes) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
   return x < y + (uintptr_t)b_bytes && y < x + (uintptr_t)a_bytes;
@@ -622,7 +721,12 @@ extern "C" int mla_pages_resize(int32_t* refs, int64_t num_pages, int32_t* block
   if (new_lens == nullptr || misaligned(new_lens, 4) || overlap(new_lens, 4ll * rows, seq_lens, 4ll * rows))
     return MLA_ERR_INVALID_ARG;
   const int slices = (int)ceil_div(width, kSlice);
-  if (launch(resize_ask_kernel, 1 + some((int64_t)rows * slices), stream, k, t, new_lens, slices) != cudaSuccess ||
+  if (by_cluster(num_pages, rows, width)) {
+    return launch(resize_kernel, kCluster, stream, k, t, new_lens, slices, slots, (int)tokens) == cudaSuccess
+               ? MLA_OK
+               : MLA_ERR_CUDA;
+  }
+  if (launch(resize_ask_kernel, 1 + some(ceil_div((int64_t)rows * slices, kWarps)), stream, k, t, new_lens, slices) != cudaSuccess ||
       launch(count_free_kernel, k.chunks, stream, k) != cudaSuccess ||
       launch(resize_give_kernel, k.chunks + some(ceil_div((int64_t)rows * std::max(tokens, 1), kThreads)), stream, k, t,
              new_lens, slots, (int)tokens) != cudaSuccess)
@@ -655,10 +759,14 @@ extern "C" int mla_pages_fork(int32_t* refs, int64_t num_pages, const int32_t* b
   const Children c{parents, table_out, out_stride, lens_out, out_rows};
   const int slices = (int)ceil_div(width, kSlice);
   const int64_t segments = ceil_div(row_bytes * page_size, kSegment);
-  if (launch(fork_ask_kernel, 1 + some((int64_t)rows * slices), stream, k, t, c, slices) != cudaSuccess ||
-      launch(fork_rows_kernel, k.chunks + some((int64_t)out_rows * slices), stream, k, t, c, slices) != cudaSuccess ||
-      launch(fork_give_kernel, k.chunks, stream, k, t, c) != cudaSuccess ||
-      launch(fork_copy_kernel, some((int64_t)out_rows * layers * segments), stream, k, t, c, cache) != cudaSuccess)
+  const bool cluster = by_cluster(num_pages, std::max(rows, out_rows), width);
+  if (cluster && launch(fork_kernel, kCluster, stream, k, t, c, slices) != cudaSuccess) return MLA_ERR_CUDA;
+  if (!cluster &&
+      (launch(fork_ask_kernel, 1 + some(ceil_div((int64_t)rows * slices, kWarps)), stream, k, t, c, slices) != cudaSuccess ||
+       launch(fork_rows_kernel, k.chunks + some(ceil_div((int64_t)out_rows * slices, kWarps)), stream, k, t, c, slices) != cudaSuccess ||
+       launch(fork_give_kernel, k.chunks, stream, k, c) != cudaSuccess))
+    return MLA_ERR_CUDA;
+  if (launch(fork_copy_kernel, some((int64_t)out_rows * layers * segments), stream, k, t, c, cache) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }
@@ -679,10 +787,13 @@ extern "C" int mla_pages_compact(int32_t* refs, int64_t num_pages, int32_t* bloc
     return MLA_ERR_INVALID_ARG;
   const int slices = rows == 0 ? 1 : (int)ceil_div(width, kSlice);
   const int64_t segments = ceil_div(row_bytes * page_size, kSegment);
-  const int64_t pieces = std::max(num_pages / 2 * layers * segments, (int64_t)rows * slices);
-  if (launch(count_live_kernel, k.chunks, stream, k) != cudaSuccess ||
-      launch(compact_match_kernel, k.chunks, stream, k, page_map, n_live) != cudaSuccess ||
-      launch(compact_move_kernel, some(pieces), stream, k, t, cache, page_map, slices) != cudaSuccess)
+  const int64_t pieces = std::max(num_pages / 2 * layers * segments, ceil_div((int64_t)rows * slices, kWarps));
+  const bool cluster = by_cluster(num_pages, 0, 0);
+  if (cluster && launch(compact_kernel, kCluster, stream, k, page_map, n_live) != cudaSuccess) return MLA_ERR_CUDA;
+  if (!cluster && (launch(count_live_kernel, k.chunks, stream, k) != cudaSuccess ||
+                   launch(compact_match_kernel, k.chunks, stream, k, page_map, n_live) != cudaSuccess))
+    return MLA_ERR_CUDA;
+  if (launch(compact_move_kernel, some(pieces), stream, k, t, cache, page_map, slices) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }
