@@ -205,10 +205,12 @@ cudaError_t opt_in_smem(const void* kernel, int bytes, int dev, int slot) {
 }  // namespace mla
 
 // Few-row blocks go to the 128-key-tile kernel; 128-row blocks with a bf16
-// cache to the four-stage kernel (fp8 and 4 bits need room for raw stages it lacks).
+// cache to the four-stage kernel (fp8 needs room for raw stages it lacks); 4-bit caches have kernels of their own.
 int mla_launch_fwd(const mla::FwdParams& p, void* stream) {
-  if (p.key_tile == mla::kKeyTileSmall)
-    return p.kv_dtype == MLA_KV_FP4_E2M1 ? mla_launch_fwd_fp4_sm103(p, stream) : mla_launch_fwd_small_sm103(p, stream);
+  if (p.kv_dtype == MLA_KV_FP4_E2M1)
+    return p.key_tile == mla::kKeyTileSmall ? mla_launch_fwd_fp4_sm103(p, stream)
+                                            : mla_launch_fwd_fp4_wide_sm103(p, stream);
+  if (p.key_tile == mla::kKeyTileSmall) return mla_launch_fwd_small_sm103(p, stream);
   if (p.kv_dtype == MLA_KV_BF16) return mla_launch_fwd_pipe_sm103(p, stream);
   return mla_launch_fwd_sm103(p, stream);
 }

@@ -58,7 +58,6 @@
 #include <cstdint>
 
 #include "../../include/mla_decode.h"
-#include "fp4.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -69,7 +68,7 @@ constexpr int ATOM = T * 128;          // one 64-dim slab of a 16-bit stage: 64 
 constexpr int ATOM8 = T * 64;          // the same slab of raw fp8 codes: 64 keys x 64 B
 constexpr int SLOTS = 5;               // slabs per stage: 4 value + 1 rope (half of it used)
 constexpr int STAGE = SLOTS * ATOM;    // 40 KB of 16-bit operands (36 KB of it filled)
-constexpr int RAW_STAGE8 = SLOTS * ATOM8;  // 20 KB of fp8 codes
+constexpr int RAW_STAGE = SLOTS * ATOM8;  // 20 KB of fp8 codes
 constexpr int QROPE = 128 * 128;       // rope dims of Q, 128 rows x 128 B
 // Exchange with the partner CTA: each softmax warp sends and receives the
 // partial scores of its 16 rows x 64 keys per tile (1024 scores), each
@@ -91,11 +90,10 @@ constexpr int kThreads = 32 * 12;
 // raw stage of codes its loader warp copies into and converts from.  (A
 // fourth bf16 stage needs a 13th warp, which cuts the registers to 128 a
 // thread; measured, the 12-warp kernel with 3 stages is faster.)
-template <int kDtype>
+template <bool kFp8>
 struct Layout {
   static constexpr int NS = 3;              // operand stages = loader warps
-  static constexpr int NR = kDtype != MLA_KV_BF16 ? 3 : 0;  // raw stages of codes (one per loader warp)
-  static constexpr int RAW_STAGE = kDtype == MLA_KV_FP4_E2M1 ? T * fp4::kRawRow : RAW_STAGE8;
+  static constexpr int NR = kFp8 ? 3 : 0;   // raw fp8 stages (one per loader warp)
   static constexpr int OFF_STAGE = 0;
   static constexpr int OFF_RAW = OFF_STAGE + NS * STAGE;
   static constexpr int OFF_QROPE = OFF_RAW + NR * RAW_STAGE;
@@ -103,9 +101,8 @@ struct Layout {
   static constexpr int OFF_BAR = OFF_RECV + XCHG;
   static constexpr int SMEM_BYTES = OFF_BAR + 512 + 1024;  // + barriers + alignment slack
 };
-static_assert(Layout<MLA_KV_BF16>::SMEM_BYTES <= 232448, "bf16 smem");
-static_assert(Layout<MLA_KV_FP8_E4M3>::SMEM_BYTES <= 232448, "fp8 smem");
-static_assert(Layout<MLA_KV_FP4_E2M1>::SMEM_BYTES <= 232448, "4-bit smem");
+static_assert(Layout<false>::SMEM_BYTES <= 232448, "bf16 smem");
+static_assert(Layout<true>::SMEM_BYTES <= 232448, "fp8 smem");
 
 // TMEM columns
 constexpr uint32_t TM_O = 0;     // 256 fp32 columns: this CTA's value half
@@ -209,12 +206,7 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two_codes) {
 
 // fp32 bits + half a unit of the 24-bit value: the top three bytes are the
 // value rounded to 16 significant bits (half away from zero on the magnitude).
-template <bool kNaN = false>
-__device__ __forceinline__ uint32_t round_up_bits(float x) {
-  // The MMA's NaN, 0x7FFFFFFF, would carry into the sign and leave a zero.
-  if (kNaN) return (uint32_t)min((int)__float_as_uint(x), 0x7FFFFF7F) + 0x80u;
-  return __float_as_uint(x) + 0x80u;
-}
+__device__ __forceinline__ uint32_t round_up_bits(float x) { return __float_as_uint(x) + 0x80u; }
 
 // Four values -> three words (the upper three bytes of each).
 __device__ __forceinline__ void pack24(uint32_t A, uint32_t B, uint32_t C, uint32_t D, uint32_t* w) {
@@ -268,17 +260,14 @@ __device__ __forceinline__ uint64_t vmajor_desc(uint32_t addr) {
   return ptx::smem_desc(addr, ATOM, 1024, 2);
 }
 
-template <int kDtype>
+template <bool kFp8>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fwd_sm103_kernel(mla::FwdParams p) {
-  using L = Layout<kDtype>;
-  constexpr bool kFp8 = kDtype == MLA_KV_FP8_E4M3, kFp4 = kDtype == MLA_KV_FP4_E2M1;
-  constexpr bool kF16 = kFp8 || kFp4;  // codes that the loaders convert to f16 operands
-  constexpr int RAW_STAGE = L::RAW_STAGE;
+  using L = Layout<kFp8>;
   constexpr int NS = L::NS;
   constexpr int OFF_STAGE = L::OFF_STAGE, OFF_RAW = L::OFF_RAW, OFF_QROPE = L::OFF_QROPE;
   constexpr int OFF_RECV = L::OFF_RECV, OFF_BAR = L::OFF_BAR;
-  constexpr uint32_t kAB = kF16 ? 0u : 1u;  // operand type: f16 (fp8 and 4-bit caches) or bf16
+  constexpr uint32_t kAB = kFp8 ? 0u : 1u;  // operand type: f16 (fp8 cache) or bf16
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -331,7 +320,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   }
   const int n_tiles = k1 > k0 ? (k1 - k0 + T - 1) / T : 0;
   const int vdim0 = (int)rank * 256;  // this CTA's value dims
-  const float s_kv = (kF16 && p.kv_scale) ? *p.kv_scale : 1.f;
+  const float s_kv = (p.kv_dtype == MLA_KV_FP8_E4M3 && p.kv_scale) ? *p.kv_scale : 1.f;
 
   if (n_tiles == 0) {
     // No key of this split: the row results are out = 0, lse = -inf.  Both
@@ -389,16 +378,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (warp == kMmaWarp) {
     // --------------------------------------------------------------- MMA ---
-    // 4 bits: the whole warp walks the loop and one lane of it issues.  (In a branch
-    // that one lane takes alone an MMA costs about 64 cycles to issue, here what
-    // the tensor cores need: N = 64 from TMEM 32, N = 256 128.  Batch 64 x 128
-    // heads x 8192: 230 -> 215 us.)
-    const bool leader = kFp4 ? ptx::elect_one() : true;
-    auto all = [](bool x) { return kFp4 ? __all_sync(0xffffffffu, x) != 0 : x; };
-    if (kFp4 || lane == 0) {
+    if (lane == 0) {
       const uint32_t id_qk = ptx::idesc_f16(128, T, kAB, false, false);
       const uint32_t id_pv = ptx::idesc_f16(128, 256, kAB, false, true);
-      bool ok = all(wait(c, ptx::smem_u32(&bars.q_ready), 0));
+      bool ok = wait(c, ptx::smem_u32(&bars.q_ready), 0);
       ptx::tc_fence_after();
       // Operand descriptors from bases: the start address is the low field in
       // 16-byte units, so a stage, a slab or a 16-key step of V is an add (no
@@ -410,27 +393,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       auto issue_qk = [&](int u, int s) {  // tile u from stage s (u % NS)
         const uint32_t d = tmem + TM_S + (u & 1) * T;
         const uint64_t k0 = dk + s * kStageU;
-        if (!leader) return;
-#pragma unroll
         for (int a = 0; a < 4; ++a)
-#pragma unroll
           for (int kk = 0; kk < 4; ++kk)
             ptx::mma_ts(d, tmem + TM_Q + a * 32 + kk * 8, k0 + a * kAtomU + 2 * kk, id_qk,
                         (a | kk) != 0);
         // this CTA's 32 rope dims: 16-dim steps 2 rank, 2 rank + 1 of the rope slab
-#pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
-          ptx::mma_ss(d, dqr + 4 * rank + 2 * kk, k0 + 4 * kAtomU + 4 * rank + 2 * kk, id_qk, 1);
+        for (int kk = 2 * (int)rank; kk < 2 * (int)rank + 2; ++kk)
+          ptx::mma_ss(d, dqr + 2 * kk, k0 + 4 * kAtomU + 2 * kk, id_qk, 1);
         ptx::mma_commit(ptx::smem_u32(&bars.s_full[u & 1]));
       };
       auto issue_pv = [&](int t, int s, bool second) {  // tile t from stage s (t % NS)
         const uint32_t pa = tmem + TM_S + (t & 1) * T;
         const uint64_t v0 = dv + s * kStageU;
-        if (!leader) return;
-#pragma unroll
         for (int kk = 0; kk < T / 16; ++kk)
           ptx::mma_ts(tmem + TM_O, pa + kk * 8, v0 + kk * (2048 >> 4), id_pv, (t | kk) != 0);
-        if (!kF16 && second) {  // second-order weights (see the softmax)
+        if (!kFp8 && second) {  // second-order weights (see the softmax)
           for (int kk = 0; kk < T / 16; ++kk)
             ptx::mma_ts(tmem + TM_O, pa + 32 + kk * 8, v0 + kk * (2048 >> 4), id_pv, 1);
         }
@@ -451,7 +428,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       while (ok && np < n_tiles) {
         bool progress = false;
         if (nq < n_tiles && nq <= np + 1 &&
-            all(ptx::mbar_test_wait(ptx::smem_u32(&bars.kv_full[sq]), phq))) {
+            ptx::mbar_test_wait(ptx::smem_u32(&bars.kv_full[sq]), phq)) {
           ptx::tc_fence_after();
           issue_qk(nq++, sq);
           if (sq == NS - 1) {
@@ -462,7 +439,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           }
           progress = true;
         }
-        if (np < nq && all(ptx::mbar_test_wait(ptx::smem_u32(&bars.p_full[np & 1]), (np >> 1) & 1))) {
+        if (np < nq && ptx::mbar_test_wait(ptx::smem_u32(&bars.p_full[np & 1]), (np >> 1) & 1)) {
           ptx::tc_fence_after();
           const bool second = *reinterpret_cast<volatile uint64_t*>(&bars.heavy[np & 1]) != 0;
           issue_pv(np++, sp, second);
@@ -489,7 +466,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             *c.abort = 1;
             ok = false;
           }
-          ok = all(ok);
         }
       }
       (void)ok;
@@ -509,12 +485,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // and arrives on the stage's full barrier, while the other loader warps
     // have their tiles in flight.  Block-table entries for the warp's next
     // tile are read before it waits.
-    // 4 bits: a lane looks up and converts keys lane and lane + 32 of the tile;
-    // the copies go 128 bytes of codes (8 lanes), 64 of rope (4) and 16 of
-    // scales (1) a key.
-    constexpr int LPI = kFp4 ? 1 : kFp8 ? 4 : 8;  // lanes per piece
+    constexpr int LPI = kFp8 ? 4 : 8;        // lanes per piece
     constexpr int IPI = 32 / LPI;            // pieces per warp instruction
-    constexpr int NK = T / IPI;              // keys per lane: 16 (bf16), 8 (fp8) or 2 (4 bits)
+    constexpr int NK = T / IPI;              // keys per lane: 16 (bf16) or 8 (fp8)
     const int lw = warp;  // the operand stage this warp owns
     const int g = lane / LPI, sub = lane % LPI;
     constexpr int n_slots = SLOTS;
@@ -552,7 +525,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int t = lw; t < n_tiles; t += NS) {
       const int s = lw;
       const char* row[NK];
-      uint32_t rix[NK];  // 4 bits: the cache row's index (num_pages * page_size < 2^31)
       bool bad = false;
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
@@ -563,36 +535,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
         const uint32_t key = (uint32_t)key_of(t, i);
         const int64_t r = page * p.page_size + (int64_t)(key - page_of(key) * pdiv);
-        row[i] = cache + r * (kFp4 ? fp4::kRow : kFp8 ? mla::kDQK : mla::kDQK * 2);
-        rix[i] = (uint32_t)r;
+        row[i] = cache + r * (kFp8 ? mla::kDQK : mla::kDQK * 2);
       }
       if (bad) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);
       load_pages(t + NS);
-      if constexpr (!kF16) {
+      if constexpr (!kFp8) {
         if (t >= NS && !wait_all(c, ptx::smem_u32(&bars.kv_empty[s]), ((t / NS) - 1) & 1))
           break;
       }
-      const uint32_t dst = sbase + (kF16 ? OFF_RAW + lw * RAW_STAGE : OFF_STAGE + s * STAGE);
-      if constexpr (kFp4) {
-        __syncwarp();  // every lane has converted the codes that these replace
-#pragma unroll
-        for (int i = 0; i < T / 4; ++i) {
-          const int kk = 4 * i + (lane >> 3), ch = lane & 7;
-          const char* src = cache + (size_t)__shfl_sync(0xffffffffu, rix[i / 8], kk & 31) * fp4::kRow;
-          ptx::cp_async_16(dst + kk * fp4::kRawRow + ch * 16, src + 128 * (int)rank + ch * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < T / 8; ++i) {
-          const int kk = 8 * i + (lane >> 2), ch = lane & 3;
-          const char* src = cache + (size_t)__shfl_sync(0xffffffffu, rix[i / 4], kk & 31) * fp4::kRow;
-          ptx::cp_async_16(dst + kk * fp4::kRawRow + fp4::kRawRope + ch * 16,
-                           src + fp4::kRope + 64 * (int)rank + ch * 16);
-        }
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-          ptx::cp_async_16(dst + (32 * i + lane) * fp4::kRawRow + fp4::kRawScales,
-                           row[i] + fp4::kScales + 16 * (int)rank);
-      } else
+      const uint32_t dst = sbase + (kFp8 ? OFF_RAW + lw * RAW_STAGE : OFF_STAGE + s * STAGE);
       for (int sl = 0; sl < n_slots; ++sl) {
         if (sl == 4 && !rope_lane) continue;
         const int dim = sl < 4 ? vdim0 + sl * 64 : 512;
@@ -634,31 +585,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             st_shared_u4(rowp + (((2 * sub) ^ (kk & 7)) * 16), lo);
             st_shared_u4(rowp + (((2 * sub + 1) ^ (kk & 7)) * 16), hi);
           }
-        }
-      }
-      if constexpr (kFp4) {
-        __syncwarp();  // the other lanes' copies
-        if (t >= NS && !wait_all(c, ptx::smem_u32(&bars.kv_empty[s]), ((t / NS) - 1) & 1))
-          break;
-        const uint32_t out = sbase + OFF_STAGE + s * STAGE;
-#pragma unroll 1
-        for (int i = 0; i < 2; ++i) {
-          const int kk = 32 * i + lane;
-          const uint32_t raw = dst + kk * fp4::kRawRow, rowp = out + kk * 128;
-          const uint4 scales = ld_shared_u4(raw + fp4::kRawScales);
-          const uint32_t sc[4] = {scales.x, scales.y, scales.z, scales.w};
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            uint4 v[4];
-            fp4::convert(ld_shared_u4(raw + j * 16), sc[j >> 1] >> (16 * (j & 1)), v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              st_shared_u4(rowp + (j >> 1) * ATOM + (((4 * (j & 1) + e) ^ (kk & 7)) * 16), v[e]);
-          }
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            st_shared_u4(rowp + 4 * ATOM + (((4 * (int)rank + e) ^ (kk & 7)) * 16),
-                         ld_shared_u4(raw + fp4::kRawRope + e * 16));
         }
       }
       ptx::fence_proxy_async_smem();
@@ -707,7 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           uint4 x = valid_row ? qv[(vdim0 + chunk * 64) / 8 + v] : make_uint4(0, 0, 0, 0);
-          if (kF16) x = bf16x8_to_f16x8(x, q_range);
+          if (kFp8) x = bf16x8_to_f16x8(x, q_range);
           buf[v * 4 + 0] = x.x;
           buf[v * 4 + 1] = x.y;
           buf[v * 4 + 2] = x.z;
@@ -720,12 +646,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int v = 0; v < 8; ++v) {
           uint4 x = valid_row ? qv[512 / 8 + v] : make_uint4(0, 0, 0, 0);
-          if (kF16) x = bf16x8_to_f16x8(x, q_range);
+          if (kFp8) x = bf16x8_to_f16x8(x, q_range);
           *reinterpret_cast<uint4*>(qr + ((v ^ (r & 7)) * 16)) = x;
         }
         ptx::fence_proxy_async_smem();
       }
-      if (kF16 && q_range) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
+      if (kFp8 && q_range) atomicOr(p.status, MLA_DEVFLAG_Q_RANGE);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
       ptx::mbar_arrive(ptx::smem_u32(&bars.q_ready));
@@ -749,7 +675,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int buf = t & 1;
       if (!wait_all(c, ptx::smem_u32(&bars.s_full[buf]), (t >> 1) & 1)) { ok = false; break; }
       if (!live) {
-        if (!kF16 && lane == 0) reinterpret_cast<volatile uint8_t*>(&bars.heavy[buf])[sw] = 0;
+        if (!kFp8 && lane == 0) reinterpret_cast<volatile uint8_t*>(&bars.heavy[buf])[sw] = 0;
         ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
         continue;
       }
@@ -778,8 +704,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           uint32_t w[12];
 #pragma unroll
           for (int k = 0; k < 4; ++k)  // rounded to 24 bits: the top 3 bytes of x + 0x80
-            pack24(round_up_bits<kFp4>(s[16 * qd + 4 * k]), round_up_bits<kFp4>(s[16 * qd + 4 * k + 1]),
-                   round_up_bits<kFp4>(s[16 * qd + 4 * k + 2]), round_up_bits<kFp4>(s[16 * qd + 4 * k + 3]),
+            pack24(round_up_bits(s[16 * qd + 4 * k]), round_up_bits(s[16 * qd + 4 * k + 1]),
+                   round_up_bits(s[16 * qd + 4 * k + 2]), round_up_bits(s[16 * qd + 4 * k + 3]),
                    w + 3 * k);
 #pragma unroll
           for (int v = 0; v < 3; ++v)
@@ -913,9 +839,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          pk[2 * j] = kF16 ? pack_f16(s[4 * j], s[4 * j + 1]) : pack_bf16(s[4 * j], s[4 * j + 1]);
+          pk[2 * j] = kFp8 ? pack_f16(s[4 * j], s[4 * j + 1]) : pack_bf16(s[4 * j], s[4 * j + 1]);
           pk[2 * j + 1] =
-              kF16 ? pack_f16(s[4 * j + 2], s[4 * j + 3]) : pack_bf16(s[4 * j + 2], s[4 * j + 3]);
+              kFp8 ? pack_f16(s[4 * j + 2], s[4 * j + 3]) : pack_bf16(s[4 * j + 2], s[4 * j + 3]);
         }
         lA += sA;
         lB += sB;
@@ -924,7 +850,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // holds pairs 4j + i%4, which is where the 16x128b shape writes.
       const uint32_t pcol = tmem + lanes16 + TM_S + buf * T;
       ptx::tmem_st16x128b_x8(pcol, pk);
-      if constexpr (!kF16) {
+      if constexpr (!kFp8) {
         // bf16 keeps 8 significant bits.  Where one key carries a sizeable
         // share of a row's weight (more than 1/16 of the row sum so far), the
         // rounding would show in O, so the warp's rows also get a second bf16
@@ -972,9 +898,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // parity wait on o_done only tells the current phase from the one
       // before it, and o_done may be one phase short or already complete).
       ptx::tc_fence_after();
-      // 4 bits: a sum that is NaN is no empty row
-      const bool someA = kFp4 ? !(lA <= 0.f) : lA > 0.f, someB = kFp4 ? !(lB <= 0.f) : lB > 0.f;
-      const float invA = someA ? s_kv / lA : 0.f, invB = someB ? s_kv / lB : 0.f;
+      const float invA = lA > 0.f ? s_kv / lA : 0.f, invB = lB > 0.f ? s_kv / lB : 0.f;
       const int rowA = rb * mla::kRowTile + rA, rowB = rb * mla::kRowTile + rB;
       const bool okA = rowA < p.rows, okB = rowB < p.rows;
       const size_t pA = part * p.rows + rowA;
@@ -999,8 +923,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       if (rank == 0 && cq == 0) {
-        const float lseA = someA ? (mA + log2f(lA)) * 0.6931471805599453f : -INFINITY;
-        const float lseB = someB ? (mB + log2f(lB)) * 0.6931471805599453f : -INFINITY;
+        const float lseA = lA > 0.f ? (mA + log2f(lA)) * 0.6931471805599453f : -INFINITY;
+        const float lseB = lB > 0.f ? (mB + log2f(lB)) * 0.6931471805599453f : -INFINITY;
         if (single) {
           if (okA) p.lse[(size_t)b * p.rows + rowA] = lseA;
           if (okB) p.lse[(size_t)b * p.rows + rowB] = lseB;
@@ -1018,7 +942,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   if (warp == kMmaWarp) {
     if (bars.abort) {
       // wait for every tcgen05 op this CTA issued before giving TMEM back
-      if (kFp4 ? ptx::elect_one() : lane == 0) {
+      if (lane == 0) {
         ptx::mma_commit(ptx::smem_u32(&bars.drain));
         wait_drain(ptx::smem_u32(&bars.drain), 0);
       }
@@ -1033,21 +957,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }  // namespace
 
 int mla_launch_fwd_sm103(const mla::FwdParams& p, void* stream) {
-  auto kernel = fwd_sm103_kernel<MLA_KV_BF16>;
-  int smem = Layout<MLA_KV_BF16>::SMEM_BYTES, slot = 0;
-  if (p.kv_dtype == MLA_KV_FP8_E4M3) {
-    kernel = fwd_sm103_kernel<MLA_KV_FP8_E4M3>;
-    smem = Layout<MLA_KV_FP8_E4M3>::SMEM_BYTES;
-    slot = 1;
-  } else if (p.kv_dtype == MLA_KV_FP4_E2M1) {
-    kernel = fwd_sm103_kernel<MLA_KV_FP4_E2M1>;
-    smem = Layout<MLA_KV_FP4_E2M1>::SMEM_BYTES;
-    slot = 12;
-  }
+  const bool fp8 = p.kv_dtype == MLA_KV_FP8_E4M3;
+  auto kernel = fp8 ? fwd_sm103_kernel<true> : fwd_sm103_kernel<false>;
+  const int smem = fp8 ? Layout<true>::SMEM_BYTES : Layout<false>::SMEM_BYTES;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return (int)e;
-  e = mla::opt_in_smem(reinterpret_cast<const void*>(kernel), smem, dev, slot);
+  e = mla::opt_in_smem(reinterpret_cast<const void*>(kernel), smem, dev, fp8 ? 1 : 0);
   if (e != cudaSuccess) return (int)e;
   // Splits vary slowest, so every sequence's first chunk is dispatched
   // before any second chunk (the planner simulates this order).  Launched as

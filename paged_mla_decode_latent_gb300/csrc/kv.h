@@ -18,3 +18,4 @@ constexpr int kFewRowsFp4 = 32;
 }  // namespace mla
 
 int mla_launch_fwd_fp4_sm103(const mla::FwdParams& p, void* stream);
+int mla_launch_fwd_fp4_wide_sm103(const mla::FwdParams& p, void* stream);
