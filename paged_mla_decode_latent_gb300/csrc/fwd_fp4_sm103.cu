@@ -22,14 +22,23 @@
 // scores of the tile before are done, V (512 dims) to a short ring in shared
 // memory as soon as the MMAs have read what was there.  The codes wait in
 // shared memory for both.  Per 128-key tile, all at once:
-//   copy warps (3) the rows of later tiles, 16-byte cp.async, 32 keys (a part)
+//   copy warps (2) the rows of later tiles, 16-byte cp.async, 32 keys (a part)
 //                  at a time into a ring
 //   K warps (4)    part q of the tile: codes to f16, into TMEM lanes 32 q ...
-//   MMA warp       S as soon as K is there; O^T += V^T P 32 keys at a time
+//   QK warp        S as soon as K is there
 //   softmax warps  a key a thread, all N rows: weights relative to a running
 //   (4)            maximum that is raised (and O rescaled) only when a weight
 //                  would pass 2^8, as one vote of the four warps decides
-//   V warps (4)    128 dims each: codes to f16, 32 keys at a time
+//   V warps (8)    two groups that take turns, a part each; 128 dims a warp
+//   PV warp        O^T += V^T P, 32 keys at a time
+//
+// What bounds it: the chain of these handoffs and conversions, not one unit.  A
+// tile takes about 4500 cycles an SM, of which its shared-memory traffic (codes in
+// and out twice, V in and out, the MMAs' operands) needs 3300, issue slots half and
+// DRAM 40 %.  Batch 8 x 16 heads x 109440 keys: 107 us (3.4 TB/s of 6.7); batch 64 x
+// 32 heads x 8192: 102 us.  With eight K warps (24 warps at 80 registers) 106 and
+// 105 us, with one group of V warps (16 warps at 128) 117 and 100 us.  With waits
+// that poll in place of the suspended ones 109 (the MMA warps only) to 119 us (all).
 //
 // Everything is exact up to the weights: f16 holds a code times its scale, and Q
 // where it is within f16 (else MLA_DEVFLAG_Q_RANGE); scores and outputs are
@@ -61,11 +70,11 @@ constexpr int kVUnit = 8 * kVSlab;        // a part's V: 32 KB
 constexpr int kQSlabs = 9;
 
 // Warps.  Those that work on TMEM lanes 32 q ... are warps q modulo 4.
-constexpr int kVWarp0 = 8, kSoftmaxWarp0 = 16, kQkWarp = 20, kPvWarp = 21, kCopyWarp0 = 22, kCopyWarps = 2;
-constexpr int kThreads = 24 * 32;
-// Registers a thread of each group of four warps; the launch gives 80 each.
-constexpr int kLaunchRegs = 80, kKRegs = 72, kVRegs = 64, kSoftmaxRegs = 136, kOtherRegs = 72;
-static_assert(2 * kKRegs + 2 * kVRegs + kSoftmaxRegs + kOtherRegs <= 6 * kLaunchRegs, "no more than the launch gives");
+constexpr int kVWarp0 = 4, kSoftmaxWarp0 = 12, kQkWarp = 16, kPvWarp = 17, kCopyWarp0 = 18, kCopyWarps = 2;
+constexpr int kThreads = 20 * 32;
+// Registers a thread of each group of four warps; the launch gives 96 each.
+constexpr int kLaunchRegs = 96, kKRegs = 96, kVRegs = 72, kSoftmaxRegs = 160, kOtherRegs = 80;
+static_assert(kKRegs + 2 * kVRegs + kSoftmaxRegs + kOtherRegs <= 5 * kLaunchRegs, "no more than the launch gives");
 
 template <int N>
 struct Layout {
@@ -95,11 +104,11 @@ constexpr uint32_t kSleepNs = 20000;
 
 struct Bars {
   uint64_t raw_full[10];   // a part has landed (32 lanes of a copy warp)
-  uint64_t raw_empty[10];  // its two K warps and four V warps have read it
+  uint64_t raw_empty[10];  // its K warp and four V warps have read it
   uint64_t v_full[2], v_empty[2];
-  uint64_t k_full[2];      // K of a tile is in TMEM (256 threads)
+  uint64_t k_full[2];      // K of a tile is in TMEM (four warps)
   uint64_t s_full[2];      // scores done, and K read
-  uint64_t p_full[2];      // weights written, and scores read (128 threads)
+  uint64_t p_full[2];      // weights written, and scores read (four warps)
   uint64_t p_done[2];      // the tile's values are summed
   uint64_t q_ready;
   uint64_t drain[2];
@@ -299,16 +308,16 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
   if (threadIdx.x == 0) {
     for (int i = 0; i < R; ++i) {
       ptx::mbar_init(ptx::smem_u32(&bars.raw_full[i]), 32);
-      ptx::mbar_init(ptx::smem_u32(&bars.raw_empty[i]), 6);
+      ptx::mbar_init(ptx::smem_u32(&bars.raw_empty[i]), 5);
     }
     for (int i = 0; i < L::kVUnits; ++i) {
       ptx::mbar_init(ptx::smem_u32(&bars.v_full[i]), 4);
       ptx::mbar_init(ptx::smem_u32(&bars.v_empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
-      ptx::mbar_init(ptx::smem_u32(&bars.k_full[i]), 256);
+      ptx::mbar_init(ptx::smem_u32(&bars.k_full[i]), 4);
       ptx::mbar_init(ptx::smem_u32(&bars.s_full[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bars.p_full[i]), 128);
+      ptx::mbar_init(ptx::smem_u32(&bars.p_full[i]), 4);
       ptx::mbar_init(ptx::smem_u32(&bars.p_done[i]), 1);
     }
     ptx::mbar_init(ptx::smem_u32(&bars.q_ready), 128);
@@ -331,13 +340,13 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
   if (warp < kVWarp0) {
     take_registers<kKRegs>();
     // ----------------------------------------------------------------- K ---
-    // Warps q and q + 4: part q of every tile, a key a lane; even and odd slabs of 64 dims.
-    const int q = warp & 3, h = warp >> 2;
+    // Warp q: part q of every tile, a key a lane, in slabs of 64 dims.
+    const int q = warp;
     const uint32_t kcol = tmem + ((uint32_t)(32 * q) << 16) + L::TM_K;
     Ring<R> ring;
     ring.next(q);
     int first = 0;  // the tile's first slab in the ring of slabs
-    constexpr int kEarly = (L::kKSlabs - 9) & ~1;  // slabs before it (a pair each) take the place of tile t - 2's
+    constexpr int kEarly = L::kKSlabs - 9;  // slabs before it take the place of tile t - 2's, the others tile t - 1's
     for (int t = 0; t < n_tiles; ++t, ring.next(4)) {
       auto column = [&](int a) {
         const int at = first + a;
@@ -346,14 +355,11 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
       if (!wait_all(c, ptx::smem_u32(&bars.raw_full[ring.slot]), ring.phase)) break;
       const uint32_t raw = sbase + L::OFF_RAW + ring.slot * kPart + lane * kRaw;
       const uint4 s0 = ld_shared_u4(raw + fp4::kScales), s1 = ld_shared_u4(raw + fp4::kScales + 16);
-      const uint32_t sc[4] = {h ? s0.y : s0.x, h ? s0.w : s0.z, h ? s1.y : s1.x, h ? s1.w : s1.z};
-      // The first slabs take the place of those of tile t - 2, the others that of
-      // tile t - 1's, whose scores must be done.
+      const uint32_t sc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
       bool ok = true;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int a = 2 * i + h;
-        if (2 * i == kEarly) {
+      for (int a = 0; a < 8; ++a) {
+        if (a == kEarly) {
           ok = t < 1 || wait_all(c, ptx::smem_u32(&bars.s_full[(t - 1) & 1]), ((t - 1) >> 1) & 1);
           if (!ok) break;
           ptx::tc_fence_after();
@@ -362,13 +368,14 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
         for (int e = 0; e < 2; ++e) {  // 32 dims
           uint4 v[4];
           uint32_t r[16];
-          fp4::convert(ld_shared_u4(raw + 32 * a + 16 * e), sc[i] >> (16 * e), v);
+          fp4::convert(ld_shared_u4(raw + 32 * a + 16 * e), sc[a] >> (16 * e), v);
           words(v, r);
           tmem_st16(column(a) + 16 * e, r);
         }
       }
       if (!ok) break;
-      {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
         uint4 v[4];
         uint32_t r[16];
 #pragma unroll
@@ -380,7 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
       if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars.raw_empty[ring.slot]));
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bars.k_full[t & 1]));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars.k_full[t & 1]));
       first += 9;
       if (first >= L::kKSlabs) first -= L::kKSlabs;
     }
@@ -575,7 +583,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
       }
       ptx::fence_proxy_async_smem();
       ptx::tc_fence_before();
-      if (ok) ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
+      __syncwarp();
+      if (ok && lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
     }
 
     // ---------------------------------------------------------- epilogue ---

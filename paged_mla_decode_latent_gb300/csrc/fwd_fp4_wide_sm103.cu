@@ -10,18 +10,24 @@
 //   * The MMA warp walks its loop as a whole and one elected lane issues.  In a
 //     branch that one lane takes alone an MMA costs about 64 cycles to issue,
 //     here what the tensor cores need (N = 64 with A from TMEM: 32, N = 256: 128).
-//   * The swap of partial scores is taken off the softmax warps' path: they send
-//     those of two tiles before they finish the first of them, so that a block is
-//     on its way (about 1000 cycles) while they work on another.  That takes a
-//     second receive buffer (24 KB), which fits because a 4-bit tile's codes are
-//     13 KB, and because the rope half of a key is kept in 64-byte rows (a stage
-//     of 36 KB instead of 40).
+//   * The swap of partial scores goes through two receive buffers (24 KB each), and
+//     a tile's own scores stay in registers while the partner's block travels
+//     (about 1000 cycles), instead of being read from TMEM again.  The second buffer
+//     fits because a 4-bit tile's codes are 13 KB, and because the rope half of a
+//     key is kept in 64-byte rows (a stage of 36 KB instead of 40).
 //
-// Batch 64 x 128 heads x 8192, one call after another in a graph: 230 us as a form
-// of the 128-row kernel, 215 with the MMAs issued from a converged warp.
+// What bounds it: the softmax warps' path from scores to weights, in which the swap
+// is the largest part; a tile takes 2800 cycles, its MMAs 1120.  Batch 64 x 128 heads
+// x 8192: 187 us, 40 % of what cuBLAS reaches in bf16 (batch 8 x 65536: 174 us).
+// As a form of the 128-row kernel 230 us;
+// MMAs issued from a converged warp 215; two warps a stage that convert instead of
+// one, the two buffers and the scores kept 193; an arrival a warp instead of one a
+// thread, and no sleep in the MMA warp's loop, 187.  Blocks sent for a pair of tiles
+// at a time took 233 us, the next tile's block sent early where its scores were
+// ready 201, sixteen softmax warps 210.
 //
 // Per 64-key tile, in each CTA:
-//   loader warps  : three, one for each operand stage: 16-byte cp.async of the
+//   loader warps  : six, two for each operand stage: 16-byte cp.async of the
 //                   tile's codes, scales and rope dims into the warp's raw stage,
 //                   then f16 into the operand stage once the value MMAs have read
 //                   what was there.
@@ -93,7 +99,7 @@ constexpr uint64_t kDrainNs = 500000000ull;  // bound of the wind-down waits aft
 constexpr uint32_t kSleepNs = 20000;  // suspend-time hint of a waiting thread
 
 struct Bars {
-  uint64_t kv_full[NS];   // operand stage ready (the 64 threads of its loader warps arrive)
+  uint64_t kv_full[NS];   // operand stage ready (its two loader warps arrive)
   uint64_t kv_empty[NS];  // operand stage consumed by the MMAs
   uint64_t s_full[2];
   uint64_t p_full[2];
@@ -318,12 +324,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < NS; ++s) {
-      ptx::mbar_init(ptx::smem_u32(&bars.kv_full[s]), 64);
+      ptx::mbar_init(ptx::smem_u32(&bars.kv_full[s]), 2);
       ptx::mbar_init(ptx::smem_u32(&bars.kv_empty[s]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       ptx::mbar_init(ptx::smem_u32(&bars.s_full[i]), 1);
-      ptx::mbar_init(ptx::smem_u32(&bars.p_full[i]), 32 * kSoftmaxWarps);
+      ptx::mbar_init(ptx::smem_u32(&bars.p_full[i]), kSoftmaxWarps);
     }
     for (int i = 0; i < 2; ++i)
       for (int w = 0; w < kSoftmaxWarps; ++w) {
@@ -435,7 +441,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int e = 0; e < 4; ++e)
         st_shared_u4(out + 4 * ATOM + sw64(kk, e), ld_shared_u4(raw + fp4::kRawRope + e * 16));
       ptx::fence_proxy_async_smem();
-      ptx::mbar_arrive(ptx::smem_u32(&bars.kv_full[lw]));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars.kv_full[lw]));
     }
     ptx::cp_async_wait<0>();  // nothing of this warp is in flight when it leaves
   };
@@ -515,11 +522,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         t_last = 0;
         continue;
       }
-      // Nothing ready: no spinning on the issue slots that the softmax and loader
-      // warps of this sub-partition need.
-      if (nq < n_tiles && nq <= np + 1) __nanosleep(32);
-      else (void)ptx::mbar_try_wait(ptx::smem_u32(&bars.p_full[np & 1]), (np >> 1) & 1);
-      if ((++idle & 15) == 0) {
+      if ((++idle & 63) == 0) {
         const uint64_t now = ptx::globaltimer_ns();
         if (t_last == 0) t_last = now;
         if (*c.abort) {
@@ -627,7 +630,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int buf = t & 1;
       if (!wait_all(c, ptx::smem_u32(&bars.s_full[buf]), (t >> 1) & 1)) { ok = false; break; }
       if (!live) {
-        ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
+        if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
         continue;
       }
       ptx::tc_fence_after();
@@ -795,7 +798,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       ptx::tmem_st16x128b_x8(pcol, pk);
       ptx::tmem_st_wait();
       ptx::tc_fence_before();
-      ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
+      __syncwarp();
+      if (lane == 0) ptx::mbar_arrive(ptx::smem_u32(&bars.p_full[buf]));
     }
 
     // ---------------------------------------------------------- epilogue ---

@@ -12,7 +12,7 @@ inline bool kv_dtype_known(int d) {
 
 // Up to so many score rows a sequence a 4-bit cache has a kernel of its own, whose
 // work units are single CTAs.  (In blocks of 32 it takes 64 rows in the time of the
-// 128-row kernel, 187 against 182 us at batch 64 x 8192, and more rows longer.)
+// kernel for more rows, 187 against 180 us at batch 64 x 8192, and 128 twice that.)
 constexpr int kFewRowsFp4 = 32;
 
 }  // namespace mla
