@@ -4,27 +4,23 @@
 // The division of the work is the 128-row kernel's (fwd_sm103.cu): CTA r of the
 // pair owns value dims [256 r, 256 r + 256), contracts those and rope dims [32 r,
 // 32 r + 32) for the scores, and the two add up each other's partial scores, which
-// travel as 24-bit values over distributed shared memory.  Three things differ.
+// travel over distributed shared memory.  Three things differ.
 //
 //   * The loaders convert 4-bit rows to f16 operands (fp4.cuh), a key a lane.
 //   * The MMA warp walks its loop as a whole and one elected lane issues.  In a
 //     branch that one lane takes alone an MMA costs about 64 cycles to issue,
 //     here what the tensor cores need (N = 64 with A from TMEM: 32, N = 256: 128).
-//   * The swap of partial scores goes through two receive buffers (24 KB each), and
-//     a tile's own scores stay in registers while the partner's block travels
-//     (about 1000 cycles), instead of being read from TMEM again.  The second buffer
-//     fits because a 4-bit tile's codes are 13 KB, and because the rope half of a
-//     key is kept in 64-byte rows (a stage of 36 KB instead of 40).
+//   * The swap of partial scores goes through two receive buffers (32 KB each), in
+//     fp32, and a tile's own scores stay in registers while the partner's block
+//     travels, instead of being read from TMEM again.  The buffers fit because a
+//     4-bit tile's codes are 13 KB, and because the rope half of a key is kept in
+//     64-byte rows (a stage of 36 KB instead of 40).
 //
-// What bounds it: the softmax warps' path from scores to weights, in which the swap
-// is the largest part; a tile takes 2800 cycles, its MMAs 1120.  Batch 64 x 128 heads
-// x 8192: 187 us, 40 % of what cuBLAS reaches in bf16 (batch 8 x 65536: 174 us).
-// As a form of the 128-row kernel 230 us;
-// MMAs issued from a converged warp 215; two warps a stage that convert instead of
-// one, the two buffers and the scores kept 193; an arrival a warp instead of one a
-// thread, and no sleep in the MMA warp's loop, 187.  Blocks sent for a pair of tiles
-// at a time took 233 us, the next tile's block sent early where its scores were
-// ready 201, sixteen softmax warps 210.
+// What bounds it: distributed shared memory, of which a pair swaps 32 KB each way a
+// tile (1.15 of the tile's 1.5 us).  Batch 64 x 128 heads x 8192: 197 us, 38 % of what
+// cuBLAS reaches in bf16; x 64 heads: 174 us.  With the scores rounded to 24 bits for
+// the swap 187 and 180 us, but the log-sum-exp then loses four bits to a plain form
+// in fp32.
 //
 // Per 64-key tile, in each CTA:
 //   loader warps  : six, two for each operand stage: 16-byte cp.async of the
@@ -61,12 +57,11 @@ constexpr int NS = 3;                     // operand stages = loader warps
 constexpr int RAW_PART = 32 * fp4::kRawRow;  // a loader's 6.5 KB of codes, scales and rope
 constexpr int QROPE = 128 * 64;           // the CTA's 32 rope dims of Q, 64-byte rows
 // Exchange with the partner CTA: each softmax warp sends and receives the partial
-// scores of its 16 rows x 64 keys per tile (1024 scores), each rounded to 24 bits
-// (16 significant bits) and packed four to three words; a buffer for even tiles
-// and one for odd ones.
+// scores of its 16 rows x 64 keys per tile; a buffer for even tiles and one for odd
+// ones.
 constexpr int kSoftmaxWarps = 8;
-constexpr int RECV_W = 32 * 32 * 3;               // one warp's block (3 KB)
-constexpr int RECV = kSoftmaxWarps * RECV_W;      // one tile (24 KB)
+constexpr int RECV_W = 32 * 32 * 4;               // one warp's block (4 KB)
+constexpr int RECV = kSoftmaxWarps * RECV_W;      // one tile (32 KB)
 // Warps: 0..5 loaders (warps 2 w and 2 w + 1 fill operand stage w, 32 keys each), 6
 // MMA, 7 without work, 8..15 softmax.
 constexpr int kLoaders = 2 * NS;
@@ -103,7 +98,7 @@ struct Bars {
   uint64_t kv_empty[NS];  // operand stage consumed by the MMAs
   uint64_t s_full[2];
   uint64_t p_full[2];
-  uint64_t recv_full[2][kSoftmaxWarps];  // the partner warp's partial scores landed (3 KB)
+  uint64_t recv_full[2][kSoftmaxWarps];  // the partner warp's partial scores landed (4 KB)
   uint64_t recv_free[2][kSoftmaxWarps];  // the partner warp has read what this warp sent
   uint64_t o_done;
   uint64_t o_final;  // the last PV has drained (one phase)
@@ -176,27 +171,6 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   __half2 v = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&v);
-}
-
-// fp32 bits + half a unit of the 24-bit value: the top three bytes are the
-// value rounded to 16 significant bits (half away from zero on the magnitude).
-// (The MMA's NaN, 0x7FFFFFFF, would carry into the sign and leave a zero.)
-__device__ __forceinline__ uint32_t round_up_bits(float x) {
-  return (uint32_t)min((int)__float_as_uint(x), 0x7FFFFF7F) + 0x80u;
-}
-
-// Four values -> three words (the upper three bytes of each).
-__device__ __forceinline__ void pack24(uint32_t A, uint32_t B, uint32_t C, uint32_t D, uint32_t* w) {
-  w[0] = __byte_perm(A, B, 0x5321);
-  w[1] = __byte_perm(B, C, 0x6532);
-  w[2] = __byte_perm(C, D, 0x7653);
-}
-
-__device__ __forceinline__ void unpack24(const uint32_t* w, float* u) {
-  u[0] = __uint_as_float(__byte_perm(w[0], 0u, 0x2104));
-  u[1] = __uint_as_float(__byte_perm(w[0], w[1], 0x5430) & 0xFFFFFF00u);
-  u[2] = __uint_as_float(__byte_perm(w[1], w[2], 0x4320) & 0xFFFFFF00u);
-  u[3] = __uint_as_float(w[2] & 0xFFFFFF00u);
 }
 
 // This warp group's share of the launch's registers from here on.
@@ -646,18 +620,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t dst = peer_recv0 + buf * RECV + lane * 16;
         const uint32_t bar = peer_full0 + buf * (8 * kSoftmaxWarps);
 #pragma unroll
-        for (int qd = 0; qd < 2; ++qd) {  // 16 scores -> 12 words -> 3 stores
-          uint32_t w[12];
-#pragma unroll
-          for (int k = 0; k < 4; ++k)  // rounded to 24 bits: the top 3 bytes of x + 0x80
-            pack24(round_up_bits(s[16 * qd + 4 * k]), round_up_bits(s[16 * qd + 4 * k + 1]),
-                   round_up_bits(s[16 * qd + 4 * k + 2]), round_up_bits(s[16 * qd + 4 * k + 3]),
-                   w + 3 * k);
-#pragma unroll
-          for (int v = 0; v < 3; ++v)
-            ptx::st_async_u4(dst + (3 * qd + v) * 512, w[4 * v], w[4 * v + 1], w[4 * v + 2],
-                             w[4 * v + 3], bar);
-        }
+        for (int v = 0; v < 8; ++v)
+          ptx::st_async_u4(dst + v * 512, __float_as_uint(s[4 * v]), __float_as_uint(s[4 * v + 1]),
+                           __float_as_uint(s[4 * v + 2]), __float_as_uint(s[4 * v + 3]), bar);
       }
       {
         const uint32_t full = ptx::smem_u32(&bars.recv_full[buf][sw]);
@@ -666,24 +631,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t src = my_recv(buf) + lane * 16;
         uint32_t fold = 0;
 #pragma unroll
-        for (int qd = 0; qd < 2; ++qd) {
-          uint32_t w[12];
-#pragma unroll
-          for (int v = 0; v < 3; ++v) {
-            const uint4 x = ld_shared_u4(src + (3 * qd + v) * 512);
-            w[4 * v] = x.x;
-            w[4 * v + 1] = x.y;
-            w[4 * v + 2] = x.z;
-            w[4 * v + 3] = x.w;
-            fold ^= x.x ^ x.y ^ x.z ^ x.w;
-          }
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            float u[4];
-            unpack24(w + 3 * k, u);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[16 * qd + 4 * k + e] += u[e];
-          }
+        for (int v = 0; v < 8; ++v) {
+          const uint4 x = ld_shared_u4(src + v * 512);
+          fold ^= x.x ^ x.y ^ x.z ^ x.w;
+          s[4 * v] += __uint_as_float(x.x);
+          s[4 * v + 1] += __uint_as_float(x.y);
+          s[4 * v + 2] += __uint_as_float(x.z);
+          s[4 * v + 3] += __uint_as_float(x.w);
         }
         // The buffer is read (the vote needs every lane's loaded words): the
         // partner may send the tile after next.
