@@ -142,12 +142,14 @@ typedef struct mla_decode_plan_t {
   int32_t row_blocks;   /* ceil(rows / row_tile) */
   int32_t max_ctx;      /* longest context the plan covers */
   int32_t key_tile;     /* keys per pipeline tile: 128 when rows <= 64 (bf16), <= 16 (fp8)
-                           or <= 32 (4 bits), the few-row kernels; 64 otherwise */
+                           or <= 32 (4 bits), the few-row kernels; 64 otherwise (also for
+                           4 bits, whose kernel then takes 256 keys at a time) */
   int32_t chunk_len;    /* keys per split, a multiple of key_tile */
   int32_t num_splits;   /* splits per sequence = ceil(max_ctx / chunk_len) */
   int32_t num_sms;      /* SM count the partition was balanced for */
-  int32_t cluster_size; /* CTAs cooperating on one (b, row block, split) */
-  int32_t grid_x, grid_y, grid_z; /* launch grid of mla_decode_fwd: (2 x row_blocks, batch,
+  int32_t cluster_size; /* CTAs cooperating on one (b, row block, split): 2, or 1 for the
+                           few-row kernel of a 4-bit cache */
+  int32_t grid_x, grid_y, grid_z; /* launch grid of mla_decode_fwd: (cluster_size x row_blocks, batch,
                                      num_splits); splits vary slowest */
   int32_t wait_limit_us; /* bound of every device-side wait, in microseconds; 0 (what
                             mla_decode_plan writes) means 2 s.  The one field a caller

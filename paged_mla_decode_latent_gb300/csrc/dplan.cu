@@ -265,7 +265,7 @@ extern "C" int mla_decode_plan_device(const mla_decode_dplan_t* dplan, const int
   a.page_size = dplan->page_size;
   a.ctx_capacity = dplan->ctx_capacity;
   a.max_units = dplan->max_units;
-  a.tile_keys = dplan->key_tile;
+  a.tile_keys = mla::chunk_step(dplan->kv_dtype, dplan->key_tile);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // The status word is reset here, before the planning kernel, so that only
   // kernels sit between the planner, the decode and the merge.

@@ -4,8 +4,7 @@
 // 2i + 1 in the low and high half of byte i), 32 e4m3 scales (one for 16 dims)
 // and the 64 rope dims in f16.  Latent dim d stands for code[d] * scale[d / 16],
 // rope dim r for rope[r], both times the cache's kv_scale, which goes to the
-// scores and the output instead.  CTA r of a pair reads codes [128 r, 128 r +
-// 128), scales [16 r, 16 r + 16) and rope dims [32 r, 32 r + 32): 208 bytes.
+// scores and the output instead.
 //
 // A code has two significant bits and a scale four, so their product has six
 // and lies in [2^-10, 2688]: exact in f16.
@@ -20,9 +19,6 @@ namespace fp4 {
 constexpr int kRow = 416;       // bytes of a row
 constexpr int kScales = 256;    // where its scales begin
 constexpr int kRope = 288;      // where its rope dims begin
-// What one CTA of a pair holds of a row: codes, scales, rope.  13 pieces of 16
-// bytes: odd, so that eight keys' pieces lie in different banks.
-constexpr int kRawScales = 128, kRawRope = 144, kRawRow = 208;
 
 #ifdef __CUDACC__
 // Eight codes to four f16 pairs, the low half of a byte first.
@@ -50,6 +46,13 @@ __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint4 scaled(uint32_t codes, uint32_t s) {
   const uint4 v = e2m1x8_to_f16x8(codes);
   return make_uint4(mul_f16x2(v.x, s), mul_f16x2(v.y, s), mul_f16x2(v.z, s), mul_f16x2(v.w, s));
+}
+
+// One of two e4m3 scales (the low 16 bits of `scales`), twice, as f16.
+__device__ __forceinline__ uint32_t scale_pair(uint32_t scales, int which) {
+  uint32_t s;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(s) : "h"((uint16_t)scales));
+  return __byte_perm(s, 0u, which ? 0x3232 : 0x1010);
 }
 
 // 32 codes (16 bytes) with two e4m3 scales (the low 16 bits of `scales`) to 32 f16.

@@ -11,9 +11,16 @@ inline bool kv_dtype_known(int d) {
 }
 
 // Up to so many score rows a sequence a 4-bit cache has a kernel of its own, whose
-// work units are single CTAs.  (In blocks of 32 it takes 64 rows in the time of the
-// kernel for more rows, 187 against 180 us at batch 64 x 8192, and 128 twice that.)
+// work units are single CTAs.  (In blocks of 32 it takes 64 rows in twice the time of
+// the kernel for more rows, 204 against 111 us at batch 64 x 8192.)
 constexpr int kFewRowsFp4 = 32;
+
+// Keys by which a plan cuts sequences: the decode kernel's tile.  The plan's key_tile
+// tells the few-row kernels (128) from the others (64); the one for more rows of a
+// 4-bit cache has tiles of 256.
+inline int chunk_step(int kv_dtype, int key_tile) {
+  return kv_dtype == MLA_KV_FP4_E2M1 && key_tile == kKeyTile ? 256 : key_tile;
+}
 
 }  // namespace mla
 

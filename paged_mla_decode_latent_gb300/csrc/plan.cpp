@@ -34,9 +34,10 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 int64_t align256(int64_t a) { return round_up(a, 256); }
 
-// Simulated time (ns) of one launch with a given chunk length.
+// Simulated time (ns) of one launch with a given chunk length
+// (a whole number of steps; a unit pays for whole steps).
 double simulate(const int32_t* lens, int batch, int row_blocks, int chunk, int splits,
-                int pairs, double ns_per_key, double ns_fixed, double ns_partial,
+                int step, int pairs, double ns_per_key, double ns_fixed, double ns_partial,
                 double ns_empty, double ns_combine_fixed, double ns_combine_per_unit) {
   std::priority_queue<double, std::vector<double>, std::greater<double>> free_at;
   for (int p = 0; p < pairs; ++p) free_at.push(0.0);
@@ -49,7 +50,7 @@ double simulate(const int32_t* lens, int batch, int row_blocks, int chunk, int s
       for (int rb = 0; rb < row_blocks; ++rb) {
         int64_t lo = (int64_t)s * chunk;
         int64_t keys = std::max<int64_t>(0, std::min<int64_t>(lens[b], lo + chunk) - lo);
-        double cost = keys > 0 ? ns_fixed + keys * ns_per_key + (splits > 1 ? ns_partial : 0.0)
+        double cost = keys > 0 ? ns_fixed + (step > 128 ? round_up(keys, step) : keys) * ns_per_key + (splits > 1 ? ns_partial : 0.0)
                                : ns_empty;
         units += keys > 0;
         double t = free_at.top();
@@ -105,6 +106,8 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
   p.key_tile = mla_small_rows_fit(p.rows, kv_dtype) ? mla::kKeyTileSmall : mla::kKeyTile;
   p.num_sms = num_sms;
   const bool fp4 = kv_dtype == MLA_KV_FP4_E2M1 && p.key_tile == mla::kKeyTileSmall;
+  const bool fp4_wide = kv_dtype == MLA_KV_FP4_E2M1 && !fp4;
+  const int step = mla::chunk_step(kv_dtype, p.key_tile);
   p.cluster_size = fp4 ? 1 : mla::kClusterSize;
 
   // Per-pair cost model of the decode kernel on GB300.  Its pipeline is bound
@@ -117,8 +120,10 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
   // all partials.
   const int pairs = std::max(1, num_sms / p.cluster_size);
   // The few-row kernel of 4-bit caches: single CTAs, 2.2 us per 128-key tile up
-  // to 16 rows and 2.8 up to 32.
-  const double ns_per_key = (fp4 && p.rows > 16 ? 2800.0 : 2200.0) / p.key_tile;
+  // to 16 rows and 2.8 up to 32.  The one for more rows: 2.9 us per 256-key tile up to
+  // 64 rows and 3.9 up to 128.
+  const double ns_per_key = fp4_wide ? (p.rows <= 64 ? 2900.0 : 3900.0) / step
+                                     : (fp4 && p.rows > 16 ? 2800.0 : 2200.0) / p.key_tile;
   const double ns_fixed = fp4 ? 8000.0 : 10000.0, ns_empty = 400.0, ns_partial = 1000.0;
   // The combine reads every non-empty unit's partials once (about 5000
   // bytes/ns) after a launch gap.
@@ -126,14 +131,14 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
   // 4-bit caches about 5 us)
   const double ns_combine_fixed = fp4 ? 5000.0 : 12000.0;
   const double ns_combine_per_unit = std::min(p.rows, p.row_tile) * (MLA_D_V * 4.0 + 4.0) / 5000.0;
-  int best_chunk = (int)round_up(std::max(max_ctx, 1), p.key_tile);
+  int best_chunk = (int)round_up(std::max(max_ctx, 1), step);
   int best_splits = 1;
   if (max_ctx > 0) {
-    double best_t = simulate(seq_lens_host, batch, p.row_blocks, best_chunk, 1, pairs, ns_per_key,
+    double best_t = simulate(seq_lens_host, batch, p.row_blocks, best_chunk, 1, step, pairs, ns_per_key,
                              ns_fixed, ns_partial, ns_empty, ns_combine_fixed,
                           ns_combine_per_unit);
     const int64_t max_splits =
-        std::min<int64_t>(ceil_div(max_ctx, p.key_tile), mla::kMaxSplits);
+        std::min<int64_t>(ceil_div(max_ctx, step), mla::kMaxSplits);
     // The best split candidate is kept only if it beats one unit per
     // sequence clearly: the model leaves out that the pairs slow down a
     // little when all of them run, and that short tail units fill their
@@ -145,7 +150,7 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
     auto consider = [&](int chunk) {
       const int splits = (int)ceil_div(max_ctx, chunk);
       if (splits < 2 || splits > mla::kMaxSplits) return;
-      double t = simulate(seq_lens_host, batch, p.row_blocks, chunk, splits, pairs, ns_per_key,
+      double t = simulate(seq_lens_host, batch, p.row_blocks, chunk, splits, step, pairs, ns_per_key,
                           ns_fixed, ns_partial, ns_empty, ns_combine_fixed,
                           ns_combine_per_unit);
       if (t < split_t) {
@@ -157,7 +162,7 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
     // Even splits of the longest context ...
     int last_splits = 1;
     for (int64_t s = 2; s <= max_splits; ++s) {
-      int chunk = (int)round_up(ceil_div(max_ctx, s), p.key_tile);
+      int chunk = (int)round_up(ceil_div(max_ctx, s), step);
       int splits = (int)ceil_div(max_ctx, chunk);
       if (splits == last_splits) continue;
       last_splits = splits;
@@ -168,8 +173,8 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
     // the SM pairs the first chunks leave idle (first chunks are dispatched
     // first).
     if (max_ctx <= 32768)
-      for (int64_t chunk = round_up(ceil_div(max_ctx, 2), p.key_tile); chunk < max_ctx;
-           chunk += p.key_tile)
+      for (int64_t chunk = round_up(ceil_div(max_ctx, 2), step); chunk < max_ctx;
+           chunk += step)
         consider((int)chunk);
     if (split_t < unsplit_t * 0.9) {
       best_t = split_t;

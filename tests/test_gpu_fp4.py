@@ -36,8 +36,8 @@ def test_every_code_and_scale(heads):
     assert status == 0
     ref, ref_l = p.reference()
     assert np.isfinite(ref).all()
-    # Each weight is rounded to f16 (2^-11) and each output to bf16 (2^-8); the fp32 sums and the scores' 2^-17 in the
-    # partner's half are far below.  With w the rounded weights the output moves by 2^-11 sum w |v| at most; 2^-10 for
+    # Each weight is rounded to f16 (2^-11) and each output to bf16 (2^-8); the fp32 sums of weights and
+    # scores are far below.  With w the rounded weights the output moves by 2^-11 sum w |v| at most; 2^-10 for
     # the two roundings of a weight and its share of the sum.
     for b in range(2):
         keys = np.abs(p.keys(b)[:, :512]).max()
@@ -122,6 +122,47 @@ def test_a_nan_scale_spoils_the_sequence_that_holds_it(heads, at, n):
     p.cache[p.table[1, 2], 3, 256 + at] = 0x7F
     out, lse, _, status = p.run()
     assert status == 0 and np.isnan(out[1]).all() and np.isnan(lse[1]).all() and np.array_equal(out[0], good[0])
+
+
+# What a key's rope adds to every score, by its place in the sequence: the running maximum rises with most tiles, with
+# the keys of one CTA's half of a 256-key tile only, once by much, never after the first key.
+RAMPS = {"up": lambda j: j / 20.0, "up in the first half": lambda j: np.where(j % 256 < 128, j / 20.0, 0.0),
+         "up in the second half": lambda j: np.where(j % 256 >= 128, j / 20.0, 0.0),
+         "a jump": lambda j: np.where(j == 700, 100.0, 0.0), "down": lambda j: np.where(j == 0, 80.0, 0.0)}
+
+
+@pytest.mark.parametrize("heads,sq", [(16, 1), (32, 1), (64, 1), (128, 1), (100, 2)])
+@pytest.mark.parametrize("ramp", RAMPS)
+def test_running_maximum(heads, sq, ramp):
+    p = f4.Fp4Problem(2, sq, heads, [1300, 801], 16, sq > 1, seed=8)
+    p.q_bits[..., 512:] = 0
+    p.q_bits[..., 512] = 0x4280  # 64
+    unit = 64.0 * p.scale * p.kv_scale
+    for b in range(2):
+        j = np.arange(p.lens[b])
+        rope = np.zeros((p.lens[b], 64), np.float16)
+        rope[:, 0] = RAMPS[ramp](j) / unit
+        p.cache[p.table[b, j // 16], j % 16, 288:] = rope.view(np.uint8)
+    for num_sms in (0, 2):  # several splits, one
+        out, lse, plan, status = p.run(num_sms)
+        assert status == 0
+        assert_close(out, lse, *p.reference(), f"{ramp}, {plan.num_splits} splits")
+
+
+@pytest.mark.parametrize("heads,sq,lens", [(33, 1, [255, 256, 257]), (64, 1, [1, 128, 129]), (65, 1, [512, 3, 400]),
+                                           (128, 8, [700, 20, 16]), (43, 3, [130, 0, 5])])
+def test_row_blocks(heads, sq, lens):
+    p = f4.Fp4Problem(3, sq, heads, lens, 16, sq > 1, seed=10)
+    for num_sms in (0, 2):
+        out, lse, plan, status = p.run(num_sms)
+        assert status == 0
+        assert_close(out, lse, *p.reference(), f"{plan.num_splits} splits")
+
+
+@pytest.mark.parametrize("heads", [40, 128])
+def test_waits_of_a_pair_run_out_without_a_fault(heads):
+    """With a bound of 1 us the waits of both CTAs of a pair give up, and the next call is right."""
+    test_waits_run_out_without_a_fault(heads)
 
 
 @pytest.mark.parametrize("heads", [16, 32])
