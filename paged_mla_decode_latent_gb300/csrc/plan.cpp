@@ -128,8 +128,9 @@ extern "C" int mla_decode_plan(const int32_t* seq_lens_host, int32_t batch, int3
   // The combine reads every non-empty unit's partials once (about 5000
   // bytes/ns) after a launch gap.
   // measured: launch, dependency wait and the LSE pass (behind the few-row kernel of
-  // 4-bit caches about 5 us)
-  const double ns_combine_fixed = fp4 ? 5000.0 : 12000.0;
+  // 4-bit caches about 5 us, behind their pair kernel 2: batch 4 x 128 heads x 1024
+  // takes 25 us in four splits and 33 in one, 13 x 36 rows x 999 20 and 25)
+  const double ns_combine_fixed = fp4 ? 5000.0 : fp4_wide ? 2000.0 : 12000.0;
   const double ns_combine_per_unit = std::min(p.rows, p.row_tile) * (MLA_D_V * 4.0 + 4.0) / 5000.0;
   int best_chunk = (int)round_up(std::max(max_ctx, 1), step);
   int best_splits = 1;
