@@ -39,8 +39,11 @@ constexpr int kSlice = 256;               // table entries a warp takes at a tim
 constexpr int kSegment = 4 * 16 * kThreads;  // bytes that a CTA moves at a time
 constexpr int kMaxRows = 65535;
 constexpr int kCluster = 8;
-// What a cluster takes alone: more pages or entries than these it reads too slowly.
-constexpr int64_t kClusterPages = 1 << 16, kClusterEntries = 1 << 18;
+// What a cluster takes alone.  On the GPU it is no faster than the chain (resize and fork
+// of 64 rows, us in a graph: 5.6 and 6.3 against 5.8 and 5.9 at 4096 pages, 6.0 and 7.5
+// against 5.5 and 6.8 at 32768, 7.4 and 9.2 against 5.9 and 7.4 at 65536), but the host
+// spends 4 us less on a call (8 against 12 for resize, 13 against 17 for fork).
+constexpr int64_t kClusterPages = 1 << 15, kClusterEntries = 1 << 18;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t a) { return ceil_div(a, 256) * 256; }

@@ -25,7 +25,8 @@ def started(pages, page, rows, width, layers=1, row=16, seed=0, keep=0.3, fill=0
 
 
 SIZES = [(1, 1, 1, 1), (9, 7, 3, 4), (100, 16, 5, 40), (4096, 1, 33, 300), (4097, 3, 8, 600), (8192, 64, 64, 100),
-         (20001, 16, 70, 2500), (513, 4096, 4, 3)]
+         (20001, 16, 70, 2500), (513, 4096, 4, 3),
+         (40001, 2, 50, 900), (300, 16, 600, 500)]  # these two: a kernel a step
 
 
 @pytest.mark.parametrize("pages,page,rows,width", SIZES)
@@ -76,7 +77,7 @@ def test_compact(pages, page, rows, width, layers, row):
 
 
 @pytest.mark.parametrize("live", ["none", "all", "first half", "second half"])
-@pytest.mark.parametrize("pages", [4096, 8192, 5000, 8])
+@pytest.mark.parametrize("pages", [4096, 8192, 5000, 8, 40000])
 def test_compact_at_the_ends(live, pages):
     b = Book(pages, 2, 1, 1, seed=2)
     held = {"none": slice(0), "all": slice(None), "first half": slice(pages // 2), "second half": slice(pages // 2, None)}[live]
