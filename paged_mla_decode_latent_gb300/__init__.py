@@ -373,12 +373,10 @@ def dplan_check(d: DPlan, workspace, stream=None) -> int:
 def gather_kv_b_proj(kv_cache, kv_scale, block_table, seq_lens, cu_seqlens, max_ctx: int, w_kv_b,
                      k_out, v_out, status, stream=None) -> None:
     """``mla_gather_kv_b_proj``: k_out [T, H, 192], v_out [T, H, 128] bf16 from the
-    paged latent and kv_b_proj w_kv_b [H, 256, 512] bf16."""
-    import torch
-    fp8 = kv_cache.dtype in (torch.uint8, torch.float8_e4m3fn)
+    paged latent and kv_b_proj w_kv_b [H, 256, 512] bf16.  (Not from 4-bit rows.)"""
     st = lib().mla_gather_kv_b_proj(
         _ptr(kv_cache), int(kv_cache.shape[0]), int(kv_cache.shape[1]),
-        KV_FP8_E4M3 if fp8 else KV_BF16, _ptr(kv_scale), _ptr(block_table),
+        _kv_dtype(kv_cache), _ptr(kv_scale), _ptr(block_table),
         int(block_table.stride(0)), _ptr(seq_lens), _ptr(cu_seqlens), int(seq_lens.numel()),
         int(max_ctx), _ptr(w_kv_b), int(w_kv_b.shape[0]), _ptr(k_out), _ptr(v_out), _ptr(status),
         _stream(stream))
@@ -390,6 +388,7 @@ def epilogue(ql_nope, q_pe, kv_c, k_pe, slot_mapping, q_out, kv_cache, kv_scale=
     """``mla_decode_epilogue``: q_out = ql_nope || q_pe; cache[slot] = kv_c || k_pe
     (bf16, e4m3 codes of x / kv_scale for a uint8 / float8 cache, or 4-bit rows)."""
     T, H, _ = ql_nope.shape
+    _check_fp4(_kv_dtype(kv_cache), kv_cache.shape[1], kv_cache, "mla_decode_epilogue")
     st = lib().mla_decode_epilogue(
         _ptr(ql_nope), _ptr(q_pe), _ptr(kv_c), _ptr(k_pe), _ptr(slot_mapping), int(T), int(H),
         _ptr(q_out), _ptr(kv_cache), int(kv_cache.shape[0]), int(kv_cache.shape[1]),

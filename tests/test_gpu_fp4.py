@@ -313,3 +313,23 @@ def test_captured_and_replayed_on_another_stream():
         g.replay()
         torch.cuda.synchronize()
         assert np.array_equal(out.double().cpu().numpy(), want) and np.array_equal(lse.double().cpu().numpy(), want_l)
+
+
+def test_calls_that_do_not_take_4_bit_rows():
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    p = f4.Fp4Problem(2, 1, 16, [40, 30], 16, seed=1)
+    t = p.to_device()
+    bf = dict(dtype=torch.bfloat16, device="cuda")
+    k, v, status = torch.zeros(70, 2, 192, **bf), torch.zeros(70, 2, 128, **bf), torch.zeros(1, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 40, 70], dtype=torch.int32, device="cuda")
+    with pytest.raises(mla.MLADecodeError) as e:
+        mla.gather_kv_b_proj(t["cache"], t["scale"], t["bt"], t["lens"], cu, 40, torch.zeros(2, 256, 512, **bf), k, v, status)
+    assert e.value.status == mla.ERR_UNSUPPORTED
+    with pytest.raises(mla.MLADecodeError):
+        mla.decode_prefix(t["q"], t["cache"], t["bt"][0, :1].contiguous(), t["bt"], t["lens"], 16, kv_scale=t["scale"])
+    ql, qp, kc, kp = (torch.zeros(s, **bf) for s in ((2, 16, 512), (2, 16, 64), (2, 512), (2, 64)))
+    slots = torch.arange(2, device="cuda")
+    for cache in (t["cache"][:, ::2], t["cache"][None]):  # strided, one layer too many
+        with pytest.raises(mla.MLADecodeError):
+            mla.epilogue(ql, qp, kc, kp, slots, torch.zeros(2, 16, 576, **bf), cache, t["scale"])
