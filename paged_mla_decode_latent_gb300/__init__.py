@@ -219,7 +219,8 @@ def _kv_dtype(cache) -> int:
 
 def _check_fp4(kv_dtype, page_size, cache, where):
     """A plan for 4-bit rows goes with a cache of them, and no other plan does."""
-    if (kv_dtype == KV_FP4_E2M1) != (_kv_dtype(cache) == KV_FP4_E2M1) or kv_dtype == KV_FP4_E2M1 and not (
+    four = cache.dtype is _torch().uint8 and cache.shape[-1] == FP4_ROW
+    if (kv_dtype == KV_FP4_E2M1) is not four or four and not (
             cache.dim() == 3 and cache.shape[1] == page_size and cache.is_contiguous()):
         raise MLADecodeError(ERR_INVALID_ARG, where)
 
@@ -232,14 +233,15 @@ def _row_stride(table):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    import torch
+    """A stream's handle as an integer; None: the current stream of the current device."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream))
+        c = _torch()._C
+        return c._cuda_getCurrentRawStream(c._cuda_getDevice())
+    return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
 def _torch():
