@@ -14,7 +14,7 @@
 // the book is small a cluster of eight CTAs takes the steps in one launch, with the
 // cluster's barrier between them; else each step is a kernel, launched while the
 // one before it still runs and waiting for it (programmatic dependent launch).
-// Moving rows is always a kernel of its own, over the whole GPU.
+// Moving rows is a kernel of its own, over the whole GPU, unless they are few.
 //
 // refs and the tables are small (4 bytes a page or entry), so resize is bound by
 // the latency of its three kernels, fork and compact by those and by the rows
@@ -44,6 +44,10 @@ constexpr int kCluster = 8;
 // against 5.5 and 6.8 at 32768, 7.4 and 9.2 against 5.9 and 7.4 at 65536), but the host
 // spends 4 us less on a call (8 against 12 for resize, 13 against 17 for fork).
 constexpr int64_t kClusterPages = 1 << 15, kClusterEntries = 1 << 18;
+// And the bytes up to which it copies fork's rows, too (8 beams, us in a graph and of the
+// host: 10.1 and 10.8 against 10.6 and 13.1 by a kernel of its own at 72 KB, 12.4 and 10.8
+// against 11.7 and 12.9 at 288 KB).
+constexpr int64_t kClusterBytes = 1 << 17;
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t align256(int64_t a) { return ceil_div(a, 256) * 256; }
@@ -469,20 +473,6 @@ __global__ void __launch_bounds__(kThreads) fork_give_kernel(Book k, Children c)
 }
 
 // The three steps by one cluster.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
-    fork_kernel(Book k, Table t, Children c, int slices) {
-  const int id = blockIdx.x;
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
-  if (id == 0) fork_needs(k, t, c);
-  fork_release(k, t, c, slices, kCluster - 1 - id, kCluster);
-  fork_rows(k, t, c, slices, kCluster - 1 - id, kCluster);
-  ptx::cluster_sync_all();
-  for (int x = id; x < k.chunks; x += kCluster) count_chunk<false>(k, x);
-  ptx::cluster_sync_all();
-  for (int x = id; x < k.chunks; x += kCluster) fork_give(k, c, x);
-}
-
 // The first `bytes` bytes at `from` to `to`, by the CTA: segment `s` of them.
 __device__ __forceinline__ void move_segment(uint8_t* to, const uint8_t* from, int64_t bytes, int64_t s) {
   const int64_t at = s * kSegment + threadIdx.x * 16;
@@ -495,22 +485,44 @@ __device__ __forceinline__ void move_segment(uint8_t* to, const uint8_t* from, i
     if (at + i * kThreads * 16 < bytes) __stcs(reinterpret_cast<uint4*>(to + at + i * kThreads * 16), v[i]);
 }
 
-__global__ void __launch_bounds__(kThreads) fork_copy_kernel(Book k, Table t, Children c, Cache cache) {
-  ptx::grid_dependency_wait();
-  ptx::launch_dependents();
+// The filled rows of the pages that children get a copy of: CTA `id` of `of`.
+__device__ void fork_copy(const Book& k, const Table& t, const Children& c, const Cache& cache, int id, int of) {
   const int64_t page_bytes = cache.row_bytes * k.page_size;
   const int64_t segments = (page_bytes + kSegment - 1) / kSegment;
-  const int64_t units = (int64_t)k.totals->given * cache.layers * segments;
-  for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+  const int64_t units = (int64_t)__ldcg(&k.totals->given) * cache.layers * segments;
+  for (int64_t u = id; u < units; u += of) {
     const int n = (int)(u / (cache.layers * segments));
     const int64_t rest = u - n * (cache.layers * segments);
     const int layer = (int)(rest / segments);
-    const int child = k.row_b[n], r = c.parents[child], len = c.lens[child];
-    const int from = t.at[r * t.stride + len / k.page_size], to = k.row_c[n];
+    const int child = __ldcg(&k.row_b[n]), r = c.parents[child], len = __ldcg(&c.lens[child]);
+    const int from = t.at[r * t.stride + len / k.page_size], to = __ldcg(&k.row_c[n]);
     if (from < 0 || from >= k.pages) continue;  // flagged
     uint8_t* base = cache.at + layer * cache.layer_stride;
     move_segment(base + to * page_bytes, base + from * page_bytes, len % k.page_size * cache.row_bytes, rest % segments);
   }
+}
+
+__global__ void __launch_bounds__(kThreads) fork_copy_kernel(Book k, Table t, Children c, Cache cache) {
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  fork_copy(k, t, c, cache, blockIdx.x, gridDim.x);
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
+    fork_kernel(Book k, Table t, Children c, Cache cache, int slices, bool copies) {
+  const int id = blockIdx.x;
+  ptx::grid_dependency_wait();
+  ptx::launch_dependents();
+  if (id == 0) fork_needs(k, t, c);
+  fork_release(k, t, c, slices, kCluster - 1 - id, kCluster);
+  fork_rows(k, t, c, slices, kCluster - 1 - id, kCluster);
+  ptx::cluster_sync_all();
+  for (int x = id; x < k.chunks; x += kCluster) count_chunk<false>(k, x);
+  ptx::cluster_sync_all();
+  for (int x = id; x < k.chunks; x += kCluster) fork_give(k, c, x);
+  if (!copies) return;
+  ptx::cluster_sync_all();
+  fork_copy(k, t, c, cache, id, kCluster);
 }
 
 // -------------------------------------------------------------- compact ---
@@ -763,7 +775,9 @@ extern "C" int mla_pages_fork(int32_t* refs, int64_t num_pages, const int32_t* b
   const int slices = (int)ceil_div(width, kSlice);
   const int64_t segments = ceil_div(row_bytes * page_size, kSegment);
   const bool cluster = by_cluster(num_pages, std::max(rows, out_rows), width);
-  if (cluster && launch(fork_kernel, kCluster, stream, k, t, c, slices) != cudaSuccess) return MLA_ERR_CUDA;
+  const bool copies = cluster && layers * row_bytes * page_size <= kClusterBytes / std::max(out_rows, 1);
+  if (cluster && launch(fork_kernel, kCluster, stream, k, t, c, cache, slices, copies) != cudaSuccess) return MLA_ERR_CUDA;
+  if (copies) return MLA_OK;
   if (!cluster &&
       (launch(fork_ask_kernel, 1 + some(ceil_div((int64_t)rows * slices, kWarps)), stream, k, t, c, slices) != cudaSuccess ||
        launch(fork_rows_kernel, k.chunks + some(ceil_div((int64_t)out_rows * slices, kWarps)), stream, k, t, c, slices) != cudaSuccess ||
