@@ -472,7 +472,6 @@ __global__ void __launch_bounds__(kThreads) fork_give_kernel(Book k, Children c)
   fork_give(k, c, blockIdx.x);
 }
 
-// The three steps by one cluster.
 // The first `bytes` bytes at `from` to `to`, by the CTA: segment `s` of them.
 __device__ __forceinline__ void move_segment(uint8_t* to, const uint8_t* from, int64_t bytes, int64_t s) {
   const int64_t at = s * kSegment + threadIdx.x * 16;
@@ -508,6 +507,7 @@ __global__ void __launch_bounds__(kThreads) fork_copy_kernel(Book k, Table t, Ch
   fork_copy(k, t, c, cache, blockIdx.x, gridDim.x);
 }
 
+// The three steps by one cluster, and the copies if they are few.
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     fork_kernel(Book k, Table t, Children c, Cache cache, int slices, bool copies) {
   const int id = blockIdx.x;
