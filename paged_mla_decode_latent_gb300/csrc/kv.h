@@ -11,8 +11,8 @@ inline bool kv_dtype_known(int d) {
 }
 
 // Up to so many score rows a sequence a 4-bit cache has a kernel of its own, whose
-// work units are single CTAs.  (In blocks of 32 it takes 64 rows in twice the time of
-// the kernel for more rows, 204 against 111 us at batch 64 x 8192.)
+// work units are single CTAs.  (64 rows in blocks of 32 take 187 us at batch
+// 64 x 8192, by the kernel for more rows 111, which 48 rows take as well; 32 here 102.)
 constexpr int kFewRowsFp4 = 32;
 
 // Keys by which a plan cuts sequences: the decode kernel's tile.  The plan's key_tile
