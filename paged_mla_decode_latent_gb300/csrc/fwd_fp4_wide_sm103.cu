@@ -244,20 +244,21 @@ __device__ __forceinline__ void take_registers() {
   if constexpr (kRegs < kLaunchRegs) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
-// Loads that stay where they are written, ahead of the conversion that they feed.
+// Loads that stay where they are written, ahead of the conversion that they feed.  (Plain
+// ones: the newest rows may come from the kernel that this one is launched behind.)
 __device__ __forceinline__ uint4 ld_ahead_u4(const void* p) {
   uint4 v;
-  asm volatile("ld.global.nc.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_ahead_u32(const void* p) {
   uint32_t v;
-  asm volatile("ld.global.nc.u32 %0, [%1];" : "=r"(v) : "l"(p));
+  asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
   return v;
 }
 __device__ __forceinline__ uint32_t ld_ahead_u16(const void* p) {
   uint16_t v;
-  asm volatile("ld.global.nc.u16 %0, [%1];" : "=h"(v) : "l"(p));
+  asm volatile("ld.global.u16 %0, [%1];" : "=h"(v) : "l"(p));
   return v;
 }
 
@@ -918,7 +919,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t t = __umulhi(pmul, key);
         return pdiv == 1u ? key : (t + ((key - t) >> 1)) >> pshift;
       };
-      auto page_at = [&](int key) -> int { return (int)ld_ahead_u32(&bt[page_of((uint32_t)key)]); };
+      auto page_at = [&](int key) -> int { return __ldg(&bt[page_of((uint32_t)key)]); };
       for (int t = 0; t < n_tiles; ++t) {
         const int slot = t % kRowTiles;
         if (t >= kRowTiles && !wait_all(c, BAR(rows_empty, slot), (t / kRowTiles - 1) & 1)) break;

@@ -333,3 +333,36 @@ def test_calls_that_do_not_take_4_bit_rows():
     for cache in (t["cache"][:, ::2], t["cache"][None]):  # strided, one layer too many
         with pytest.raises(mla.MLADecodeError):
             mla.epilogue(ql, qp, kc, kp, slots, torch.zeros(2, 16, 576, **bf), cache, t["scale"])
+
+
+@pytest.mark.parametrize("heads", [16, 64, 128])
+def test_steps_one_after_another_on_a_cache_16_bytes_off(heads):
+    """Each step inserts a token and decodes right behind the insert, over a cache that begins between two sectors; the
+    row before the new one was read by the step before."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    B, page, first, n = 3, 16, [30, 300, 511], 6
+    p = f4.Fp4Problem(B, 1, heads, [m + n for m in first], page, False, seed=13, poison=False)
+    t = p.to_device()
+    flat = torch.zeros(t["cache"].numel() + 16, dtype=torch.uint8, device="cuda")
+    cache = flat[16:].view(t["cache"].shape)
+    cache.copy_(t["cache"])
+    for b, m in enumerate(first):  # what the steps write is not there yet
+        for j in range(m, m + n):
+            cache[int(p.table[b, j // page]), j % page] = 0x7F
+    g = torch.Generator(device="cuda").manual_seed(3)
+    rnd = lambda *s: torch.randn(*s, generator=g, device="cuda").to(torch.bfloat16)  # noqa: E731
+    plan = mla.plan(p.lens, heads, 1, page, mla.KV_FP4_E2M1)
+    ws, out = mla.workspace_for(plan), torch.empty(B, 1, heads, 512, dtype=torch.bfloat16, device="cuda")
+    lse, q, got = torch.empty(B, 1, heads, device="cuda"), torch.empty(B, heads, 576, dtype=torch.bfloat16, device="cuda"), []
+    for k in range(n):
+        ql, qp, kc, kp = rnd(B, heads, 512), rnd(B, heads, 64), rnd(B, 512), rnd(B, 64)
+        lens = torch.tensor([m + k + 1 for m in first], dtype=torch.int32, device="cuda")
+        slots = torch.tensor([int(p.table[b, (m + k) // page]) * page + (m + k) % page for b, m in enumerate(first)], device="cuda")
+        mla.step(plan, ql, qp, kc, kp, slots, q, cache, t["scale"], t["bt"], lens, p.scale, out, lse, ws)
+        got.append((q.clone(), out.double().cpu().numpy(), lse.double().cpu().numpy()))
+    assert mla.check(plan, ws) == 0
+    p.cache = cache.cpu().numpy()
+    for k, (qk, o, l) in enumerate(got):
+        p.q_bits, p.lens = qk.view(torch.int16).cpu().numpy().view(np.uint16).reshape(B, 1, heads, 576), np.array([m + k + 1 for m in first], np.int32)
+        assert_close(o, l, *p.reference(), f"step {k}")
