@@ -14,6 +14,8 @@
 // the book is small a cluster of eight CTAs takes the steps in one launch, with the
 // cluster's barrier between them; else each step is a kernel, launched while the
 // one before it still runs and waiting for it (programmatic dependent launch).
+// A call's last kernel lets no other start before it is done: the decode kernels
+// read the lengths, which it may have written, before they wait.
 // Moving rows is a kernel of its own, over the whole GPU, unless they are few.
 //
 // refs and the tables are small (4 bytes a page or entry), so resize is bound by
@@ -327,7 +329,6 @@ __global__ void __launch_bounds__(kThreads) count_free_kernel(Book k) {
 __global__ void __launch_bounds__(kThreads) resize_give_kernel(Book k, Table t, const int32_t* new_lens,
                                                                int64_t* slots, int tokens) {
   ptx::grid_dependency_wait();
-  ptx::launch_dependents();
   int before;
   const int chunk = min((int)blockIdx.x, k.chunks), free_pages = chunk_sums(k, chunk, &before);
   if (chunk < k.chunks) resize_give(k, t, new_lens, slots, tokens, chunk, free_pages, before);
@@ -339,7 +340,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     resize_kernel(Book k, Table t, const int32_t* new_lens, int slices, int64_t* slots, int tokens) {
   const int id = blockIdx.x;
   ptx::grid_dependency_wait();
-  ptx::launch_dependents();
   if (id == 0) resize_needs(k, t, new_lens);
   resize_release(k, t, new_lens, slices, kCluster - 1 - id, kCluster);
   ptx::cluster_sync_all();
@@ -503,7 +503,6 @@ __device__ void fork_copy(const Book& k, const Table& t, const Children& c, cons
 
 __global__ void __launch_bounds__(kThreads) fork_copy_kernel(Book k, Table t, Children c, Cache cache) {
   ptx::grid_dependency_wait();
-  ptx::launch_dependents();
   fork_copy(k, t, c, cache, blockIdx.x, gridDim.x);
 }
 
@@ -512,7 +511,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
     fork_kernel(Book k, Table t, Children c, Cache cache, int slices, bool copies) {
   const int id = blockIdx.x;
   ptx::grid_dependency_wait();
-  ptx::launch_dependents();
+  if (!copies) ptx::launch_dependents();
   if (id == 0) fork_needs(k, t, c);
   fork_release(k, t, c, slices, kCluster - 1 - id, kCluster);
   fork_rows(k, t, c, slices, kCluster - 1 - id, kCluster);
@@ -599,7 +598,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kThreads)
 
 __global__ void __launch_bounds__(kThreads) compact_move_kernel(Book k, Table t, Cache cache, int32_t* map, int slices) {
   ptx::grid_dependency_wait();
-  ptx::launch_dependents();
   const int moves = k.totals->given, n = k.totals->live;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < moves; i += (int64_t)gridDim.x * kThreads) {
     const int from = k.page_a[i], to = k.page_b[i];

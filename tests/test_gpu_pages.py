@@ -367,3 +367,75 @@ def test_a_generation_with_beams_over_a_4_bit_cache():
         attend(append([len(s) + (3 if b % 2 else 2) if len(s) else 0 for b, s in enumerate(seen)], 3))
     append([0] * B, 1)
     assert int(status) == 0 and not refs.any()
+
+
+@pytest.mark.parametrize("pages,page,W", [(200, 16, 20), (33000, 2, 160)])  # one launch a call, a kernel a step
+def test_a_decode_right_behind_sees_the_new_lengths(pages, page, W):
+    """Rows shrink and grow and the decode follows with nothing between, one call after another and in a graph: the
+    lengths, tables and copied rows that it reads are those of the call before it."""
+    import torch
+    import paged_mla_decode_latent_gb300 as mla
+    H, B = 16, 5
+    rng = np.random.default_rng(2)
+    b = Book(pages, page, B, W, 1, 416, 3)
+    b.cache = f4.encode(rng.standard_normal((pages * page, 512)), rng.standard_normal((pages * page, 64)), 0.01).reshape(1, pages, page, 416)
+    b.resize([300, 17, 0, 64, 200])
+    g = Gpu(b)
+    q = torch.from_numpy(rng.standard_normal((B, 1, H, 576)).astype(np.float32)).to(torch.bfloat16).cuda()
+    scale = torch.tensor([0.01], device="cuda")
+    plan = mla.plan([W * page] * B, H, 1, page, mla.KV_FP4_E2M1)
+    ws = mla.workspace_for(plan)
+    new = [torch.tensor(n, dtype=torch.int32, device="cuda") for n in
+           ([1, 0, 33, 320, 7], [310, 5, 0, 2, 7], [16, 290, 100, 0, 15], [0, 1, 320, 48, 49], [300, 17, 0, 64, 200])]
+    parents = torch.tensor([4, 0, 0, 3, 1], dtype=torch.int32, device="cuda")
+    table2, lens2 = torch.zeros(B, W, dtype=torch.int32, device="cuda"), torch.zeros(B, dtype=torch.int32, device="cuda")
+    outs = [(torch.empty(B, 1, H, 512, dtype=torch.bfloat16, device="cuda"), torch.empty(B, 1, H, device="cuda")) for _ in range(len(new) + 1)]
+
+    def attend(table, lens, out, lse):
+        mla.fwd(plan, q, g.cache[0], scale, table, lens, 0.05, out, lse, ws)
+        mla.combine(plan, lens, out, lse, ws)
+
+    def steps():
+        for n, o in zip(new, outs):
+            mla.pages_resize(g.refs, g.table, g.lens, n, page, g.ws, None, g.status)
+            attend(g.table, g.lens, *o)
+        mla.pages_fork(g.refs, g.table, g.lens, parents, table2, lens2, g.cache, g.ws, g.status)
+        attend(table2, lens2, *outs[-1])
+
+    start = [x.clone() for x in (g.refs, g.table, g.lens, g.cache)]
+
+    def again():
+        for x, y in zip((g.refs, g.table, g.lens, g.cache), start):
+            x.copy_(y)
+
+    def expected(table, lens):
+        rows = f4.decode_rows(g.cache[0].cpu().numpy()) * 0.01
+        ref, lse, qq = np.zeros((B, 1, H, 512)), np.full((B, 1, H), -np.inf), q.double().cpu().numpy()
+        for i, n in enumerate(lens):
+            if n == 0:
+                continue
+            j = np.arange(n)
+            keys = rows[table[i, j // page], j % page]
+            z = qq[i, 0] @ keys.T * 0.05
+            w = np.exp(z - z.max(1, keepdims=True))
+            lse[i, 0], ref[i, 0] = z.max(1) + np.log(w.sum(1)), w / w.sum(1, keepdims=True) @ keys[:, :512]
+        return ref, lse
+
+    plain = []
+    for n in new:
+        b.resize(n.cpu().numpy())
+        plain.append((b.table.copy(), b.lens.copy()))
+    steps()
+    want = [expected(*s) for s in plain] + [expected(table2.cpu().numpy(), lens2.cpu().numpy())]
+    first = [o.clone() for o, _ in outs]
+    for k, (o, (ref, lse)) in enumerate(zip(outs, want)):
+        assert_close(o[0].double().cpu().numpy(), o[1].double().cpu().numpy(), ref, lse, f"step {k}")
+    again()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        steps()
+    for _ in range(20):
+        again()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, f) for (o, _), f in zip(outs, first))
