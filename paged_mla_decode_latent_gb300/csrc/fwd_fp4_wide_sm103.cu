@@ -28,7 +28,7 @@
 //   PV warp       (even CTA) O^T += V^T P, 32 keys at a time
 // K and V read the cache into registers (a key's pieces side by side in a quad of lanes):
 // no shared memory is left for a ring of codes, and less of it leaves more L1 for the
-// reads that come back to a line (five units of V instead of three: 184 against 146 us).
+// reads that come back to a line (five units of V took 184 us where three took 163).
 //
 // What bounds it: no unit, but the chain of handoffs; a tile takes 7900 cycles at N =
 // 128, its MMAs 4400 and its shared-memory traffic 3500.  Batch 64 x 128 heads x 8192:
