@@ -12,7 +12,7 @@
 // f16 (16 KB each way for 256 keys at N = 128), a bit a warp on whether a tile raises the
 // running maxima, and the maxima where it does.  Contracting the dims in halves instead,
 // as the 128-row kernel of the wider caches does, trades partial scores, 128 KB for 256
-// keys: at 28 GB/s each way it was bound by that (197 us where this takes 146, below).
+// keys: at 28 GB/s each way it was bound by that (197 us where this takes 143, below).
 // Scores are summed in fp32 in one place.
 //
 // Per tile, all at once:
@@ -30,13 +30,14 @@
 // no shared memory is left for a ring of codes, and less of it leaves more L1 for the
 // reads that come back to a line (five units of V took 184 us where three took 163).
 //
-// What bounds it: no unit, but the chain of handoffs; a tile takes 7900 cycles at N =
+// What bounds it: no unit, but the chain of handoffs; a tile takes 7700 cycles at N =
 // 128, its MMAs 4400 and its shared-memory traffic 3500.  Batch 64 x 128 heads x 8192:
-// 146 us (1.50 TB/s; 52 % of what cuBLAS reaches in bf16), batch 8 x 128 x 65536: 141;
+// 143 us (1.53 TB/s; 53 % of what cuBLAS reaches in bf16), batch 8 x 128 x 65536: 138;
 // batch 64 x 64 heads x 8192: 111 us.  Steps to there from 277: four lanes a key instead
 // of one 234, slabs of 128 dims instead of 64 232, rows fetched to L2 ahead 208, scores
 // to registers, K and V in eight warps each and the rows looked up by a warp of their
-// own 184, three units of V 163, fewer registers spilled 146.
+// own 184, three units of V 163, fewer registers spilled 146, six query loads in flight
+// instead of nine (the last registers) 143.
 //
 // Every wait is bounded (2 s unless the plan sets another limit); one that runs out
 // sets MLA_DEVFLAG_TIMEOUT and the pair winds down.
@@ -592,17 +593,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // problem's are zero.
     {
       bool range = false;
+      constexpr int kPieces = N <= 64 ? 9 : 6;  // in flight a thread
+      static_assert(R * 72 % (kPieces * kSoftmaxThreads) == 0, "whole rounds");
 #pragma unroll 1
-      for (int i0 = st; i0 < R * 72; i0 += 9 * kSoftmaxThreads) {
-        uint4 x[9];
+      for (int i0 = st; i0 < R * 72; i0 += kPieces * kSoftmaxThreads) {
+        uint4 x[kPieces];
 #pragma unroll
-        for (int j = 0; j < 9; ++j) {
+        for (int j = 0; j < kPieces; ++j) {
           const int i = i0 + kSoftmaxThreads * j, r = i / 72, ch = i - 72 * r, row = R * (int)rank + r;
           x[j] = make_uint4(0, 0, 0, 0);
           if (row < n_rows) x[j] = reinterpret_cast<const uint4*>(p.q + ((size_t)b * p.rows + row0 + row) * mla::kDQK)[ch];
         }
 #pragma unroll
-        for (int j = 0; j < 9; ++j) {
+        for (int j = 0; j < kPieces; ++j) {
           const int i = i0 + kSoftmaxThreads * j, r = i / 72, ch = i - 72 * r;
           uint32_t w[4] = {x[j].x, x[j].y, x[j].z, x[j].w};
 #pragma unroll
