@@ -118,7 +118,8 @@ typedef enum mla_kv_dtype {
 #define MLA_DEVFLAG_NO_PAGES 0x40  /* pages: fewer are free than were asked for */
 #define MLA_DEVFLAG_BAD_ROW 0x80   /* pages: a parent outside the table */
 #define MLA_DEVFLAG_REFS 0x100     /* pages: a count below zero, or a free page in a table */
-#define MLA_DEVFLAG_SHARED 0x200   /* pages: a row grows in a page that others hold too */
+#define MLA_DEVFLAG_SHARED 0x200   /* pages: a row grows in a page that others hold too
+                                      (its tokens there get no slot) */
 
 #define MLA_DECODE_PLAN_VERSION 1
 #define MLA_D_QK 576 /* query/key row width: 512 latent + 64 rope */
@@ -652,15 +653,21 @@ int64_t mla_pages_workspace_bytes(int64_t num_pages, int32_t rows);
  * all rows give back the pages past their new length, then rows in order are
  * given the free pages that they need.  A row that cannot have all of them, and
  * every later row that needs any, keeps its old length (MLA_DEVFLAG_NO_PAGES).
- * seq_lens holds the lengths that came of it.  A row that grows in its last,
- * partly filled page must be the only one that holds it (MLA_DEVFLAG_SHARED tells;
- * mla_pages_fork sees to it, and a row cut back into a shared page does not grow
- * again without one).
+ * seq_lens holds the lengths that came of it.
+ *
+ * A row that grows in its last, partly filled page must be the only one that
+ * holds it once the others have given theirs back.  A row is not if it was cut back
+ * into a page that it shares: mla_pages_fork leaves that page with its first child.
+ * To grow such a row, go on from it twice: the second child has a copy of the page,
+ * and the first is let go by a later call.  Without that its tokens in the shared
+ * page get no slot (-1: those places hold the others' tokens), although its length
+ * counts them, and MLA_DEVFLAG_SHARED is set; the others' tokens are safe.
  *
  * new_lens  device int32 [rows], not seq_lens itself
  * slots     optional device int64 [rows, tokens] (tokens >= 0, 0: none): the cache
  *           slots of each row's last `tokens` tokens, as slot_mapping of
- *           mla_decode_epilogue; -1 for a token that this call did not add
+ *           mla_decode_epilogue; -1 for a token that this call did not add, and
+ *           for one in a page that others hold or that does not exist
  */
 int mla_pages_resize(int32_t* refs, int64_t num_pages, int32_t* block_table, int64_t bt_stride,
                      int32_t width, int32_t* seq_lens, const int32_t* new_lens, int32_t rows,
@@ -672,11 +679,11 @@ int mla_pages_resize(int32_t* refs, int64_t num_pages, int32_t* block_table, int
  * old one (-1: an empty row; other values outside [0, rows) count as -1 and set
  * MLA_DEVFLAG_BAD_ROW).  Beams, samples from one prompt, a batch put in another
  * order; rows that nobody goes on from are freed.  Children share their parent's
- * whole pages.  A partly filled last page stays with the lowest-numbered child;
- * each further child, in order, gets the lowest free page and a copy of its filled
- * slots in every layer (the other slots are left as they were).  A child that
- * finds no free page keeps the whole pages only, and its length is cut to them
- * (MLA_DEVFLAG_NO_PAGES).  The old table and lengths are left as they were; they
+ * whole pages.  A partly filled last page stays with the lowest-numbered child
+ * (also where other rows hold it, see mla_pages_resize); each further child, in
+ * order, gets the lowest free page and a copy of its filled slots in every layer
+ * (the other slots are left as they were).  A child that finds no free page keeps
+ * the whole pages only, and its length is cut to them (MLA_DEVFLAG_NO_PAGES).  The old table and lengths are left as they were; they
  * no longer count.
  *
  * parents    device int32 [out_rows]

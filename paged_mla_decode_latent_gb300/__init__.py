@@ -597,7 +597,8 @@ def _status_on(dev, status) -> bool:
 def pages_resize(refs, block_table, seq_lens, new_lens, page_size: int, workspace, slots=None, status=None,
                  stream=None) -> None:
     """``mla_pages_resize``: rows of the table get the lengths new_lens (0: freed); refs, block_table and seq_lens
-    are changed in place.  slots int64 [rows, tokens]: where each row's last tokens go, -1 for those not added."""
+    are changed in place.  slots int64 [rows, tokens]: where each row's last tokens go, -1 for those not added and those
+    in a page that other rows hold."""
     torch = _torch()
     dev, rows = _device(refs), block_table.shape[0]
     if not (dev >= 0 and _table_on(dev, block_table) and _ints_on(dev, refs, refs.shape[0])

@@ -246,6 +246,8 @@ __device__ __forceinline__ Grant granted(const Book& k, const Table& t, const in
 }
 
 // The rows' lengths, and the slots of tokens in pages that they had: CTA `id` of `n`.
+// Such a token lies in the row's last, partly filled page.  Where others hold that page
+// the place is theirs too (a row that was cut back into a shared page): no slot.
 __device__ void resize_rows(const Book& k, const Table& t, const int32_t* new_lens, int64_t* slots, int tokens,
                             int free_pages, int id, int n) {
   const int per = max(tokens, 1);
@@ -265,7 +267,8 @@ __device__ void resize_rows(const Book& k, const Table& t, const int32_t* new_le
     if (pos < g.old_len) {
       slots[i] = -1;
     } else if (pos / k.page_size < g.held) {
-      slots[i] = (int64_t)t.at[b * t.stride + pos / k.page_size] * k.page_size + pos % k.page_size;
+      const int page = t.at[b * t.stride + g.held - 1];
+      slots[i] = known(k, page) && k.refs[page] <= 1 ? (int64_t)page * k.page_size + pos % k.page_size : -1;
     }
   }
 }
