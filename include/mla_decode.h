@@ -391,16 +391,17 @@ int mla_gather_kv_b_proj(const void* kv_cache, int64_t num_pages, int32_t page_s
  * q_out        device bf16 [T, H, 576]: the q of mla_decode_fwd
  * kv_cache     device [num_pages, page_size, 576] bf16 or e4m3 codes, or 4-bit rows
  * kv_dtype     mla_kv_dtype of the cache; kv_scale device fp32[1] (fp8 and 4 bits)
- * cache_inputs_early  1: kv_c and k_pe are older than the kernel this call
- *              is queued behind, so they are read before the dependency
- *              wait (as slot_mapping and kv_scale always are); 0: after it
+ * cache_inputs_early  1: kv_c, k_pe and slot_mapping are older than the kernel
+ *              this call is queued behind, so they are read before the
+ *              dependency wait; 0: nothing is
  * status       optional device int32 status word (NULL = none): a slot
  *              >= num_pages * page_size is skipped and sets
  *              MLA_DEVFLAG_BAD_PAGE
  *
- * ql_nope and q_pe may be written by the kernel queued just before this one
- * (the dependency wait covers them); slot_mapping, kv_scale and, with
- * cache_inputs_early = 1, kv_c and k_pe must be older than that kernel.
+ * Any input may be written by the kernel queued just before this one (the
+ * dependency wait covers them; mla_pages_resize writes slot_mapping), but with
+ * cache_inputs_early = 1 kv_c, k_pe and slot_mapping must be older than that
+ * kernel.
  * Returns MLA_OK, MLA_ERR_INVALID_ARG or MLA_ERR_CUDA.
  */
 int mla_decode_epilogue(const void* ql_nope, const void* q_pe, const void* kv_c,

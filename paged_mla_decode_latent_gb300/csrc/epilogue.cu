@@ -6,9 +6,10 @@
 // Source: "[Perf][Kimi-K3] Cut MLA decode concat/cache epilogue latency"
 // (vLLM PR 54896), Purpose items 1-3.  Kept from it: one 8-element
 // load -> convert -> store per thread (16 bytes of bf16 in, 16 bytes of bf16
-// or 8 bytes of fp8 out); the inputs that are older than the producing GEMM
-// (slot_mapping, kv_scale and, when the caller says so, the cache-row inputs)
-// read before the programmatic dependency wait, the query inputs after it;
+// or 8 bytes of fp8 out); where the caller says that they are older than the
+// kernel before this one, slot_mapping and the cache-row inputs read before the
+// programmatic dependency wait, all else after it (only the wait makes what that
+// kernel wrote visible, and it may be the one that chose the slots);
 // the dependent launch triggered right after that wait so the decode's
 // prologue overlaps this kernel's last round trip.  Different from it: the
 // page's kernel splits a row over 3 warps up to 64 tokens and keeps one warp
@@ -68,17 +69,18 @@ __global__ void __launch_bounds__(kThreads) epilogue_kernel(EpiParams p) {
   const int h = (int)(row % rows_per_token);  // h == heads: the cache row
   const bool cache_row = active && h == p.heads;
 
-  // Older inputs first: the slot and, if the caller allows it, the cache row.
+  // Where the caller says that they are older than the kernel before this one: the slot and
+  // the cache row first.
   int64_t slot = -1;
   uint4 v = make_uint4(0, 0, 0, 0);
-  if (cache_row) {
+  auto load_row = [&] {
     slot = p.slot_mapping[t];
-    if (p.cache_early) {
-      v = piece < 64 ? reinterpret_cast<const uint4*>(p.kv_c + (int64_t)t * 512)[piece]
-                     : reinterpret_cast<const uint4*>(p.k_pe + (int64_t)t * 64)[piece - 64];
-    }
-  }
-  // ql_nope / q_pe may come from the kernel this one is launched behind.
+    v = piece < 64 ? reinterpret_cast<const uint4*>(p.kv_c + (int64_t)t * 512)[piece]
+                   : reinterpret_cast<const uint4*>(p.k_pe + (int64_t)t * 64)[piece - 64];
+  };
+  if (cache_row && p.cache_early) load_row();
+  // All else may come from the kernel this one is launched behind: the slots from the call
+  // that gave the tokens their pages, say.
   asm volatile("griddepcontrol.wait;" ::: "memory");
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (!active) return;
@@ -89,10 +91,7 @@ __global__ void __launch_bounds__(kThreads) epilogue_kernel(EpiParams p) {
     reinterpret_cast<uint4*>(p.q_out + qrow * MLA_D_QK)[piece] = x;
     return;
   }
-  if (!p.cache_early) {
-    v = piece < 64 ? reinterpret_cast<const uint4*>(p.kv_c + (int64_t)t * 512)[piece]
-                   : reinterpret_cast<const uint4*>(p.k_pe + (int64_t)t * 64)[piece - 64];
-  }
+  if (!p.cache_early) load_row();
   if (slot < 0) return;  // padding token: no insert
   if (slot >= p.num_slots) {
     if (piece == 0 && p.status) atomicOr(p.status, MLA_DEVFLAG_BAD_PAGE);

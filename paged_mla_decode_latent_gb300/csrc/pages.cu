@@ -14,8 +14,10 @@
 // the book is small a cluster of eight CTAs takes the steps in one launch, with the
 // cluster's barrier between them; else each step is a kernel, launched while the
 // one before it still runs and waiting for it (programmatic dependent launch).
-// A call's last kernel lets no other start before it is done: the decode kernels
-// read the lengths, which it may have written, before they wait.
+// What a call wrote is visible behind the dependency wait of the kernel after it, where
+// the inserts and the device planner read it; the decode kernels read the lengths before
+// they wait, but their calls queue a memset first, which no launch overlaps.  A call's last
+// kernel triggers no early start on top of that.
 // Moving rows is a kernel of its own, over the whole GPU, unless they are few.
 //
 // refs and the tables are small (4 bytes a page or entry), so resize is bound by
