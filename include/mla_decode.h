@@ -91,7 +91,9 @@ typedef enum mla_kv_dtype {
  * rope[r].  A scale with its sign bit set counts with its sign; a NaN scale
  * makes its 16 dims NaN.  A NaN or infinity in a row spoils every query row of
  * the sequence, also those whose causal mask hides that key; rows past a
- * sequence's length are never read.
+ * sequence's length are never read.  A query row beyond f16 sets
+ * MLA_DEVFLAG_Q_RANGE and comes out NaN, also where all of its scores are minus
+ * infinity: out = 0 with lse = -inf is a row without keys only.
  *
  * The inserts (mla_decode_epilogue, mla_decode_rope_epilogue, mla_decode_step)
  * write, for a block of 16 values x and with every quotient rounded to fp32,

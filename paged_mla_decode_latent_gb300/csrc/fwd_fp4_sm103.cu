@@ -472,6 +472,7 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
           const int tok = tid / p.heads;
           n = p.causal ? ctx - p.sq + tok + 1 : ctx;
           n = min(max(0, min(n, ctx)), k1);
+          if (n <= k0) n = 0;  // none of this unit's
         }
         vis[tid] = n;
       }
@@ -599,7 +600,8 @@ __global__ void __launch_bounds__(kThreads, 1) fwd_fp4_kernel(mla::FwdParams p) 
     }
     softmax_sync();
     if (tid < N) {
-      const float sum = xmax[tid] + xmax[N + tid] + xmax[2 * N + tid] + xmax[3 * N + tid];
+      float sum = xmax[tid] + xmax[N + tid] + xmax[2 * N + tid] + xmax[3 * N + tid];
+      if (sum == 0.f && vis[tid] > 0) sum = NAN;  // keys whose scores are all -inf, not a row without any
       inv[tid] = sum == 0.f ? 0.f : s_kv / sum;
       const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - m_mine) * 0.6931471805599453f;
       if (tid < n_rows) {

@@ -633,7 +633,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       return min(max(0, min(n, ctx)), k1);
     };
     if (st < N) {
-      st_shared_u32(at(kVisible, st), st < n_rows ? visible(st) : 0);
+      const int n = st < n_rows ? visible(st) : 0;
+      st_shared_u32(at(kVisible, st), n > k0 ? n : 0);  // 0: none of this unit's
       st_shared_f32(at(kMinusMax, st), -kMaxSentinel);
       st_shared_f32(at(kTop, st), kRescaleThreshold + kMaxSentinel);
     }
@@ -796,6 +797,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     ok = ok && wait_all(c, BAR(sum_full, 0), 0);
     if (st < N) {
       sum += ld_shared_f32(at(kPartnerSum, st));  // the same in both CTAs
+      // keys whose scores are all -inf, not a row without any
+      if (sum == 0.f && ld_shared_u32(at(kVisible, st)) != 0) sum = NAN;
       st_shared_f32(at(kFactor, st), sum == 0.f ? 0.f : s_kv / sum);
       if (ok && rank == 0 && st < n_rows) {
         const float lse = sum == 0.f ? -INFINITY : (log2f(sum) - ld_shared_f32(at(kMinusMax, st))) * 0.6931471805599453f;
