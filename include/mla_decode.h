@@ -691,8 +691,9 @@ int mla_pages_resize(int32_t* refs, int64_t num_pages, int32_t* block_table, int
  *
  * parents    device int32 [out_rows]
  * table_out  device int32 [out_rows, out_stride], out_stride >= width; lens_out
- *            device int32 [out_rows]; neither overlaps what it is made from.
- *            Entries past a row's pages may be written too.
+ *            device int32 [out_rows].  Neither overlaps, from its first entry to
+ *            its last, what it is made from, refs or the other.  Entries past a
+ *            row's pages may be written too.
  * kv_cache   device, 16-byte aligned: `layers` caches, layer_stride bytes apart, of
  *            num_pages * page_size rows of row_bytes bytes (1152 bf16, 576 fp8,
  *            MLA_FP4_ROW; any multiple of 16 up to 2^20)

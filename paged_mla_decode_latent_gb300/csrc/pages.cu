@@ -768,12 +768,18 @@ extern "C" int mla_pages_fork(int32_t* refs, int64_t num_pages, const int32_t* b
   if (st != MLA_OK) return st;
   if (rows < 1) return MLA_ERR_INVALID_ARG;
   if (out_rows > 0 && (parents == nullptr || table_out == nullptr || lens_out == nullptr || misaligned(parents, 4) ||
-                       misaligned(table_out, 4) || misaligned(lens_out, 4) || out_stride < width ||
-                       overlap(table_out, ((out_rows - 1) * out_stride + width) * 4, block_table,
-                               ((rows - 1) * bt_stride + width) * 4) ||
-                       overlap(lens_out, 4ll * out_rows, seq_lens, 4ll * rows) ||
-                       overlap(lens_out, 4ll * out_rows, parents, 4ll * out_rows)))
+                       misaligned(table_out, 4) || misaligned(lens_out, 4) || out_stride < width))
     return MLA_ERR_INVALID_ARG;
+  if (out_rows > 0) {  // what is written overlaps nothing else: parents are read again when rows are copied
+    const int64_t table_bytes = ((rows - 1) * bt_stride + width) * 4, out_bytes = ((out_rows - 1) * out_stride + width) * 4;
+    const int64_t lens_bytes = 4ll * out_rows;
+    if (overlap(table_out, out_bytes, block_table, table_bytes) || overlap(table_out, out_bytes, seq_lens, 4ll * rows) ||
+        overlap(table_out, out_bytes, parents, lens_bytes) || overlap(table_out, out_bytes, refs, 4 * num_pages) ||
+        overlap(table_out, out_bytes, lens_out, lens_bytes) || overlap(lens_out, lens_bytes, block_table, table_bytes) ||
+        overlap(lens_out, lens_bytes, seq_lens, 4ll * rows) || overlap(lens_out, lens_bytes, parents, lens_bytes) ||
+        overlap(lens_out, lens_bytes, refs, 4 * num_pages))
+      return MLA_ERR_INVALID_ARG;
+  }
   const Children c{parents, table_out, out_stride, lens_out, out_rows};
   const int slices = (int)ceil_div(width, kSlice);
   const int64_t segments = ceil_div(row_bytes * page_size, kSegment);
