@@ -712,7 +712,7 @@ int mla_pages_fork(int32_t* refs, int64_t num_pages, const int32_t* block_table,
  *
  * page_map  device int32 [num_pages]: a page's new number, -1 for one that was
  *           free; for tables other than this one
- * n_live    device int32 [1]: n
+ * n_live    device int32 [1]: n; neither overlaps the other or anything above
  * kv_cache, layers, layer_stride, row_bytes  as mla_pages_fork
  */
 int mla_pages_compact(int32_t* refs, int64_t num_pages, int32_t* block_table, int64_t bt_stride,

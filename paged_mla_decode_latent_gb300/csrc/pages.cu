@@ -811,6 +811,13 @@ extern "C" int mla_pages_compact(int32_t* refs, int64_t num_pages, int32_t* bloc
   if (st != MLA_OK) return st;
   if (page_map == nullptr || n_live == nullptr || misaligned(page_map, 4) || misaligned(n_live, 4))
     return MLA_ERR_INVALID_ARG;
+  // What is written overlaps nothing else: counts that change between two reads give ranks below zero.
+  const int64_t page_bytes = 4 * num_pages, table_bytes = rows > 0 ? ((rows - 1) * bt_stride + width) * 4 : 0;
+  if (overlap(page_map, page_bytes, refs, page_bytes) || overlap(n_live, 4, refs, page_bytes) ||
+      overlap(page_map, page_bytes, n_live, 4) || overlap(page_map, page_bytes, block_table, table_bytes) ||
+      overlap(n_live, 4, block_table, table_bytes) || overlap(page_map, page_bytes, seq_lens, 4ll * rows) ||
+      overlap(n_live, 4, seq_lens, 4ll * rows))
+    return MLA_ERR_INVALID_ARG;
   const int slices = rows == 0 ? 1 : (int)ceil_div(width, kSlice);
   const int64_t segments = ceil_div(row_bytes * page_size, kSegment);
   const int64_t pieces = std::max(num_pages / 2 * layers * segments, ceil_div((int64_t)rows * slices, kWarps));
