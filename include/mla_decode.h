@@ -256,18 +256,22 @@ int mla_decode_check(const mla_decode_plan_t* plan, const void* workspace, void*
  *   mla_decode_dplan_info      host: sizes from capacities only (no lengths)
  *   mla_decode_plan_device     device: the split-KV partition from the device
  *                              lengths, written into the workspace
- *   mla_decode_fwd_dplan       the decode over a grid of max_units CTA pairs,
- *                              each taking its unit from the list (slots past
- *                              the list's length exit at once)
+ *   mla_decode_fwd_dplan       the decode over a grid of max_units CTA pairs
+ *                              (4 bits, up to 32 rows: single CTAs), each
+ *                              taking its unit from the list (slots past the
+ *                              list's length exit at once)
  *   mla_decode_combine_dplan   the merge of the sequences that were cut
  *
  * Nothing queued depends on the lengths' values, so a CUDA graph of the last
  * three calls stays valid whatever the lengths become, up to ctx_capacity.
- * The partition: with P = num_sms / 2 pairs and K = the batch's 64-key tiles,
- * sequences are cut into chunks of max(ceil(ceil(K / P) / 2), 2) tiles unless
- * none is longer than 5/4 of the share ceil(K / P) (then none is cut); units
- * are listed chunk level by chunk level, sequences with more chunks first.
- * At most 2P + B chunks, so max_units = row_blocks * (2P + B).
+ * The partition: with P = num_sms / 2 and K = the batch's tiles (of key_tile
+ * keys, 256 for 4 bits and more than 32 rows), sequences are cut into chunks of
+ * max(ceil(ceil(K / P) / 2), 2) tiles unless none is longer than 5/4 of the share
+ * ceil(K / P) (then none is cut); units are listed chunk level by chunk level,
+ * sequences with more chunks first.  At most 2P + B chunks, so max_units =
+ * row_blocks * (2P + B).  P counts the CTA pairs that run at a time; of the
+ * single CTAs of a 4-bit cache up to 32 rows twice as many do, and sequences that
+ * this leaves whole run on half of the SMs (mla_decode_plan balances for all).
  *
  * Page tables: the padded block table of mla_decode_fwd (kv_indptr NULL), or
  * the CSR form: kv_indptr device int32 [B + 1], sequence b's page ids are
@@ -282,11 +286,12 @@ typedef struct mla_decode_dplan_t {
   int32_t row_blocks;     /* ceil(rows / 128) */
   int32_t ctx_capacity;   /* longest context any call may bring */
   int32_t num_sms;        /* SMs the partition is balanced for */
-  int32_t pairs;          /* P = num_sms / 2 (at most 127) */
+  int32_t pairs;          /* P = num_sms / 2 (at most 127), whatever a unit's CTAs */
   int32_t max_parts;      /* partial-slot capacity, 2P + B */
   int32_t max_units;      /* work-list capacity and launch size, row_blocks * (2P + B) */
-  int32_t min_chunk_keys; /* shortest chunk a cut sequence gets (2 key tiles) */
-  int32_t key_tile;       /* 64, or 128 for the few-row kernel (as mla_decode_plan_t) */
+  int32_t min_chunk_keys; /* shortest chunk a cut sequence gets: 2 tiles, 512 keys for 4
+                             bits and more than 32 rows, else 2 * key_tile */
+  int32_t key_tile;       /* 64, or 128 for the few-row kernels (as mla_decode_plan_t) */
   int32_t wait_limit_us;  /* as in mla_decode_plan_t: 0 = 2 s; the one field a caller may set */
   int32_t reserved0;
   int64_t ws_units_offset;  /* int32x4 [max_units] {b, row block | chunk << 8, k0, k1} */

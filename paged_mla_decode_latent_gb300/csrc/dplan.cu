@@ -225,7 +225,7 @@ extern "C" int mla_decode_dplan_info(int32_t batch, int32_t num_heads, int32_t s
   d.max_parts = 2 * d.pairs + batch;
   d.max_units = d.row_blocks * d.max_parts;
   d.key_tile = mla_small_rows_fit(d.rows, kv_dtype) ? mla::kKeyTileSmall : mla::kKeyTile;
-  d.min_chunk_keys = kMinChunkTiles * d.key_tile;
+  d.min_chunk_keys = kMinChunkTiles * mla::chunk_step(kv_dtype, d.key_tile);
   int64_t off = 0;
   d.ws_units_offset = off;
   off = align256(off + (int64_t)d.max_units * 16);
