@@ -98,9 +98,14 @@ typedef enum mla_kv_dtype {
  * The inserts (mla_decode_epilogue, mla_decode_rope_epilogue, mla_decode_step)
  * write, for a block of 16 values x and with every quotient rounded to fp32,
  *   q = x / kv_scale,  scale = e4m3(min(max |q| / 6, 448)),  code = e2m1(q / scale)
- * to nearest even, codes saturating at +-6; a block whose scale rounds to zero
- * gets zero codes, one that holds a NaN a NaN scale.  A rope dim is f16(x /
- * kv_scale), saturating at +-65504.
+ * to nearest even, codes saturating at +-6; a value that rounds to zero keeps its
+ * sign.  A block whose scale rounds to zero gets codes 0, one that holds a NaN codes
+ * 0 and a NaN scale.  A rope dim is f16(x / kv_scale), saturating at +-65504 without
+ * a flag: kv_scale covers the rope dims too (a latent maximum of 2688 kv_scale leaves
+ * them 24 times as much).
+ *
+ * The decode takes queries and softmax weights as f16 and sums in fp32: a query
+ * value below 2^-14 in size is off by up to 2^-25, a weight by 2^-11 of itself.
  *
  * Taken by mla_decode_plan and mla_decode_dplan_info and what follows them,
  * mla_decode_fwd_noalloc, mla_decode_step and both epilogues.  The shared-prefix
@@ -228,7 +233,8 @@ int mla_decode_fwd(const mla_decode_plan_t* plan, const void* q, const void* kv_
  * mla_decode_combine -- log-sum-exp merge of the split partials:
  *   L = ln sum_s exp(lse_s),  out = sum_s exp(lse_s - L) * o_s,  lse = L
  * over the splits of each row; splits with no keys (lse_s = -inf) carry no
- * weight, and a row with no keys at all gets out = 0, lse = -inf.
+ * weight, and a row with no keys at all gets out = 0, lse = -inf.  A split with
+ * lse_s = NaN makes its row NaN, whatever the others hold.
  *
  * Arguments as in mla_decode_fwd (same plan, seq_lens, workspace, out, lse,
  * stream).  A no-op returning MLA_OK when plan->num_splits == 1.
@@ -433,7 +439,8 @@ int mla_decode_epilogue(const void* ql_nope, const void* q_pe, const void* kv_c,
  * The rotation is fp32, rounded once to the type it is stored in.  slot < 0 (a
  * padding token) inserts nothing; its query rows are still written.  The slots
  * of one call are distinct (of two tokens with one slot, each 16-byte piece
- * keeps either).
+ * keeps either; a 4-bit row may then hold values of neither, as a block's codes and
+ * its scale are written apart).
  *
  * The inputs may be views of the projections they come from: strides are in
  * elements, >= 0 and multiples of 8, the last dimension contiguous, every base

@@ -40,9 +40,11 @@
 // 105 us, with one group of V warps (16 warps at 128) 117 and 100 us.  With waits
 // that poll in place of the suspended ones 109 (the MMA warps only) to 119 us (all).
 //
-// Everything is exact up to the weights: f16 holds a code times its scale, and Q
-// where it is within f16 (else MLA_DEVFLAG_Q_RANGE); scores and outputs are
-// summed in fp32, weights are rounded to f16.
+// f16 holds a code times its scale exactly, and a bf16 query value between 2^-17 and
+// 65504 in size.  Above (MLA_DEVFLAG_Q_RANGE) the row comes out NaN, below a value is off
+// by up to 2^-25, which a key of 2688 kv_scale turns into 2^-13 kv_scale of a score.
+// Scores and outputs are summed in fp32; weights are rounded to f16, 2^-11 of themselves
+// (the output's own bf16 is eight times as coarse), as the MMA takes them.
 //
 // Every wait is bounded (2 s unless the plan sets another limit).  A wait that
 // runs out sets MLA_DEVFLAG_TIMEOUT; the warps then run through their loops

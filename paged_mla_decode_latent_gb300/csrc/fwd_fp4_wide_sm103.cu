@@ -39,6 +39,8 @@
 // own 184, three units of V 163, fewer registers spilled 146, six query loads in flight
 // instead of nine (the last registers) 143.
 //
+// Precision is that of the kernel for fewer rows: queries and weights in f16.
+//
 // Every wait is bounded (2 s unless the plan sets another limit); one that runs out
 // sets MLA_DEVFLAG_TIMEOUT and the pair winds down.
 
