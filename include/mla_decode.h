@@ -698,8 +698,8 @@ int mla_pages_resize(int32_t* refs, int64_t num_pages, int32_t* block_table, int
  * (also where other rows hold it, see mla_pages_resize); each further child, in
  * order, gets the lowest free page and a copy of its filled slots in every layer
  * (the other slots are left as they were).  A child that finds no free page keeps
- * the whole pages only, and its length is cut to them (MLA_DEVFLAG_NO_PAGES).  The old table and lengths are left as they were; they
- * no longer count.
+ * the whole pages only, and its length is cut to them (MLA_DEVFLAG_NO_PAGES).
+ * The old table and lengths are left as they were; they no longer count.
  *
  * parents    device int32 [out_rows]
  * table_out  device int32 [out_rows, out_stride], out_stride >= width; lens_out
